@@ -55,7 +55,8 @@ enum {
     WQ4_ERR_TIMEOUT = -6,      /* a kernel's bounded pipeline wait ran out (see wq4_get_last_error) */
     WQ4_ERR_BOUNDS = -7        /* debug build only: a kernel's bounds check failed (wq4_last_violation) */
 };
-enum { WQ4_BF16 = 0, WQ4_FP16 = 1 };
+enum { WQ4_BF16 = 0, WQ4_FP16 = 1,
+       WQ4_FP32 = 2 };             /* only where a call says so (wq4_block_mm, wq4_token_logprobs) */
 enum { WQ4_U4B8 = 0, WQ4_U4_ZP = 1, WQ4_U4_FZP = 2 };
 
 /* Library version (major * 10000 + minor * 100 + patch) and a text for a status code. */
@@ -224,6 +225,76 @@ int wq4_grouped_mm_dev_ptrs(int P, const int* M, const int* N, const int* K,
                             const void* const* X_dev, const void* const* Wp_dev, void* const* Y_dev,
                             int group_size, int dtype, int qtype,
                             void* workspace, size_t workspace_bytes, wq4_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ *
+ * 8-bit rows: the projections of a model that stay in 8-bit float next to the 4-bit ones, what
+ * feeds them and what reads the last one's answer.
+ *
+ * Quantised rows [T][D] are e4m3 codes Q, row t at Q + t ldq (ldq bytes, a multiple of 16), and one
+ * fp32 scale per token and block of 128 columns, scales[b lds + t] (lds elements, a multiple of 4,
+ * >= T): the value of element (t, d) is Q[t][d] scales[d / 128][t]. A last block of fewer than 128
+ * columns has a scale of its own. Both pointers are 16-byte aligned. Padding (codes past D, scales
+ * past T) is neither read nor written.
+ *
+ * A block's scale is max(max |y| / 448, 2^-126) and its codes are y / scale rounded to nearest even
+ * (448 is the largest e4m3 value). A NaN becomes a NaN code and does not touch the scale; a block
+ * with an infinity gets an infinite scale, and all its values read back as NaN.
+ * ------------------------------------------------------------------------------------------ */
+
+/* RMS norm with the residual's addition, into quantised rows:
+ *     h = X + R        y = h / sqrt(mean(h^2) + eps) * weight        (fp32 throughout)
+ *   X       [T][D] dtype (WQ4_BF16 or WQ4_FP16), row stride ldx elements.
+ *   R       the residual, [T][D] dtype, row stride ldr; NULL: h = X.
+ *   weight  [D] dtype.
+ *   R_out   h rounded to dtype, the next layer's residual, row stride ldro, or NULL; needs R. May be X
+ *           or R itself (same stride). The norm goes by the unrounded h.
+ *   Y       y rounded to dtype (what wq4_mm reads), row stride ldy, or NULL. May be X or R itself (same
+ *           stride) where R_out is not.
+ *   Q, scales, ldq, lds   y as quantised rows, or both NULL; one of Y and Q at least is given.
+ * eps is finite and >= 0. D <= 32768, any D >= 1; rows whose sizes, strides and pointers are multiples
+ * of 16 bytes are read and written in 16-byte vectors. T == 0 is a no-op. */
+int wq4_add_rmsnorm_quant(const void* X, long long ldx, const void* R, long long ldr, const void* weight, int T, int D,
+                          float eps, int dtype, void* R_out, long long ldro, void* Y, long long ldy, void* Q,
+                          long long ldq, float* scales, long long lds, wq4_stream_t stream);
+
+/* Gated activation into quantised rows: y = silu(g) u with g = X[t][0..D), u = X[t][D..2D) and
+ * silu(g) = g / (1 + exp(-g)), in fp32.
+ *   X       [T][2 D] dtype (WQ4_BF16 or WQ4_FP16), row stride ldx elements.
+ *   Q, scales, ldq, lds   quantised rows of D columns.
+ * Any D >= 1 (up to 2^24). T == 0 is a no-op. */
+int wq4_silu_mul_quant(const void* X, long long ldx, int T, int D, int dtype, void* Q, long long ldq, float* scales,
+                       long long lds, wq4_stream_t stream);
+
+/* Product of quantised rows with an 8-bit weight that has one scale per 128 x 128 block:
+ *     Y[m][n] = sum over blocks b of x_scales[b][m] w_scales[n / 128][b] sum over k in b of X[m][k] W[n][k]
+ * with fp32 accumulation, rounded once.
+ *   X, x_scales   quantised rows [M][K] (ldx bytes, ldsx elements).
+ *   W         [N][K] e4m3, row stride ldw bytes (a multiple of 16), 16-byte aligned: read as it is, there
+ *             is nothing to prepack.
+ *   w_scales  [ceil(N / 128)][ceil(K / 128)] fp32, row stride ldsw elements.
+ *   Y         [M][N] dtype (WQ4_BF16, WQ4_FP16 or WQ4_FP32), row stride ldy elements.
+ * Any M >= 0 and N >= 1; K a multiple of 16 (WQ4_ERR_UNSUPPORTED otherwise). Needs no workspace.
+ * Results are identical from run to run (fixed reduction order). M == 0 is a no-op. */
+int wq4_block_mm(const void* X, long long ldx, const float* x_scales, long long ldsx, const void* W, long long ldw,
+                 const float* w_scales, long long ldsw, void* Y, long long ldy, int M, int N, int K, int dtype,
+                 wq4_stream_t stream);
+
+/* Log probabilities of given tokens, the entropy of each row's distribution and its most likely tokens,
+ * from logits x (log p = x - log sum exp x), in fp32:
+ *   logits        [T][V] dtype (WQ4_BF16, WQ4_FP16 or WQ4_FP32), row stride ld elements.
+ *   tokens        [T] the token of each row whose log probability is asked for; one outside [0, V) gives
+ *                 NaN. NULL, with logprobs, when there is none to ask for.
+ *   logprobs      [T] log p of tokens[t], or NULL with tokens.
+ *   entropy       [T] -sum p log p in nats, or NULL.
+ *   top_ids, top_logprobs   [T][top_k] the top_k most likely tokens in order, the lower index first among
+ *                 equal logits; both NULL with top_k == 0. top_k <= 32 and <= V.
+ * Logits of -inf are tokens that cannot occur: log probability -inf, no part in the entropy, never listed;
+ * a row with fewer than top_k others is filled up with id -1 and log probability -inf. A row of nothing
+ * but -inf has log probabilities -inf and entropy 0. In a row that holds a NaN or +inf every log
+ * probability and the entropy are NaN (ids still rank the values that are not NaN).
+ * V <= 2^30. T == 0 is a no-op. */
+int wq4_token_logprobs(const void* logits, long long ld, const long long* tokens, int T, int V, int dtype, int top_k,
+                       float* logprobs, float* entropy, int* top_ids, float* top_logprobs, wq4_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ *
  * Errors and options.

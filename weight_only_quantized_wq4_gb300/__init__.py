@@ -72,6 +72,11 @@ def load_library(path: str = LIB_PATH):
         "wq4_grouped_mm_device_m": (c_int, [c_int, vp, ip, ip, ip, vpp, vpp, vpp, c_int, c_int, c_int, vp, c_size, vp]),
         "wq4_grouped_dev_ptrs_workspace_bytes": (c_int, [c_int, ip, ip, ip, c_int, ctypes.POINTER(c_size)]),
         "wq4_grouped_mm_dev_ptrs": (c_int, [c_int, ip, ip, ip, vp, vp, vp, c_int, c_int, c_int, vp, c_size, vp]),
+        "wq4_add_rmsnorm_quant": (c_int, [vp, ll, vp, ll, vp, c_int, c_int, ctypes.c_float, c_int, vp, ll, vp, ll, vp,
+                                          ll, vp, ll, vp]),
+        "wq4_silu_mul_quant": (c_int, [vp, ll, c_int, c_int, c_int, vp, ll, vp, ll, vp]),
+        "wq4_block_mm": (c_int, [vp, ll, vp, ll, vp, ll, vp, ll, vp, ll, c_int, c_int, c_int, c_int, vp]),
+        "wq4_token_logprobs": (c_int, [vp, ll, vp, c_int, c_int, c_int, c_int, vp, vp, vp, vp, vp]),
         "wq4_get_last_error": (c_int, [vp]),
         "wq4_debug_checks": (c_int, []),
         "wq4_last_violation": (c_int, [ip]),
@@ -357,3 +362,170 @@ def grouped_mm_dev_ptrs(M: Sequence[int], N: Sequence[int], K: Sequence[int], X_
                                        _cuda(Y_ptrs, "Y_ptrs"), group_size, DTYPES[dtype], QTYPES[qtype],
                                        _cuda(workspace, "workspace"), workspace.numel(), _stream(dev)),
            "wq4_grouped_mm_dev_ptrs")
+
+
+# ------------------------------------------------------------------------------------ 8-bit rows
+def _rows(t, name: str, dtypes, like=None):
+    """Pointer and row stride (in elements) of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError("%s must be a 2-D tensor of %s" % (name, " or ".join(str(d)[6:] for d in dtypes)))
+    if not t.is_cuda or (like is not None and t.device != like.device):
+        raise ValueError("%s must be a CUDA tensor%s" % (name, "" if like is None else " on the device of the others"))
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
+    if rows > 1:
+        return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), (cols + 15) // 16 * 16       # (the stride of a single row is never used)
+
+
+def _vector(t, name: str, n: int, dtypes, like):
+    """Pointer of a contiguous 1-D CUDA tensor of n elements."""
+    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes:
+        raise ValueError("%s must be a 1-D tensor of %d elements of %s" %
+                         (name, n, " or ".join(str(d)[6:] for d in dtypes)))
+    if t.device != like.device or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be contiguous, on the device of the others" % name)
+    return t.data_ptr()
+
+
+def _shaped(t, name: str, rows: int, cols: int):
+    if t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s must be [%d][%d]" % (name, rows, cols))
+
+
+def alloc_quant_rows(T: int, D: int, device="cuda"):
+    """Buffers for T quantised rows of D columns: (q float8_e4m3fn [T][D], scales float32
+    [ceil(D/128)][T]), views of rows padded to 16 bytes."""
+    torch = _torch()
+    q = torch.empty((T, (D + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=device)
+    scales = torch.empty(((D + GROUP - 1) // GROUP, (T + 3) // 4 * 4), dtype=torch.float32, device=device)
+    return q[:, :D], scales[:, :T]
+
+
+def _quant_rows(q, scales, T: int, D: int, like):
+    """(q pointer, ldq, scales pointer, lds) of quantised rows."""
+    torch = _torch()
+    qp, ldq = _rows(q, "q", (torch.float8_e4m3fn,), like)
+    sp, lds = _rows(scales, "scales", (torch.float32,), like)
+    _shaped(q, "q", T, D)
+    _shaped(scales, "scales", (D + GROUP - 1) // GROUP, T)
+    return qp, ldq, sp, lds
+
+
+def add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, q=None, scales=None, residual_out=None, y=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, quantised by rows (wq4_add_rmsnorm_quant).
+
+    x: bf16/fp16 [T][D]. Returns (q, scales, residual_out): y as e4m3 codes [T][D] with fp32 scales
+    [ceil(D/128)][T], and h in x's type (None without a residual). Buffers that are not given are
+    allocated (alloc_quant_rows); residual_out may be x or residual itself. y: also write the
+    16-bit y there (what mm reads)."""
+    torch = _torch()
+    lib = load_library()
+    half = (x.dtype,)
+    code = _dtype_code(x)
+    xp, ldx = _rows(x, "x", half)
+    T, D = x.shape
+    wp = _vector(weight, "weight", D, half, x)
+    rp = ldr = rop = ldro = yp = ldy = 0
+    if residual is not None:
+        rp, ldr = _rows(residual, "residual", half, x)
+        _shaped(residual, "residual", T, D)
+        if residual_out is None:
+            residual_out = torch.empty((T, D), dtype=x.dtype, device=x.device)
+    if residual_out is not None:
+        rop, ldro = _rows(residual_out, "residual_out", half, x)
+        _shaped(residual_out, "residual_out", T, D)
+    if y is not None:
+        yp, ldy = _rows(y, "y", half, x)
+        _shaped(y, "y", T, D)
+    if q is None and scales is None:
+        q, scales = alloc_quant_rows(T, D, x.device)
+    qp, ldq, sp, lds = _quant_rows(q, scales, T, D, x)
+    _check(lib.wq4_add_rmsnorm_quant(xp, ldx, rp or None, ldr, wp, T, D, eps, code, rop or None, ldro, yp or None, ldy,
+                                     qp, ldq, sp, lds, _stream(x.device)), "wq4_add_rmsnorm_quant")
+    return q, scales, residual_out
+
+
+def silu_mul_quant(x, q=None, scales=None):
+    """y = silu(x[:, :D]) * x[:, D:] for x bf16/fp16 [T][2 D], quantised by rows (wq4_silu_mul_quant):
+    returns (q, scales) as add_rmsnorm_quant does."""
+    lib = load_library()
+    code = _dtype_code(x)
+    xp, ldx = _rows(x, "x", (x.dtype,))
+    T, D = x.shape[0], x.shape[1] // 2
+    if x.shape[1] % 2:
+        raise ValueError("x must hold a gate and an up half")
+    if q is None and scales is None:
+        q, scales = alloc_quant_rows(T, D, x.device)
+    qp, ldq, sp, lds = _quant_rows(q, scales, T, D, x)
+    _check(lib.wq4_silu_mul_quant(xp, ldx, T, D, code, qp, ldq, sp, lds, _stream(x.device)), "wq4_silu_mul_quant")
+    return q, scales
+
+
+def _out_types():
+    torch = _torch()
+    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def block_mm(q, scales, W, W_scales, out=None, dtype=None):
+    """Y[M,N] = X . W^T of quantised rows (q, scales) [M][K] with an e4m3 weight W [N][K] and its fp32 scales
+    [ceil(N/128)][ceil(K/128)] (wq4_block_mm). Y is bf16, fp16 or fp32: out's type, or dtype (a
+    torch type, bfloat16 by default)."""
+    torch = _torch()
+    lib = load_library()
+    M, K = q.shape
+    qp, ldq, sp, lds = _quant_rows(q, scales, M, K, q)
+    wp, ldw = _rows(W, "W", (torch.float8_e4m3fn,), q)
+    N = W.shape[0]
+    _shaped(W, "W", N, K)
+    wsp, ldws = _rows(W_scales, "W_scales", (torch.float32,), q)
+    _shaped(W_scales, "W_scales", (N + GROUP - 1) // GROUP, (K + GROUP - 1) // GROUP)
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=q.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError("out is not of the dtype asked for")
+    types = _out_types()
+    yp, ldy = _rows(out, "out", tuple(types), q)
+    _shaped(out, "out", M, N)
+    _check(lib.wq4_block_mm(qp, ldq, sp, lds, wp, ldw, wsp, ldws, yp, ldy, M, N, K, types[out.dtype],
+                            _stream(q.device)), "wq4_block_mm")
+    return out
+
+
+def token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None):
+    """Log probabilities of tokens (int64 [T], or None) under logits [T][V] (bf16, fp16 or fp32), each row's entropy
+    and its top_k most likely tokens (wq4_token_logprobs). Returns (logprobs [T] or None, entropy [T], top_ids
+    int32 [T][top_k], top_logprobs [T][top_k]); the last two are None with top_k = 0. Buffers that are
+    not given are allocated."""
+    torch = _torch()
+    lib = load_library()
+    types = _out_types()
+    lp, ld = _rows(logits, "logits", tuple(types))
+    T, V = logits.shape
+    dev, f32 = logits.device, (torch.float32,)
+    tp = lpp = tip = tlp = 0
+    if tokens is not None:
+        tp = _vector(tokens, "tokens", T, (torch.int64,), logits)
+        if logprobs is None:
+            logprobs = torch.empty(T, dtype=torch.float32, device=dev)
+        lpp = _vector(logprobs, "logprobs", T, f32, logits)
+    elif logprobs is not None:
+        raise ValueError("logprobs needs tokens")
+    if entropy is None:
+        entropy = torch.empty(T, dtype=torch.float32, device=dev)
+    ep = _vector(entropy, "entropy", T, f32, logits)
+    if top_k > 0:
+        if top_ids is None:
+            top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        if top_logprobs is None:
+            top_logprobs = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        for t, name, dt in ((top_ids, "top_ids", torch.int32), (top_logprobs, "top_logprobs", torch.float32)):
+            if t.shape != (T, top_k) or t.dtype != dt or t.device != dev or not t.is_contiguous():
+                raise ValueError("%s must be a contiguous %s tensor [%d][%d]" % (name, str(dt)[6:], T, top_k))
+        tip, tlp = top_ids.data_ptr(), top_logprobs.data_ptr()
+    elif top_ids is not None or top_logprobs is not None:
+        raise ValueError("top_ids and top_logprobs need top_k")
+    _check(lib.wq4_token_logprobs(lp, ld, tp or None, T, V, types[logits.dtype], top_k, lpp or None, ep, tip or None,
+                                  tlp or None, _stream(dev)), "wq4_token_logprobs")
+    return logprobs, entropy, top_ids, top_logprobs

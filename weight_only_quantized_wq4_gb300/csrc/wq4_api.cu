@@ -33,6 +33,7 @@
 #include "wq4_device.cuh"
 #include "wq4_launch.h"
 #include "wq4_params.h"
+#include "wq4_runtime.h"
 
 namespace wq4 {
 namespace {
@@ -348,10 +349,6 @@ int make_plan(const Shape* shapes, int P, int sm_count, size_t ws_cap, int group
 }
 
 // ---------------------------------------------------------------------------- tensor maps
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
@@ -667,6 +664,22 @@ int static_scratch(uint8_t** out) {
 }
 
 }  // namespace
+
+// See wq4_runtime.h.
+int runtime(Runtime* out) {
+    DeviceInfo* dev = nullptr;
+    const int rc = device_info(&dev);
+    if (rc) return rc;
+    out->sm_count = dev->sm_count;
+    out->status = dev->status;
+    out->timeout_cycles = timeout_cycles();
+    out->test_stall = g_opt.test_stall;
+    out->pdl = g_opt.pdl == 0;
+    out->trace = trace_on();
+    out->encode = encode_fn();
+    return out->encode ? WQ4_OK : WQ4_ERR_CUDA;
+}
+
 }  // namespace wq4
 
 using namespace wq4;

@@ -1,0 +1,431 @@
+// Log probabilities of given tokens, the entropy of each row and its most likely tokens, in one pass
+// over the logits.
+//
+// For a row x of V logits, with m = max x, d_i = x_i - m, z = sum exp(d_i), s = sum d_i exp(d_i):
+//     log p_i = d_i - log z            H = -sum p_i log p_i = log z - s / z
+// The pass keeps (m, z, s) of what a thread has seen, in fp32; when its m grows by D, z and s become
+// exp(-D) z and exp(-D) (s - D z), and parts are joined by the same rule. d is bounded below by
+// -kFar, where exp is 0, so that a logit of -inf (or of the type's lowest value) adds 0 and not
+// 0 * inf; a NaN passes the bound and makes the row NaN.
+//
+// The k most likely tokens need no second pass over the row. A thread remembers the largest vector
+// it saw (its maximum and where, the first among equals). 64 groups of 8 threads make 64 such
+// bests; the k-th largest of them, tau, is a bound that at least k elements reach, so only threads
+// whose own best reaches it can hold an answer, about k of 512. Their vectors (V / 512 elements each)
+// are read again by whole warps, which keep the best k in order, one per lane; the warps' lists, a
+// few dozen entries, are ranked by counting. An element's order is one 64-bit key: the float
+// as an unsigned integer of the same order, then the complement of its index, so that equal logits
+// rank by the lower index and no two keys are equal.
+//
+// Bound by memory for many rows (each logit read once). For few rows a cluster of CTAs shares a row
+// and joins its parts through distributed shared memory.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "wq4_device.cuh"
+#include "wq4_runtime.h"
+
+namespace wq4 {
+namespace {
+
+constexpr int kLpThreads = 512;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpGroups = 64;                 // bests that bound the k-th largest
+constexpr int kLpMaxTop = 32;
+constexpr int kLpMaxCluster = 8;
+constexpr int kLpUnroll = 4;                  // vectors of a thread in flight
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFar = 150.f;                 // exp(-150) is below the smallest fp32
+constexpr float kNegInf = -INFINITY;
+
+enum : int { kLpBf16 = 0, kLpFp16 = 1, kLpFp32 = 2 };   // the header's dtype codes
+
+struct LpArgs {
+    const void* logits;
+    const long long* tokens;                  // null where not asked for, like the outputs
+    float *logprobs, *entropy, *top_logprobs;
+    int* top_ids;
+    long long ld;
+    int V, k, cluster;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// One 16-byte vector of logits: kN of them, the maximum that passes NaN over, and element j as fp32.
+template <int DT>
+struct LpVec {
+    static constexpr int kN = DT == kLpFp32 ? 4 : 8;
+    static constexpr int kSize = 16 / kN;
+    __device__ static float at(const uint4& v, int j) {
+        const uint32_t w = DT == kLpFp32 ? (j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w)
+                                         : (j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w);
+        if constexpr (DT == kLpFp32) return __uint_as_float(w);
+        else if constexpr (DT == kLpBf16) return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+        else return __half2float(__ushort_as_half(static_cast<uint16_t>(j & 1 ? w >> 16 : w & 0xffffu)));
+    }
+    __device__ static float max(const uint4& v) {
+        if constexpr (DT == kLpFp32) {
+            return fmaxf(fmaxf(at(v, 0), at(v, 1)), fmaxf(at(v, 2), at(v, 3)));
+        } else {
+            uint32_t a, b, c;
+            if constexpr (DT == kLpBf16) {
+                asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+                asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+                asm("max.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+            } else {
+                asm("max.f16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+                asm("max.f16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+                asm("max.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+            }
+            const uint4 p = make_uint4(c, 0, 0, 0);
+            return fmaxf(at(p, 0), at(p, 1));
+        }
+    }
+    // all elements -inf
+    __device__ static uint4 none() {
+        const uint32_t w = DT == kLpFp32 ? 0xff800000u : DT == kLpBf16 ? 0xff80ff80u : 0xfc00fc00u;
+        return make_uint4(w, w, w, w);
+    }
+};
+
+// The order of the floats as unsigned integers (+0 and -0 alike; x is not NaN), and back.
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ unsigned long long key_of(float x, int index) {
+    return (static_cast<unsigned long long>(order_of(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(index));
+}
+
+// A row cut into 16-byte vectors on 16-byte boundaries: vector v holds elements v kN - head + j; the
+// first and the last may be partly outside the row, and what is outside is not read.
+template <int DT>
+struct LpRow {
+    const char* base;       // vector 0 (its address may lie before the row's first element)
+    int head, V, nv;
+    __device__ LpRow(const void* logits, long long ld, long long t, int V_) : V(V_) {
+        const char* p = static_cast<const char*>(logits) + t * ld * LpVec<DT>::kSize;
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+        head = off / LpVec<DT>::kSize;
+        base = p - off;
+        nv = (V + head + LpVec<DT>::kN - 1) / LpVec<DT>::kN;
+    }
+    __device__ bool whole(int v) const { return v * LpVec<DT>::kN >= head && (v + 1) * LpVec<DT>::kN <= V + head; }
+    __device__ uint4 load(int v) const { return __ldg(reinterpret_cast<const uint4*>(base) + v); }
+    __device__ uint4 load_edge(int v) const {
+        if (whole(v)) return load(v);
+        uint4 r = LpVec<DT>::none();
+        uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < LpVec<DT>::kN; ++j) {
+            const int i = v * LpVec<DT>::kN - head + j;
+            if (i < 0 || i >= V) continue;
+            if constexpr (DT == kLpFp32) {
+                w[j] = reinterpret_cast<const uint32_t*>(base)[v * 4 + j];
+            } else {
+                const uint32_t b = reinterpret_cast<const uint16_t*>(base)[v * 8 + j];
+                w[j >> 1] = j & 1 ? (w[j >> 1] & 0xffffu) | (b << 16) : (w[j >> 1] & 0xffff0000u) | b;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Softmax statistics of a set of logits; m = -inf: nothing but -inf (and NaN) so far.
+struct LpStat {
+    float m, z, s;
+    // to a reference n >= m
+    __device__ void move(float n) {
+        if (n > m) {
+            const float d = m == kNegInf ? -kFar : fmaxf(m - n, -kFar);
+            const float f = ex2(d * kLog2e);
+            s = f * fmaf(d, z, s);
+            z = f * z;
+            m = n;
+        }
+    }
+    __device__ void join(float m2, float z2, float s2) {
+        LpStat o{m2, z2, s2};
+        const float n = fmaxf(m, m2);
+        move(n);
+        o.move(n);
+        z += o.z;
+        s += o.s;
+    }
+    template <int DT>
+    __device__ void add(const uint4& v) {            // (m already covers v)
+        const float ref = m == kNegInf ? 0.f : m;
+#pragma unroll
+        for (int j = 0; j < LpVec<DT>::kN; ++j) {
+            const float d = max_nan(LpVec<DT>::at(v, j) - ref, -kFar);
+            const float e = ex2(d * kLog2e);
+            z += e;
+            s = fmaf(d, e, s);
+        }
+    }
+};
+
+struct LpShared {
+    LpStat stat[kLpWarps];
+    LpStat total;
+    unsigned long long best[kLpGroups];
+    unsigned long long tau;
+    int n;
+    unsigned long long cand[kLpWarps * kLpMaxTop];
+    unsigned long long top[kLpMaxTop];               // this CTA's best, in order, 0 where there are fewer
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a) {
+    using Vec = LpVec<DT>;
+    __shared__ LpShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const long long t = blockIdx.x / C;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const LpRow<DT> row(a.logits, a.ld, t, a.V);
+    const int v0 = static_cast<int>(static_cast<long long>(row.nv) * rank / C);
+    const int v1 = static_cast<int>(static_cast<long long>(row.nv) * (rank + 1) / C);
+
+    LpStat st{kNegInf, 0.f, 0.f};
+    int bv = -1;                                     // the vector of this thread's maximum, st.m
+    int v = v0 + tid;
+    // the vectors between the row's first and last, which may be partial
+    if (v == 0 && v < v1) {
+        const uint4 x = row.load_edge(0);
+        const float n = Vec::max(x);
+        if (n > st.m) bv = 0;
+        st.move(n);
+        st.add<DT>(x);
+        v += kLpThreads;
+    }
+    const int last = min(v1, row.nv - 1);
+    for (; v + (kLpUnroll - 1) * kLpThreads < last; v += kLpUnroll * kLpThreads) {
+        uint4 x[kLpUnroll];
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) x[u] = row.load(v + u * kLpThreads);
+        float n = st.m;
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            const float vm = Vec::max(x[u]);
+            if (vm > n) {
+                n = vm;
+                bv = v + u * kLpThreads;
+            }
+        }
+        st.move(n);
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) st.add<DT>(x[u]);
+    }
+    for (; v < v1; v += kLpThreads) {
+        const uint4 x = row.load_edge(v);
+        const float n = Vec::max(x);
+        if (n > st.m) bv = v;
+        st.move(n);
+        st.add<DT>(x);
+    }
+    // this thread's best as a bound for elements: its value and its vector's last index
+    unsigned long long best = bv < 0 ? 0ull : key_of(st.m, min(bv * Vec::kN + Vec::kN - 1 - row.head, a.V - 1));
+
+    // ---- the CTA's statistics
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, st.m, d), z2 = __shfl_xor_sync(0xffffffffu, st.z, d),
+                    s2 = __shfl_xor_sync(0xffffffffu, st.s, d);
+        st.join(m2, z2, s2);
+    }
+    if (lane == 0) sh.stat[warp] = st;
+    if (tid == 0) {
+        sh.tau = 0;
+        sh.n = 0;
+    }
+    if (tid < kLpMaxTop) sh.top[tid] = 0;
+    if (a.k > 0) {
+        unsigned long long g = best;
+#pragma unroll
+        for (int d = 1; d < kLpThreads / kLpGroups; d <<= 1) {
+            const unsigned long long o = __shfl_xor_sync(0xffffffffu, g, d);
+            g = o > g ? o : g;
+        }
+        if (tid % (kLpThreads / kLpGroups) == 0) sh.best[tid / (kLpThreads / kLpGroups)] = g;
+    }
+    __syncthreads();
+    if (warp == kLpWarps - 1) {
+        LpStat w = sh.stat[lane % kLpWarps];
+#pragma unroll
+        for (int d = kLpWarps / 2; d; d >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, w.m, d), z2 = __shfl_xor_sync(0xffffffffu, w.z, d),
+                        s2 = __shfl_xor_sync(0xffffffffu, w.s, d);
+            w.join(m2, z2, s2);
+        }
+        if (lane == 0) sh.total = w;
+    }
+
+    // ---- the CTA's k best
+    if (a.k > 0) {
+        if (tid < kLpGroups) {
+            const unsigned long long mine = sh.best[tid];
+            int above = 0;
+            for (int i = 0; i < kLpGroups; ++i) above += sh.best[i] > mine ? 1 : 0;
+            if (mine && above == a.k - 1) sh.tau = mine;
+        }
+        __syncthreads();
+        const unsigned long long tau = sh.tau;
+        unsigned long long list = 0;                 // lane i: the warp's i-th best so far
+        unsigned long long floor = tau ? tau - 1 : 0;   // what an element has to be above
+        unsigned int todo = __ballot_sync(0xffffffffu, best != 0 && best >= tau);
+        while (todo) {
+            const int from = __ffs(todo) - 1;
+            todo &= todo - 1;
+            for (int w0 = v0 + warp * 32 + from; w0 < v1; w0 += 32 * kLpThreads) {
+                const int w = w0 + lane * kLpThreads;
+                const uint4 x = w < v1 ? row.load_edge(w) : Vec::none();
+#pragma unroll
+                for (int j = 0; j < Vec::kN; ++j) {
+                    const float f = Vec::at(x, j);
+                    const unsigned long long key = f > kNegInf ? key_of(f, w * Vec::kN - row.head + j) : 0ull;
+                    unsigned int in = __ballot_sync(0xffffffffu, key > floor);
+                    while (in) {
+                        const unsigned long long c = __shfl_sync(0xffffffffu, key, __ffs(in) - 1);
+                        in &= in - 1;
+                        if (c <= floor) continue;
+                        const int at = __popc(__ballot_sync(0xffffffffu, list > c));
+                        const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
+                        if (lane == at) list = c;
+                        else if (lane > at) list = up;
+                        const unsigned long long kth = __shfl_sync(0xffffffffu, list, a.k - 1);
+                        if (kth > floor) floor = kth;
+                    }
+                }
+            }
+        }
+        const int have = min(__popc(__ballot_sync(0xffffffffu, list != 0)), a.k);
+        if (have) {
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&sh.n, have);
+            at = __shfl_sync(0xffffffffu, at, 0);
+            if (lane < have) sh.cand[at + lane] = list;
+        }
+        __syncthreads();
+        const int n = sh.n;
+        if (tid < n) {
+            const unsigned long long mine = sh.cand[tid];
+            int above = 0;
+            for (int i = 0; i < n; ++i) above += sh.cand[i] > mine ? 1 : 0;
+            if (above < a.k) sh.top[above] = mine;
+        }
+    }
+    __syncthreads();
+
+    // ---- the row's, from its CTAs'
+    if (C > 1) {
+        cluster_sync();
+        if (rank == 0) {
+            if (tid < 32) {
+                LpStat w{kNegInf, 0.f, 0.f};
+                if (lane < C) {
+                    const uint32_t p = map_to_rank(smem_u32(&sh.total), lane);
+                    w = LpStat{ld_cluster_f32(p), ld_cluster_f32(p + 4), ld_cluster_f32(p + 8)};
+                }
+#pragma unroll
+                for (int d = kLpMaxCluster / 2; d; d >>= 1) {
+                    const float m2 = __shfl_xor_sync(0xffffffffu, w.m, d), z2 = __shfl_xor_sync(0xffffffffu, w.z, d),
+                                s2 = __shfl_xor_sync(0xffffffffu, w.s, d);
+                    w.join(m2, z2, s2);
+                }
+                __syncwarp();
+                if (lane == 0) sh.stat[0] = w;
+            }
+            for (int i = tid; i < C * kLpMaxTop; i += kLpThreads) {
+                const uint32_t p = map_to_rank(smem_u32(&sh.top[i % kLpMaxTop]), i / kLpMaxTop);
+                unsigned long long key;
+                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(p) : "memory");
+                sh.cand[i] = key;
+            }
+        }
+        cluster_sync();                              // every part is read: the other CTAs may leave
+        if (rank != 0) return;
+        if (tid < kLpMaxTop) sh.top[tid] = 0;
+        __syncthreads();
+        for (int i = tid; i < C * kLpMaxTop; i += kLpThreads) {
+            const unsigned long long mine = sh.cand[i];
+            int above = 0;
+            for (int q = 0; q < C * kLpMaxTop; ++q) above += sh.cand[q] > mine ? 1 : 0;
+            if (mine && above < a.k) sh.top[above] = mine;
+        }
+        if (tid == 0) sh.total = sh.stat[0];
+        __syncthreads();
+    }
+
+    const LpStat all = sh.total;
+    const float logz = all.m == kNegInf ? 0.f : logf(all.z);   // z is NaN where the row holds a NaN
+    const bool nothing = all.m == kNegInf && all.z == 0.f;
+    auto logp = [&](float x) { return nothing ? kNegInf : (x == kNegInf ? x + 0.f * all.z : x - all.m) - logz; };
+    if (tid < a.k) {
+        const unsigned long long key = sh.top[tid];
+        a.top_ids[t * a.k + tid] = key ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
+        a.top_logprobs[t * a.k + tid] = logp(key ? value_of(static_cast<uint32_t>(key >> 32)) : kNegInf);
+    }
+    if (tid == 32 && a.entropy) a.entropy[t] = nothing ? 0.f : logz - all.s / all.z;
+    if (tid == 64 && a.logprobs) {
+        const long long id = a.tokens[t];
+        float r = NAN;
+        if (id >= 0 && id < a.V) {
+            const char* p = static_cast<const char*>(a.logits) + (t * a.ld + id) * Vec::kSize;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            x.x = DT == kLpFp32 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
+            r = logp(Vec::at(x, 0));
+        }
+        a.logprobs[t] = r;
+    }
+}
+
+}  // namespace
+}  // namespace wq4
+
+using namespace wq4;
+
+extern "C" int wq4_token_logprobs(const void* logits, long long ld, const long long* tokens, int T, int V, int dtype,
+                                  int top_k, float* logprobs, float* entropy, int* top_ids, float* top_logprobs,
+                                  wq4_stream_t stream) {
+    if (T < 0 || V < 1 || top_k < 0 || top_k > V) return WQ4_ERR_INVALID;
+    if (dtype != WQ4_BF16 && dtype != WQ4_FP16 && dtype != WQ4_FP32) return WQ4_ERR_INVALID;
+    if (top_k > kLpMaxTop || V > (1 << 30)) return WQ4_ERR_UNSUPPORTED;
+    if (T == 0) return WQ4_OK;
+    if (!logits || ld < V || !tokens != !logprobs) return WQ4_ERR_INVALID;
+    if ((top_k > 0) != (top_ids != nullptr) || (top_k > 0) != (top_logprobs != nullptr)) return WQ4_ERR_INVALID;
+    if (!logprobs && !entropy && top_k == 0) return WQ4_ERR_INVALID;
+    if (!aligned_to(logits, dtype == WQ4_FP32 ? 4 : 2) || !aligned_to(tokens, 8) || !aligned_to(logprobs, 4) ||
+        !aligned_to(entropy, 4) || !aligned_to(top_ids, 4) || !aligned_to(top_logprobs, 4))
+        return WQ4_ERR_ALIGN;
+    Runtime rt;
+    if (const int rc = runtime(&rt)) return rc;
+    // Few rows: a cluster per row, as long as the CTAs still fit the GPU twice over and a CTA's share
+    // is a batch of loads for every thread.
+    int C = 1;
+    const int vec = dtype == WQ4_FP32 ? 4 : 8;
+    while (C < kLpMaxCluster && 2LL * C * T <= 2LL * rt.sm_count && V / (2 * C) >= kLpThreads * vec) C *= 2;
+    if (static_cast<long long>(T) * C > 0x7fffffffLL) return WQ4_ERR_UNSUPPORTED;
+    const LpArgs a{logits, tokens, logprobs, entropy, top_logprobs, top_ids, ld, V, top_k, C};
+    const dim3 grid(static_cast<unsigned>(T) * C);
+    switch (dtype) {
+        case WQ4_BF16: return launch(rt, logprobs_kernel<kLpBf16>, grid, kLpThreads, 0, C, stream, a);
+        case WQ4_FP16: return launch(rt, logprobs_kernel<kLpFp16>, grid, kLpThreads, 0, C, stream, a);
+        default: return launch(rt, logprobs_kernel<kLpFp32>, grid, kLpThreads, 0, C, stream, a);
+    }
+}

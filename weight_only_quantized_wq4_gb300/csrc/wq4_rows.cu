@@ -1,0 +1,277 @@
+// Rows in 8-bit float for the block-scaled product (wq4_block_mm.cu): RMS norm with the residual's
+// addition, and the gated activation. Both end alike. A row's values y, in fp32, are cut into
+// blocks of 128; block b of token t gets the scale
+//     s[b][t] = max(max |y| / 448, 2^-126)
+// and the codes q = e4m3(y / s), rounded to nearest even; 448 is e4m3's largest value, and the
+// lower bound keeps the quotient defined for a block of zeros. A NaN stays one in its own code and
+// does not touch its block's scale; a block with an infinity has an infinite scale, so that every
+// value read back from it (q s) is NaN.
+//
+// Both are bound by memory: each element is read and written once, in 16-byte vectors of 8 elements
+// where sizes, strides and pointers allow (single elements otherwise), and everything in between
+// stays in registers. 16 neighbouring lanes hold one block of 128, so a block's maximum takes four
+// shuffles and no shared memory.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
+#include <cmath>
+
+#include "wq4_device.cuh"
+#include "wq4_runtime.h"
+
+namespace wq4 {
+namespace {
+
+constexpr int kVec = 8;                 // elements a thread handles together
+constexpr int kRowBlock = 128;          // elements that share a scale
+constexpr float kE4m3Max = 448.f;
+
+template <bool BF16>
+__device__ __forceinline__ float to_f32(uint32_t b16) {
+    if constexpr (BF16) return __uint_as_float(b16 << 16);
+    else return __half2float(__ushort_as_half(static_cast<uint16_t>(b16)));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t from_f32(float v) {
+    if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    else return __half_as_ushort(__float2half_rn(v));
+}
+
+// Eight elements from column `col` of a row of D: one 16-byte load (VEC) or single ones; zeros past
+// the row's end.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8(const uint16_t* row, int col, int D, float (&v)[kVec]) {
+    if constexpr (VEC) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (col < D) w = *reinterpret_cast<const uint4*>(row + col);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = to_f32<BF16>(u[j] & 0xffffu);
+            v[2 * j + 1] = to_f32<BF16>(u[j] >> 16);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j] = col + j < D ? to_f32<BF16>(row[col + j]) : 0.f;
+    }
+}
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store8(uint16_t* row, int col, int D, const float (&v)[kVec]) {
+    if constexpr (VEC) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = from_f32<BF16>(v[2 * j]) | (from_f32<BF16>(v[2 * j + 1]) << 16);
+        if (col < D) *reinterpret_cast<uint4*>(row + col) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (col + j < D) row[col + j] = static_cast<uint16_t>(from_f32<BF16>(v[j]));
+    }
+}
+
+// Two fp32 to two e4m3 codes (nearest even; past 448: 448; NaN stays NaN), `lo` in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// The codes of eight values of a row (the thread's 16 lanes hold the block of 128 they are in) and,
+// from the first of those lanes, the block's scale. Every lane of the warp calls it.
+template <bool VEC>
+__device__ __forceinline__ void quantise8(const float (&y)[kVec], int col, int D, uint8_t* q_row, float* scale) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) m = fmaxf(m, fabsf(y[j]));      // (fmaxf passes NaN over)
+#pragma unroll
+    for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float s = fmaxf(__fdiv_rn(m, kE4m3Max), FLT_MIN);
+    // One reciprocal for the block instead of a division for each element: the quotient can be off
+    // by an fp32 ulp, which moves a code only where it lies that near to a rounding boundary.
+    const float inv = __frcp_rn(s);
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = e4m3x2(y[2 * j] * inv, y[2 * j + 1] * inv);
+    if (col < D) {
+        if constexpr (VEC) {
+            *reinterpret_cast<uint2*>(q_row + col) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (col + j < D) q_row[col + j] = static_cast<uint8_t>(c[j >> 1] >> (8 * (j & 1)));
+        }
+        if ((threadIdx.x & 15) == 0) *scale = s;
+    }
+}
+
+// ------------------------------------------------------------------------------ RMS norm
+struct NormArgs {
+    const uint16_t *x, *r, *w;          // r: null without a residual
+    uint16_t *r_out, *y;                // null where not asked for
+    uint8_t* q;                         // null where not asked for
+    float* scales;
+    long long ldx, ldr, ldro, ldy, ldq, lds;
+    int D;
+    float eps;
+};
+
+// One CTA per row; a thread holds VPT vectors of it in registers, so the row is read once although
+// its norm has to be known before the first value can be scaled.
+template <bool BF16, bool VEC, int VPT>
+__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
+    __shared__ float part[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long t = blockIdx.x;
+    const int D = a.D;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    float h[VPT][kVec];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int col = (i * blockDim.x + tid) * kVec;
+        load8<BF16, VEC>(a.x + t * a.ldx, col, D, h[i]);
+        if (a.r) {
+            float r[kVec];
+            load8<BF16, VEC>(a.r + t * a.ldr, col, D, r);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) h[i][j] += r[j];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+        // the sum in the 16-bit type is for the next layer; the norm goes by the unrounded one
+        if (a.r_out) store8<BF16, VEC>(a.r_out + t * a.ldro, (i * blockDim.x + tid) * kVec, D, h[i]);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    ss = lane < (blockDim.x >> 5) ? part[lane] : 0.f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    const float rstd = 1.f / sqrtf(ss / static_cast<float>(D) + a.eps);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int col = (i * blockDim.x + tid) * kVec;
+        float w[kVec];
+        load8<BF16, VEC>(a.w, col, D, w);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) h[i][j] = h[i][j] * rstd * w[j];
+        if (a.y) store8<BF16, VEC>(a.y + t * a.ldy, col, D, h[i]);
+        if (a.q) quantise8<VEC>(h[i], col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
+    }
+}
+
+template <bool BF16, bool VEC>
+int go_norm(const Runtime& rt, const NormArgs& a, int T, wq4_stream_t st) {
+    const int nv = (a.D + kVec - 1) / kVec;
+    const int vpt = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4;
+    const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
+    switch (vpt) {
+        case 1: return launch(rt, norm_kernel<BF16, VEC, 1>, dim3(T), threads, 0, 1, st, a);
+        case 2: return launch(rt, norm_kernel<BF16, VEC, 2>, dim3(T), threads, 0, 1, st, a);
+        default: return launch(rt, norm_kernel<BF16, VEC, 4>, dim3(T), threads, 0, 1, st, a);
+    }
+}
+
+constexpr int kNormMaxD = 1024 * 4 * kVec;
+
+// ------------------------------------------------------------------------------ gated activation
+struct GatedArgs {
+    const uint16_t* x;                  // [T][2 D]: gate, then up
+    uint8_t* q;
+    float* scales;
+    long long ldx, ldq, lds;
+    int D, chunks;                      // chunks: CTAs per row
+};
+
+constexpr int kGatedThreads = 256;
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kGatedThreads) gated_kernel(const GatedArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long t = blockIdx.x / a.chunks;
+    const int col = ((blockIdx.x % a.chunks) * kGatedThreads + threadIdx.x) * kVec;
+    const int D = a.D;
+    const uint16_t* row = a.x + t * a.ldx;
+    float g[kVec], u[kVec];
+    load8<BF16, VEC>(row, col, D, g);
+    load8<BF16, VEC>(row + D, col, D, u);
+    // silu(g) = g / (1 + exp(-g)); where exp(-g) is infinite the quotient is the limit, 0
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) g[j] = __fdividef(g[j], 1.f + __expf(-g[j])) * u[j];
+    quantise8<VEC>(g, col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
+}
+
+// The quantised rows an operator writes and the product reads: rows of codes on 16-byte boundaries,
+// a scale row per block of 128, also on 16-byte boundaries (both are copied as tensors).
+int check_rows(const void* Q, long long ldq, const void* scales, long long lds, int T, int D) {
+    if (!Q || !scales || ldq < D || lds < T) return WQ4_ERR_INVALID;
+    if (!aligned_to(Q, 16) || !aligned_to(scales, 16) || ldq % 16 || lds % 4) return WQ4_ERR_ALIGN;
+    return WQ4_OK;
+}
+
+bool vec_ok(const void* p, long long ld) { return !p || (aligned_to(p, 16) && ld % kVec == 0); }
+
+}  // namespace
+}  // namespace wq4
+
+using namespace wq4;
+
+extern "C" {
+
+int wq4_add_rmsnorm_quant(const void* X, long long ldx, const void* R, long long ldr, const void* weight, int T, int D,
+                          float eps, int dtype, void* R_out, long long ldro, void* Y, long long ldy, void* Q,
+                          long long ldq, float* scales, long long lds, wq4_stream_t stream) {
+    if (T < 0 || D < 1 || (dtype != WQ4_BF16 && dtype != WQ4_FP16) || !(eps >= 0.f) || std::isinf(eps))
+        return WQ4_ERR_INVALID;
+    if (D > kNormMaxD) return WQ4_ERR_UNSUPPORTED;
+    if (T == 0) return WQ4_OK;
+    if (!X || !weight || (R_out && !R) || (!Y && !Q) || (!Q != !scales)) return WQ4_ERR_INVALID;
+    if (ldx < D || (R && ldr < D) || (R_out && ldro < D) || (Y && ldy < D)) return WQ4_ERR_INVALID;
+    if (!aligned_to(X, 2) || !aligned_to(R, 2) || !aligned_to(weight, 2) || !aligned_to(R_out, 2) || !aligned_to(Y, 2))
+        return WQ4_ERR_ALIGN;
+    if (Q)
+        if (const int rc = check_rows(Q, ldq, scales, lds, T, D)) return rc;
+    Runtime rt;
+    if (const int rc = runtime(&rt)) return rc;
+    const NormArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(R),
+                     static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(R_out), static_cast<uint16_t*>(Y),
+                     static_cast<uint8_t*>(Q), scales, ldx, ldr, ldro, ldy, ldq, lds, D, eps};
+    const bool vec = D % kVec == 0 && vec_ok(X, ldx) && vec_ok(R, ldr) && vec_ok(weight, 0) && vec_ok(R_out, ldro) &&
+                     vec_ok(Y, ldy);
+    if (dtype == WQ4_BF16) return vec ? go_norm<true, true>(rt, a, T, stream) : go_norm<true, false>(rt, a, T, stream);
+    return vec ? go_norm<false, true>(rt, a, T, stream) : go_norm<false, false>(rt, a, T, stream);
+}
+
+int wq4_silu_mul_quant(const void* X, long long ldx, int T, int D, int dtype, void* Q, long long ldq, float* scales,
+                       long long lds, wq4_stream_t stream) {
+    if (T < 0 || D < 1 || (dtype != WQ4_BF16 && dtype != WQ4_FP16)) return WQ4_ERR_INVALID;
+    if (D > (1 << 24)) return WQ4_ERR_UNSUPPORTED;
+    if (T == 0) return WQ4_OK;
+    if (!X || ldx < 2LL * D) return WQ4_ERR_INVALID;
+    if (!aligned_to(X, 2)) return WQ4_ERR_ALIGN;
+    if (const int rc = check_rows(Q, ldq, scales, lds, T, D)) return rc;
+    const int chunks = (D + kGatedThreads * kVec - 1) / (kGatedThreads * kVec);
+    if (static_cast<long long>(T) * chunks > 0x7fffffffLL) return WQ4_ERR_UNSUPPORTED;
+    Runtime rt;
+    if (const int rc = runtime(&rt)) return rc;
+    const GatedArgs a{static_cast<const uint16_t*>(X), static_cast<uint8_t*>(Q), scales, ldx, ldq, lds, D, chunks};
+    const bool vec = D % kVec == 0 && vec_ok(X, ldx);
+    const dim3 grid(static_cast<unsigned>(T) * chunks);
+    if (dtype == WQ4_BF16)
+        return vec ? launch(rt, gated_kernel<true, true>, grid, kGatedThreads, 0, 1, stream, a)
+                   : launch(rt, gated_kernel<true, false>, grid, kGatedThreads, 0, 1, stream, a);
+    return vec ? launch(rt, gated_kernel<false, true>, grid, kGatedThreads, 0, 1, stream, a)
+               : launch(rt, gated_kernel<false, false>, grid, kGatedThreads, 0, 1, stream, a);
+}
+
+}  // extern "C"
