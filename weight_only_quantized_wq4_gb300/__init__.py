@@ -365,33 +365,64 @@ def grouped_mm_dev_ptrs(M: Sequence[int], N: Sequence[int], K: Sequence[int], X_
 
 
 # ------------------------------------------------------------------------------------ 8-bit rows
-def _rows(t, name: str, dtypes, like=None):
-    """Pointer and row stride (in elements) of a 2-D CUDA tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.dtype not in dtypes:
-        raise ValueError("%s must be a 2-D tensor of %s" % (name, " or ".join(str(d)[6:] for d in dtypes)))
-    if not t.is_cuda or (like is not None and t.device != like.device):
-        raise ValueError("%s must be a CUDA tensor%s" % (name, "" if like is None else " on the device of the others"))
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError("the rows of %s must be contiguous" % name)
-    if rows > 1:
-        return t.data_ptr(), t.stride(0)
-    return t.data_ptr(), (cols + 15) // 16 * 16       # (the stride of a single row is never used)
+# A decode step calls these every few microseconds, so the checks below read each tensor attribute
+# once, compare device numbers, and leave to the library what it checks itself (strides against
+# sizes, alignment).
+_t = None               # torch, and its types by the library's codes, once the first call has them
+_HALF = _OUT = _F8 = _F32 = None
 
 
-def _vector(t, name: str, n: int, dtypes, like):
-    """Pointer of a contiguous 1-D CUDA tensor of n elements."""
-    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes:
-        raise ValueError("%s must be a 1-D tensor of %d elements of %s" %
-                         (name, n, " or ".join(str(d)[6:] for d in dtypes)))
-    if t.device != like.device or (n > 1 and t.stride(0) != 1):
-        raise ValueError("%s must be contiguous, on the device of the others" % name)
+def _types():
+    global _t, _HALF, _OUT, _F8, _F32
+    torch = _torch()
+    _HALF = {torch.bfloat16: 0, torch.float16: 1}
+    _OUT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    _F8, _F32 = torch.float8_e4m3fn, torch.float32
+    _t = torch
+    return load_library()
+
+
+def _refuse(t, name: str, shape, dtype, dev: int):
+    """Raises for the first thing wrong with tensor t; called when _rows or _vector found something."""
+    if t.dim() != len(shape) or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be of shape %s" % (name, list(shape)))
+    if t.dtype != dtype:
+        raise ValueError("%s must be of type %s" % (name, str(dtype)[6:]))
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
+    raise ValueError("%s must be contiguous along its last dimension" % name)
+
+
+def _rows(t, name: str, rows: int, cols: int, dtype, dev: int):
+    """Pointer and row stride (in elements) of a [rows][cols] CUDA tensor whose rows are contiguous."""
+    if t.shape != (rows, cols) or t.dtype != dtype or t.get_device() != dev or dev < 0:
+        _refuse(t, name, (rows, cols), dtype, dev)
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        _refuse(t, name, (rows, cols), dtype, dev)
+    if rows <= 1:                                     # (the stride of a single row is never used)
+        ld = (cols + 15) // 16 * 16
+    return t.data_ptr(), ld
+
+
+def _vector(t, name: str, n: int, dtype, dev: int):
+    """Pointer of a contiguous CUDA tensor of n elements."""
+    if t.shape != (n,) or t.dtype != dtype or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
+        _refuse(t, name, (n,), dtype, dev)
     return t.data_ptr()
 
 
-def _shaped(t, name: str, rows: int, cols: int):
-    if t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError("%s must be [%d][%d]" % (name, rows, cols))
+def _two_d(t, name: str, types):
+    """(rows, columns, type code, device number) of a 2-D CUDA tensor of one of `types`."""
+    code = types.get(t.dtype)
+    if code is None or t.dim() != 2 or not t.is_cuda:
+        raise ValueError("%s must be a 2-D CUDA tensor of %s" % (name, " or ".join(str(d)[6:] for d in types)))
+    rows, cols = t.shape
+    return rows, cols, code, t.get_device()
+
+
+def _raw_stream(dev: int) -> int:
+    return _t._C._cuda_getCurrentRawStream(dev)       # current_stream(dev).cuda_stream without its object
 
 
 def alloc_quant_rows(T: int, D: int, device="cuda"):
@@ -403,16 +434,6 @@ def alloc_quant_rows(T: int, D: int, device="cuda"):
     return q[:, :D], scales[:, :T]
 
 
-def _quant_rows(q, scales, T: int, D: int, like):
-    """(q pointer, ldq, scales pointer, lds) of quantised rows."""
-    torch = _torch()
-    qp, ldq = _rows(q, "q", (torch.float8_e4m3fn,), like)
-    sp, lds = _rows(scales, "scales", (torch.float32,), like)
-    _shaped(q, "q", T, D)
-    _shaped(scales, "scales", (D + GROUP - 1) // GROUP, T)
-    return qp, ldq, sp, lds
-
-
 def add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, q=None, scales=None, residual_out=None, y=None):
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, quantised by rows (wq4_add_rmsnorm_quant).
 
@@ -420,76 +441,78 @@ def add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, q=None, scale
     [ceil(D/128)][T], and h in x's type (None without a residual). Buffers that are not given are
     allocated (alloc_quant_rows); residual_out may be x or residual itself. y: also write the
     16-bit y there (what mm reads)."""
-    torch = _torch()
-    lib = load_library()
-    half = (x.dtype,)
-    code = _dtype_code(x)
-    xp, ldx = _rows(x, "x", half)
-    T, D = x.shape
-    wp = _vector(weight, "weight", D, half, x)
-    rp = ldr = rop = ldro = yp = ldy = 0
+    lib = _types() if _t is None or _lib is None else _lib
+    T, D, code, dev = _two_d(x, "x", _HALF)
+    half = x.dtype
+    xp, ldx = _rows(x, "x", T, D, half, dev)
+    wp = _vector(weight, "weight", D, half, dev)
+    rp = rop = yp = None
+    ldr = ldro = ldy = 0
     if residual is not None:
-        rp, ldr = _rows(residual, "residual", half, x)
-        _shaped(residual, "residual", T, D)
+        rp, ldr = _rows(residual, "residual", T, D, half, dev)
         if residual_out is None:
-            residual_out = torch.empty((T, D), dtype=x.dtype, device=x.device)
+            residual_out = _t.empty((T, D), dtype=half, device=x.device)
     if residual_out is not None:
-        rop, ldro = _rows(residual_out, "residual_out", half, x)
-        _shaped(residual_out, "residual_out", T, D)
+        rop, ldro = _rows(residual_out, "residual_out", T, D, half, dev)
     if y is not None:
-        yp, ldy = _rows(y, "y", half, x)
-        _shaped(y, "y", T, D)
-    if q is None and scales is None:
+        yp, ldy = _rows(y, "y", T, D, half, dev)
+    if q is None or scales is None:
+        if q is not scales:
+            raise ValueError("q and scales are given together")
         q, scales = alloc_quant_rows(T, D, x.device)
-    qp, ldq, sp, lds = _quant_rows(q, scales, T, D, x)
-    _check(lib.wq4_add_rmsnorm_quant(xp, ldx, rp or None, ldr, wp, T, D, eps, code, rop or None, ldro, yp or None, ldy,
-                                     qp, ldq, sp, lds, _stream(x.device)), "wq4_add_rmsnorm_quant")
+    qp, ldq = _rows(q, "q", T, D, _F8, dev)
+    sp, lds = _rows(scales, "scales", (D + 127) // 128, T, _F32, dev)
+    rc = lib.wq4_add_rmsnorm_quant(xp, ldx, rp, ldr, wp, T, D, eps, code, rop, ldro, yp, ldy, qp, ldq, sp, lds,
+                                   _raw_stream(dev))
+    if rc:
+        raise Wq4Error(rc, "wq4_add_rmsnorm_quant")
     return q, scales, residual_out
 
 
 def silu_mul_quant(x, q=None, scales=None):
     """y = silu(x[:, :D]) * x[:, D:] for x bf16/fp16 [T][2 D], quantised by rows (wq4_silu_mul_quant):
     returns (q, scales) as add_rmsnorm_quant does."""
-    lib = load_library()
-    code = _dtype_code(x)
-    xp, ldx = _rows(x, "x", (x.dtype,))
-    T, D = x.shape[0], x.shape[1] // 2
-    if x.shape[1] % 2:
+    lib = _types() if _t is None or _lib is None else _lib
+    T, D2, code, dev = _two_d(x, "x", _HALF)
+    D = D2 // 2
+    if D2 != 2 * D:
         raise ValueError("x must hold a gate and an up half")
-    if q is None and scales is None:
+    xp, ldx = _rows(x, "x", T, D2, x.dtype, dev)
+    if q is None or scales is None:
+        if q is not scales:
+            raise ValueError("q and scales are given together")
         q, scales = alloc_quant_rows(T, D, x.device)
-    qp, ldq, sp, lds = _quant_rows(q, scales, T, D, x)
-    _check(lib.wq4_silu_mul_quant(xp, ldx, T, D, code, qp, ldq, sp, lds, _stream(x.device)), "wq4_silu_mul_quant")
+    qp, ldq = _rows(q, "q", T, D, _F8, dev)
+    sp, lds = _rows(scales, "scales", (D + 127) // 128, T, _F32, dev)
+    rc = lib.wq4_silu_mul_quant(xp, ldx, T, D, code, qp, ldq, sp, lds, _raw_stream(dev))
+    if rc:
+        raise Wq4Error(rc, "wq4_silu_mul_quant")
     return q, scales
-
-
-def _out_types():
-    torch = _torch()
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 def block_mm(q, scales, W, W_scales, out=None, dtype=None):
     """Y[M,N] = X . W^T of quantised rows (q, scales) [M][K] with an e4m3 weight W [N][K] and its fp32 scales
     [ceil(N/128)][ceil(K/128)] (wq4_block_mm). Y is bf16, fp16 or fp32: out's type, or dtype (a
     torch type, bfloat16 by default)."""
-    torch = _torch()
-    lib = load_library()
-    M, K = q.shape
-    qp, ldq, sp, lds = _quant_rows(q, scales, M, K, q)
-    wp, ldw = _rows(W, "W", (torch.float8_e4m3fn,), q)
+    lib = _types() if _t is None or _lib is None else _lib
+    M, K, _, dev = _two_d(q, "q", {_F8: 0})
     N = W.shape[0]
-    _shaped(W, "W", N, K)
-    wsp, ldws = _rows(W_scales, "W_scales", (torch.float32,), q)
-    _shaped(W_scales, "W_scales", (N + GROUP - 1) // GROUP, (K + GROUP - 1) // GROUP)
+    kb = (K + 127) // 128
+    qp, ldq = _rows(q, "q", M, K, _F8, dev)
+    sp, lds = _rows(scales, "scales", kb, M, _F32, dev)
+    wp, ldw = _rows(W, "W", N, K, _F8, dev)
+    wsp, ldws = _rows(W_scales, "W_scales", (N + 127) // 128, kb, _F32, dev)
     if out is None:
-        out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=q.device)
+        out = _t.empty((M, N), dtype=dtype or _t.bfloat16, device=q.device)
     elif dtype is not None and out.dtype != dtype:
         raise ValueError("out is not of the dtype asked for")
-    types = _out_types()
-    yp, ldy = _rows(out, "out", tuple(types), q)
-    _shaped(out, "out", M, N)
-    _check(lib.wq4_block_mm(qp, ldq, sp, lds, wp, ldw, wsp, ldws, yp, ldy, M, N, K, types[out.dtype],
-                            _stream(q.device)), "wq4_block_mm")
+    code = _OUT.get(out.dtype)
+    if code is None:
+        raise ValueError("the product's type must be bfloat16, float16 or float32")
+    yp, ldy = _rows(out, "out", M, N, out.dtype, dev)
+    rc = lib.wq4_block_mm(qp, ldq, sp, lds, wp, ldw, wsp, ldws, yp, ldy, M, N, K, code, _raw_stream(dev))
+    if rc:
+        raise Wq4Error(rc, "wq4_block_mm")
     return out
 
 
@@ -498,34 +521,34 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entropy=N
     and its top_k most likely tokens (wq4_token_logprobs). Returns (logprobs [T] or None, entropy [T], top_ids
     int32 [T][top_k], top_logprobs [T][top_k]); the last two are None with top_k = 0. Buffers that are
     not given are allocated."""
-    torch = _torch()
-    lib = load_library()
-    types = _out_types()
-    lp, ld = _rows(logits, "logits", tuple(types))
-    T, V = logits.shape
-    dev, f32 = logits.device, (torch.float32,)
-    tp = lpp = tip = tlp = 0
+    lib = _types() if _t is None or _lib is None else _lib
+    T, V, code, dev = _two_d(logits, "logits", _OUT)
+    lp, ld = _rows(logits, "logits", T, V, logits.dtype, dev)
+    if T == 1:
+        ld = V
+    tp = lpp = tip = tlp = None
     if tokens is not None:
-        tp = _vector(tokens, "tokens", T, (torch.int64,), logits)
+        tp = _vector(tokens, "tokens", T, _t.int64, dev)
         if logprobs is None:
-            logprobs = torch.empty(T, dtype=torch.float32, device=dev)
-        lpp = _vector(logprobs, "logprobs", T, f32, logits)
+            logprobs = _t.empty(T, dtype=_F32, device=logits.device)
+        lpp = _vector(logprobs, "logprobs", T, _F32, dev)
     elif logprobs is not None:
         raise ValueError("logprobs needs tokens")
     if entropy is None:
-        entropy = torch.empty(T, dtype=torch.float32, device=dev)
-    ep = _vector(entropy, "entropy", T, f32, logits)
+        entropy = _t.empty(T, dtype=_F32, device=logits.device)
+    ep = _vector(entropy, "entropy", T, _F32, dev)
     if top_k > 0:
         if top_ids is None:
-            top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+            top_ids = _t.empty((T, top_k), dtype=_t.int32, device=logits.device)
         if top_logprobs is None:
-            top_logprobs = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        for t, name, dt in ((top_ids, "top_ids", torch.int32), (top_logprobs, "top_logprobs", torch.float32)):
-            if t.shape != (T, top_k) or t.dtype != dt or t.device != dev or not t.is_contiguous():
-                raise ValueError("%s must be a contiguous %s tensor [%d][%d]" % (name, str(dt)[6:], T, top_k))
-        tip, tlp = top_ids.data_ptr(), top_logprobs.data_ptr()
+            top_logprobs = _t.empty((T, top_k), dtype=_F32, device=logits.device)
+        tip, ldi = _rows(top_ids, "top_ids", T, top_k, _t.int32, dev)
+        tlp, ldl = _rows(top_logprobs, "top_logprobs", T, top_k, _F32, dev)
+        if T > 1 and (ldi != top_k or ldl != top_k):
+            raise ValueError("top_ids and top_logprobs must be contiguous")
     elif top_ids is not None or top_logprobs is not None:
         raise ValueError("top_ids and top_logprobs need top_k")
-    _check(lib.wq4_token_logprobs(lp, ld, tp or None, T, V, types[logits.dtype], top_k, lpp or None, ep, tip or None,
-                                  tlp or None, _stream(dev)), "wq4_token_logprobs")
+    rc = lib.wq4_token_logprobs(lp, ld, tp, T, V, code, top_k, lpp, ep, tip, tlp, _raw_stream(dev))
+    if rc:
+        raise Wq4Error(rc, "wq4_token_logprobs")
     return logprobs, entropy, top_ids, top_logprobs
