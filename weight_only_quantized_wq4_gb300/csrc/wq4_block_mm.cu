@@ -14,11 +14,15 @@
 //                           only, so that a tile's cost is its weights' bytes.
 //
 // Warp roles (one CTA per SM, persistent over tiles):
-//   warp 0   copies: per block of K, both operands' 128-byte row pieces as 2-D tensor copies with the
-//            128-byte swizzle (rows and K past the end read as zero) and the tokens' scales, into a
-//            ring of stages
-//   warp 1   MMAs: one thread issues the block's four (K = 32 each), commits to the fold warps
-//   warps 4+ fold: read P_b, add it in, at a tile's end round once and store
+//   warps 0, 2   copies: per block of K, one operand's 128-byte row pieces each as a 2-D tensor copy with
+//                the 128-byte swizzle (rows and K past the end read as zero), into a ring of stages. A
+//                thread alone cannot issue both operands' copies as fast as a block is used.
+//   warps 1, 3   MMAs: one thread each, taking steps (one block, or two with few tokens) in turn; four
+//                MMAs (K = 32) a block, then a commit to the fold warps. One thread issues an MMA in
+//                46 cycles and needs some 75 for each wait and commit besides, so that its own step of
+//                narrow MMAs takes longer than the tensor core does; two overlap.
+//   warps 4+     fold: read P_b, add it in, at a tile's end round once and store. They load the
+//                scales themselves, a few blocks ahead.
 // With fewer tiles than SMs, a cluster of CTAs shares each tile, cut along K; the parts are added in
 // rank order through distributed shared memory.
 //
@@ -38,18 +42,18 @@ namespace {
 constexpr int kBmBlock = 128;                  // K elements (bytes) of a block
 constexpr int kBmLanes = 128;                  // rows of the lane operand per tile
 constexpr int kBmMaxSmem = 232448;
+constexpr int kAhead = 4;                      // blocks whose scales are loaded together, one such group ahead
 
 struct BmArgs {
     CUtensorMap lane_map, col_map;             // e4m3 codes [rows][K], box 128 K x tile rows
-    CUtensorMap sx_map;                        // token scales [blocks][M], box tokens of a tile x 1
-    const float* sw;                           // weight scales, row n / 128, column b
+    const float *sx, *sw;                      // token scales, row b, column m; weight scales, row n / 128, column b
     void* y;
-    long long ldy, ldsw;
+    long long ldsx, ldsw, ldy;
     int M, N, kb;                              // kb: blocks of K
     int lane_tiles, tiles;                     // tile t: lane tile t % lane_tiles, column tile t / lane_tiles
     int split;                                 // CTAs per cluster, each with a part of K (1: none)
     int dtype;
-    int vec_store;                             // rows of Y start on 16-byte boundaries
+    int unit;                                  // bytes that a row of Y is stored by: 16, or what its start allows
     unsigned int* status;
     long long timeout_cycles;
     int test_stall;
@@ -58,6 +62,7 @@ struct BmArgs {
 // NT: columns of a tile; TOK_LANES: tokens on the lanes (else weight rows).
 template <int NT, bool TOK_LANES>
 struct BmCfg {
+    static constexpr int kG = TOK_LANES ? 1 : 2;                // blocks of K per step of the pipeline
     static constexpr int kFW = TOK_LANES ? 8 : 4;               // fold warps
     static constexpr int kParts = kFW / 4;                      // fold warps per lane quarter
     static constexpr int kNC = NT / kParts;                     // columns of a fold thread
@@ -65,21 +70,28 @@ struct BmCfg {
     static constexpr int kLaneBytes = kBmLanes * kBmBlock;
     static constexpr int kColBytes = NT * kBmBlock;
     static constexpr int kTokens = TOK_LANES ? kBmLanes : NT;
-    static constexpr int kScaleBytes = kTokens * 4;
-    static constexpr int kStageBytes = kLaneBytes + kColBytes + 1024;   // scales in the last KB
+    static constexpr int kBlockBytes = kLaneBytes + kColBytes;
+    static constexpr int kStageBytes = kG * kBlockBytes;
     static constexpr int kBarBytes = 1024;
-    static constexpr int kFit = (kBmMaxSmem - 1024 - kBarBytes) / kStageBytes;
-    static constexpr int kStages = kFit > 12 ? 12 : kFit;
-    static constexpr int kPBufs = NT <= 128 ? 4 : 2;
-    static constexpr int kTmemCols = NT * kPBufs < 32 ? 32 : NT * kPBufs;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes;
+    // per fold warp: rows of an output chunk on their way to coalesced stores, 32 of 64 + 16 bytes (tokens on
+    // the lanes), or the factors of a step's tokens, twice
+    static constexpr int kWarpBytes = TOK_LANES ? 32 * 80 : 2 * kG * NT * 4;
+    // An even number of stages and of P buffers: the MMA warps take alternate steps, so each walks every
+    // phase of its own ones (a parity wait is unambiguous one phase ahead only).
+    static constexpr int kFit = (kBmMaxSmem - 1024 - kBarBytes - kFW * kWarpBytes) / kStageBytes;
+    static constexpr int kStages = (kFit > 12 ? 12 : kFit) & ~1;
+    static constexpr int kPCols = kG * NT;                      // tensor-memory columns of a step's P buffer
+    static constexpr int kPBufs = kPCols <= 128 ? 4 : 2;
+    static constexpr int kTmemCols = kPCols * kPBufs;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + kFW * kWarpBytes;
     // 128 fp32 accumulators per fold thread want more registers than an even share: 384 threads
-    // launched with 168 each (64512 in all), of which the copy and MMA warps keep 72 and the fold
-    // warps take 216 (128 x 72 + 256 x 216 = 64512).
+    // launched with 168 each (64512 in all), of which the copy and MMA warps keep 56 and the fold
+    // warps take 224 (128 x 56 + 256 x 224 = 64512).
     static constexpr bool kRegSplit = kNC > 64;
-    static constexpr int kLaunchRegs = 168, kRegWg0 = 72, kRegFold = 216;
+    static constexpr int kLaunchRegs = 168, kRegWg0 = 56, kRegFold = 224;
     static_assert(!kRegSplit || 128 * kRegWg0 + 32 * kFW * kRegFold <= kThreads * kLaunchRegs, "register split");
-    static_assert(kStages >= 3 && kTmemCols <= 512 && kSmemBytes <= kBmMaxSmem, "tile");
+    static_assert(kStages >= 4 && kTmemCols <= 512 && kSmemBytes <= kBmMaxSmem, "tile");
+    static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kAhead % kG == 0, "tensor memory, steps");
     static_assert(kStages * kStageBytes >= kBmLanes * NT * 4, "cluster reduction buffer");
 };
 
@@ -95,48 +107,110 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
 // kind::f8f6f4: D fp32, A and B e4m3 (format code 0), both K-major, M x N.
 __device__ constexpr uint32_t f8_idesc(uint32_t M, uint32_t N) { return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24); }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+
+// (d0, d1) += (f0, f1) * (v0, v1), one packed fp32 FMA.
+__device__ __forceinline__ void fma_pair(float& d0, float& d1, float f0, float f1, uint32_t v0, uint32_t v1) {
+    uint64_t d, f, v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(d0), "f"(d1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(f) : "f"(f0), "f"(f1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(f), "l"(v));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
 }
 
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int dtype) {
+    uint32_t u;
+    if (dtype == WQ4_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+    return u;
 }
 
-// One value in the output type (dtype is the same for the whole launch).
-__device__ __forceinline__ void store_y(void* y, long long at, float v, int dtype) {
-    if (dtype == WQ4_BF16) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
-    else if (dtype == WQ4_FP16) static_cast<__half*>(y)[at] = __float2half_rn(v);
-    else static_cast<float*>(y)[at] = v;
-}
-
-// Columns [n, n + 8) of row m, of which those below N exist.
-__device__ __forceinline__ void store_row8(const BmArgs& a, int m, int n, const float* v) {
-    const long long at = m * a.ldy + n;
-    if (a.vec_store && n + 8 <= a.N) {
-        if (a.dtype == WQ4_FP32) {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.y) + at);
-            p[0] = make_float4(v[0], v[1], v[2], v[3]);
-            p[1] = make_float4(v[4], v[5], v[6], v[7]);
-            return;
-        }
-        uint32_t u[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (a.dtype == WQ4_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
-            else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at) = make_uint4(u[0], u[1], u[2], u[3]);
-        return;
+// UNIT bytes from shared to global memory.
+template <int UNIT>
+__device__ __forceinline__ void copy_unit(void* to, uint32_t from) {
+    if constexpr (UNIT == 16) {
+        *static_cast<uint4*>(to) = lds128(from);
+    } else if constexpr (UNIT == 8) {
+        uint2 u;
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(from));
+        *static_cast<uint2*>(to) = u;
+    } else if constexpr (UNIT == 4) {
+        uint32_t u;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(from));
+        *static_cast<uint32_t*>(to) = u;
+    } else {
+        uint16_t u;
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(from));
+        *static_cast<uint16_t*>(to) = u;
     }
+}
+
+// The 32 rows of 16 columns in `buf` (80 bytes a row) to rows m0.. of Y, columns n..: runs of a row
+// by neighbouring lanes, UNIT bytes each (what the rows of Y start on), SIZE bytes a value.
+template <int SIZE, int UNIT>
+__device__ __forceinline__ void copy_rows16(const BmArgs& a, uint32_t buf, int lane, int m0, int n) {
+    constexpr int kPerRow = 16 * SIZE / UNIT, kRows = 32 / kPerRow, kIn = UNIT / SIZE;
+    const int c = lane % kPerRow * kIn, r0 = lane / kPerRow;
+    const int cols = a.N - n - c, rows = a.M - m0;   // what exists from here on
+    uint8_t* to = static_cast<uint8_t*>(a.y) + ((m0 + r0) * a.ldy + n + c) * SIZE;
+    const long long step = a.ldy * (kRows * SIZE);
+    uint32_t from = buf + r0 * 80 + c * SIZE;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (n + j < a.N) store_y(a.y, at + j, v[j], a.dtype);
+    for (int r = r0; r < 32; r += kRows, to += step, from += kRows * 80) {
+        if (r >= rows) break;
+        if (cols >= kIn) {
+            copy_unit<UNIT>(to, from);
+        } else {                                     // the row ends inside the unit
+            for (int j = 0; j < cols; ++j) copy_unit<SIZE>(to + j * SIZE, from + j * SIZE);
+        }
+    }
+}
+
+// A warp's 32 rows from m0, one per lane, 16 columns from n, through `buf` in shared memory: stored by
+// their lanes directly, rows would touch 32 lines with every instruction.
+__device__ __forceinline__ void store_rows16(const BmArgs& a, uint32_t buf, int lane, int m0, int n, const float* v) {
+    const uint32_t mine = buf + lane * 80;
+    if (a.dtype == WQ4_FP32) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+            sts128(mine + 4 * j, __float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
+                   __float_as_uint(v[j + 3]));
+        __syncwarp();
+        if (a.unit == 16) copy_rows16<4, 16>(a, buf, lane, m0, n);
+        else copy_rows16<4, 4>(a, buf, lane, m0, n);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; j += 8)
+            sts128(mine + 2 * j, pack16(v[j], v[j + 1], a.dtype), pack16(v[j + 2], v[j + 3], a.dtype),
+                   pack16(v[j + 4], v[j + 5], a.dtype), pack16(v[j + 6], v[j + 7], a.dtype));
+        __syncwarp();
+        if (a.unit == 16) copy_rows16<2, 16>(a, buf, lane, m0, n);
+        else if (a.unit == 8) copy_rows16<2, 8>(a, buf, lane, m0, n);
+        else if (a.unit == 4) copy_rows16<2, 4>(a, buf, lane, m0, n);
+        else copy_rows16<2, 2>(a, buf, lane, m0, n);
+    }
+    __syncwarp();
+}
+
+// One column n of Y per lane, CNT tokens from m: neighbouring lanes' columns are neighbours in memory.
+template <int CNT>
+__device__ __forceinline__ void store_cols(const BmArgs& a, int m, int n, const float* v) {
+    if (n >= a.N) return;
+    const int rows = a.M - m;
+    const long long at = m * a.ldy + n;
+    if (a.dtype == WQ4_FP32) {
+        float* y = static_cast<float*>(a.y) + at;
+#pragma unroll
+        for (int j = 0; j < CNT; ++j, y += a.ldy)
+            if (j < rows) *y = v[j];
+    } else {
+        uint16_t* y = static_cast<uint16_t*>(a.y) + at;
+#pragma unroll
+        for (int j = 0; j < CNT; ++j, y += a.ldy)
+            if (j < rows) *y = static_cast<uint16_t>(pack16(v[j], 0.f, a.dtype));
+    }
 }
 
 // The tiles of one CTA, in order, and the part of K it takes of each.
@@ -159,31 +233,32 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
     const uint32_t s_bar = s_ring + C::kStages * C::kStageBytes;
     auto full_bar = [&](int s) { return s_bar + 8u * s; };
     auto empty_bar = [&](int s) { return s_bar + 8u * (16 + s); };
+    const uint32_t s_warp = s_bar + C::kBarBytes;    // the fold warps' buffers
     auto pfull_bar = [&](int b) { return s_bar + 8u * (32 + b); };
     auto pempty_bar = [&](int b) { return s_bar + 8u * (36 + b); };
     const uint32_t drain_bar = s_bar + 8u * 40, stall_bar = s_bar + 8u * 41;
     uint8_t* const gmisc = smem_raw + (s_bar - raw_s) + 8 * 48;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gmisc);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(gmisc + 4);
+    volatile int* const issued_by = reinterpret_cast<volatile int*>(gmisc + 8);   // stages the two copy threads filled
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1 + C::kFW);     // the MMAs' commit, and the fold warps done with the scales
+            mbar_init(full_bar(s), 2);               // both operands' copies
+            mbar_init(empty_bar(s), 1);
         }
         for (int b = 0; b < C::kPBufs; ++b) {
             mbar_init(pfull_bar(b), 1);
             mbar_init(pempty_bar(b), C::kFW);
         }
-        mbar_init(drain_bar, 1);
+        mbar_init(drain_bar, 2);                     // one commit from each MMA warp
         mbar_init(stall_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&a.lane_map);
         prefetch_tensormap(&a.col_map);
-        prefetch_tensormap(&a.sx_map);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
@@ -196,51 +271,67 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const WaitCtl ctl{abort_flag, a.status, a.timeout_cycles};
-    int issued = 0;                                  // stages the copy thread has filled
+    int issued = 0;                                  // stages a copy thread has filled
 
     if (warp < 4) {
         if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegWg0));
-        if (warp == 0) {
+        if (warp == 0 || warp == 2) {
             if (lane == 0) {
                 // an operand that only one tile along its side reads streams through L2
-                const uint64_t first = policy_evict_first(), last = policy_evict_last();
-                const bool cols_once = a.lane_tiles == 1, lanes_once = a.tiles == a.lane_tiles;
+                const bool lanes = warp == 0, once = lanes ? a.tiles == a.lane_tiles : a.lane_tiles == 1;
+                const uint64_t policy = once ? policy_evict_first() : policy_evict_last();
+                const CUtensorMap* map = lanes ? &a.lane_map : &a.col_map;
+                const uint32_t dst = s_ring + (lanes ? 0 : C::kLaneBytes), bytes = lanes ? C::kLaneBytes : C::kColBytes;
                 bool ok = true;
-                int i = 0;
+                int st = 0, i = 0;
+                uint32_t phase = 1;
                 for (BmSched s(a, rank); s.t < a.tiles && ok; s.t += s.step) {
-                    const int l0 = s.t % a.lane_tiles * kBmLanes, c0 = s.t / a.lane_tiles * NT;
-                    for (int b = s.kb0; b < s.kb1; ++b, ++i) {
-                        const int st = i % C::kStages;
-                        if (!mbar_wait(empty_bar(st), ((i / C::kStages) & 1) ^ 1, ctl)) { ok = false; break; }
-                        const uint32_t stage = s_ring + st * C::kStageBytes;
-                        mbar_arrive_expect_tx(full_bar(st), C::kLaneBytes + C::kColBytes + C::kScaleBytes);
-                        tma_load_2d(stage, &a.lane_map, full_bar(st), b * kBmBlock, l0, lanes_once ? first : last);
-                        tma_load_2d(stage + C::kLaneBytes, &a.col_map, full_bar(st), b * kBmBlock, c0, cols_once ? first : last);
-                        tma_load_2d(stage + C::kLaneBytes + C::kColBytes, &a.sx_map, full_bar(st), TOK_LANES ? l0 : c0, b, last);
+                    const int row = lanes ? s.t % a.lane_tiles * kBmLanes : s.t / a.lane_tiles * NT;
+                    for (int b = s.kb0; b < s.kb1; b += C::kG, ++i) {
+                        if (!mbar_wait(empty_bar(st), phase, ctl)) { ok = false; break; }
+                        const int n = min(C::kG, s.kb1 - b);
+                        mbar_arrive_expect_tx(full_bar(st), n * bytes);
+#pragma unroll
+                        for (int g = 0; g < C::kG; ++g)
+                            if (g < n)
+                                tma_load_2d(dst + st * C::kStageBytes + g * C::kBlockBytes, map, full_bar(st),
+                                            (b + g) * kBmBlock, row, policy);
+                        if (++st == C::kStages) { st = 0; phase ^= 1; }
                     }
                 }
                 issued = i;
             }
             __syncwarp();
-        } else if (warp == 1) {
+        } else {
             if (lane == 0) {
                 constexpr uint32_t idesc = f8_idesc(kBmLanes, NT);
-                bool ok = !a.test_stall || mbar_wait(stall_bar, 0, ctl);
-                int i = 0;
+                const int mine = warp >> 1;          // this thread's steps: the even or the odd ones
+                bool ok = !(a.test_stall && mine == 0) || mbar_wait(stall_bar, 0, ctl);
+                const uint64_t desc0 = make_sdesc_sw128(s_ring);
+                int st = mine, p = mine, skip = mine;
+                uint32_t full = 0, free = 1;         // phase parities
                 for (BmSched s(a, rank); s.t < a.tiles && ok; s.t += s.step) {
-                    for (int b = s.kb0; b < s.kb1; ++b, ++i) {
-                        const int st = i % C::kStages, p = i % C::kPBufs;
-                        if (!mbar_wait(full_bar(st), (i / C::kStages) & 1, ctl)) { ok = false; break; }
-                        if (!mbar_wait(pempty_bar(p), ((i / C::kPBufs) & 1) ^ 1, ctl)) { ok = false; break; }
+                    int b = s.kb0 + skip * C::kG;
+                    for (; b < s.kb1; b += 2 * C::kG) {
+                        if (!mbar_wait(full_bar(st), full, ctl)) { ok = false; break; }
+                        if (!mbar_wait(pempty_bar(p), free, ctl)) { ok = false; break; }
                         tc_fence_after();
-                        const uint32_t stage = s_ring + st * C::kStageBytes;
+                        const uint64_t desc = desc0 + static_cast<uint32_t>(st * (C::kStageBytes >> 4));
+                        const uint32_t d = tmem + p * C::kPCols;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f8(tmem + p * NT, make_sdesc_sw128(stage + 32 * k),
-                                   make_sdesc_sw128(stage + C::kLaneBytes + 32 * k), idesc, k > 0);
+                        for (int g = 0; g < C::kG; ++g) {
+                            if (b + g >= s.kb1) break;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f8(d + g * NT, desc + (g * (C::kBlockBytes >> 4) + 2 * k),
+                                       desc + (g * (C::kBlockBytes >> 4) + (C::kLaneBytes >> 4) + 2 * k), idesc, k > 0);
+                        }
                         mma_commit(pfull_bar(p));
                         mma_commit(empty_bar(st));
+                        if ((st += 2) >= C::kStages) { st = mine; full ^= 1; }
+                        if ((p += 2) >= C::kPBufs) { p = mine; free ^= 1; }
                     }
+                    skip = (b - s.kb1) / C::kG;      // (the turns go on over the tiles' ends)
                 }
                 mma_commit(drain_bar);               // every MMA is done before the tensor memory goes
                 mbar_wait_plain(drain_bar, 0, drain_limit(a.timeout_cycles));
@@ -249,79 +340,113 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
         }
     } else {
         if constexpr (C::kRegSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegFold));
+        float acc[C::kNC] = {};
         const int quarter = warp & 3, part = (warp - 4) >> 2;
         const int r = 32 * quarter + lane;           // this thread's lane of the tile
         const int col0 = part * C::kNC;              // and its first column
         const uint32_t t_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + col0;
+        const uint32_t buf = s_warp + (warp - 4) * C::kWarpBytes;
         const int sw_rows = (a.N + 127) / 128;
-        float acc[C::kNC] = {};
         bool ok = true;
-        int i = 0;
+        int p = 0;
+        uint32_t phase = 0;
         for (BmSched s(a, rank); s.t < a.tiles && ok; s.t += s.step) {
             const int l0 = s.t % a.lane_tiles * kBmLanes, c0 = s.t / a.lane_tiles * NT;
-            const int wrow = min((TOK_LANES ? c0 + col0 : l0) / 128, sw_rows - 1);
-            const float* sw = a.sw + wrow * a.ldsw;
+            const float* sw = a.sw + min((TOK_LANES ? c0 + col0 : l0) / 128, sw_rows - 1) * a.ldsw;
+            // The tokens whose scales this thread loads (none past the last token: such values are not stored),
+            // and the scales of the kAhead blocks from `b` on; they are multiplied only when their turn
+            // comes, so that nothing waits for a load just issued.
+            constexpr int kPer = TOK_LANES ? 1 : (NT + 31) / 32;     // tokens per lane
+            const int token = TOK_LANES ? l0 + r : c0 + lane;
+            const bool loads = token < a.M && (TOK_LANES || lane < NT);
+            const bool loads2 = kPer > 1 && token + 32 < a.M;
+            float nsx[kAhead * kPer], nsw[kAhead];
+            auto load_scales = [&](int b) {
+                const float* x = a.sx + token + b * a.ldsx;
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j, x += a.ldsx) {
+                    const bool in = b + j < s.kb1;
+                    nsw[j] = in ? __ldg(sw + b + j) : 0.f;
+                    nsx[j * kPer] = in && loads ? __ldg(x) : 0.f;
+                    if constexpr (kPer > 1) nsx[j * kPer + 1] = in && loads2 ? __ldg(x + 32) : 0.f;
+                }
+            };
 #pragma unroll
             for (int j = 0; j < C::kNC; ++j) acc[j] = 0.f;
-            float w = s.kb0 < s.kb1 ? __ldg(sw + s.kb0) : 0.f;
-            for (int b = s.kb0; b < s.kb1; ++b, ++i) {
-                const int st = i % C::kStages, p = i % C::kPBufs;
-                const float w_next = b + 1 < s.kb1 ? __ldg(sw + b + 1) : 0.f;
-                if (!mbar_wait(pfull_bar(p), (i / C::kPBufs) & 1, ctl)) { ok = false; break; }
-                // (the stage's copies had landed before its MMAs were issued; this wait, which passes at
-                // once, makes the scales among them visible here)
-                if (!mbar_wait(full_bar(st), (i / C::kStages) & 1, ctl)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t s_sx = s_ring + st * C::kStageBytes + C::kLaneBytes + C::kColBytes;
-                if constexpr (TOK_LANES) {
-                    const float f = lds_f32(s_sx + 4 * r) * w;
+            load_scales(s.kb0);
+            __syncwarp();                            // (no lane still reads the last tile's factors)
+            for (int b0 = s.kb0; b0 < s.kb1 && ok; b0 += kAhead) {
+                float f[kAhead * kPer];
 #pragma unroll
-                    for (int j = 0; j < C::kNC; j += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(t_addr + p * NT + j, v);
-                        tmem_ld_wait();
+                for (int j = 0; j < kAhead * kPer; ++j) f[j] = nsx[j] * nsw[j / kPer];
+                load_scales(b0 + kAhead);
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) acc[j + q] = fmaf(f, __uint_as_float(v[q]), acc[j + q]);
+                for (int j = 0; j < kAhead; j += C::kG) {
+                    if (b0 + j >= s.kb1) break;
+                    const uint32_t factors = buf + (j / C::kG & 1) * (C::kG * NT * 4);
+                    if (!TOK_LANES) {                // the step's factors, where every lane can read them
+#pragma unroll
+                        for (int g = 0; g < C::kG; ++g)
+#pragma unroll
+                            for (int q = 0; q < kPer; ++q)
+                                if (lane + 32 * q < NT)
+                                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(factors + (g * NT + lane + 32 * q) * 4),
+                                                 "f"(f[(j + g) * kPer + q])
+                                                 : "memory");
+                        __syncwarp();
                     }
-                } else {
+                    if (!mbar_wait(pfull_bar(p), phase, ctl)) { ok = false; break; }
+                    tc_fence_after();
+                    // the step's columns of P, in pieces: the next piece is read while this one is added in. (A step's
+                    // second block past the end of K is left out: its buffer holds an earlier step's values.)
+                    constexpr int kCols = NT < 32 ? 16 : 32, kPieces = C::kNC / kCols;
+                    const int pieces = kPieces * (C::kG == 1 || b0 + j + 1 < s.kb1 ? C::kG : 1);
+                    uint32_t v[2][kCols];
+                    tmem_ldn(t_addr + p * C::kPCols, v[0]);
 #pragma unroll
-                    for (int j = 0; j < C::kNC; j += 8) {
-                        uint32_t v[8];
-                        tmem_ld8(t_addr + p * NT + j, v);
-                        const uint4 f0 = lds128(s_sx + 4 * j), f1 = lds128(s_sx + 4 * j + 16);
-                        const uint32_t f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                    for (int c = 0; c < kPieces * C::kG; ++c) {
+                        if (c >= pieces) break;
+                        uint32_t(&now)[kCols] = v[c & 1];
+                        const int g = c / kPieces, at = c % kPieces * kCols;
                         tmem_ld_wait();
+                        if (c + 1 < pieces) {
+                            tmem_ldn(t_addr + p * C::kPCols + (c + 1) / kPieces * NT + (c + 1) % kPieces * kCols, v[c + 1 & 1]);
+                        } else {                     // all of the step's P is in registers: the buffer is free
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(pempty_bar(p));
+                        }
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            acc[j + q] = fmaf(__uint_as_float(f[q]) * w, __uint_as_float(v[q]), acc[j + q]);
+                        for (int q = 0; q < kCols; q += 4) {
+                            float w[4];
+                            if constexpr (TOK_LANES) {
+                                w[0] = w[1] = w[2] = w[3] = f[j];
+                            } else {
+                                const uint4 u = lds128(factors + (g * NT + at + q) * 4);
+                                w[0] = __uint_as_float(u.x), w[1] = __uint_as_float(u.y);
+                                w[2] = __uint_as_float(u.z), w[3] = __uint_as_float(u.w);
+                            }
+                            fma_pair(acc[at + q], acc[at + q + 1], w[0], w[1], now[q], now[q + 1]);
+                            fma_pair(acc[at + q + 2], acc[at + q + 3], w[2], w[3], now[q + 2], now[q + 3]);
+                        }
                     }
-                }
-                w = w_next;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(pempty_bar(p));
-                    mbar_arrive(empty_bar(st));
+                    if (++p == C::kPBufs) { p = 0; phase ^= 1; }
                 }
             }
             if (!ok) break;
             if (a.split > 1) continue;               // (one tile per cluster: the loop ends here)
             if constexpr (TOK_LANES) {
-                if (l0 + r < a.M) {
 #pragma unroll
-                    for (int j = 0; j < C::kNC; j += 8) store_row8(a, l0 + r, c0 + col0 + j, acc + j);
-                }
-            } else if (l0 + r < a.N) {
-#pragma unroll
-                for (int j = 0; j < C::kNC; ++j)
-                    if (c0 + col0 + j < a.M) store_y(a.y, (c0 + col0 + j) * a.ldy + l0 + r, acc[j], a.dtype);
+                for (int j = 0; j < C::kNC; j += 16)
+                    store_rows16(a, buf, lane, l0 + 32 * quarter, c0 + col0 + j, acc + j);
+            } else {
+                store_cols<C::kNC>(a, c0 + col0, l0 + r, acc);
             }
         }
         if (a.split > 1) {
-            // This CTA's part, [column][lane], over the ring: its MMAs and with them its copies are done,
-            // and after the barrier no fold warp reads scales from it. (Of a CTA that gave up the parts
-            // are undefined, as its outputs are; its copies still land in its own shared memory.)
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kFW) : "memory");
+            // This CTA's part, [column][lane], over the ring: its MMAs and with them its copies are done. (Of
+            // a CTA that gave up the parts are undefined, as its outputs are; its copies still land in its
+            // own shared memory.)
 #pragma unroll
             for (int j = 0; j < C::kNC; ++j)
                 asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_ring + ((col0 + j) * kBmLanes + r) * 4), "f"(acc[j])
@@ -335,38 +460,41 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
             const int t = blockIdx.x / a.split;      // (one tile per cluster)
             const int l0 = t % a.lane_tiles * kBmLanes, c0 = t / a.lane_tiles * NT;
             const int r = 32 * (warp & 3) + lane;
-            // eight columns at a time, dealt out over the ranks and their warps
-            for (int j = (rank * C::kParts + ((warp - 4) >> 2)) * 8; j < NT; j += a.split * C::kParts * 8) {
-                float v[8];
+            // sixteen columns at a time, dealt out over the ranks and their warps
+            for (int j = (rank * C::kParts + ((warp - 4) >> 2)) * 16; j < NT; j += a.split * C::kParts * 16) {
+                float v[16];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = 0.f;
+                for (int q = 0; q < 16; ++q) v[q] = 0.f;
                 for (int o = 0; o < a.split; ++o) {
                     const uint32_t base = map_to_rank(s_ring, o);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] += ld_cluster_f32(base + ((j + q) * kBmLanes + r) * 4);
+                    for (int q = 0; q < 16; ++q) v[q] += ld_cluster_f32(base + ((j + q) * kBmLanes + r) * 4);
                 }
                 if constexpr (TOK_LANES) {
-                    if (l0 + r < a.M) store_row8(a, l0 + r, c0 + j, v);
-                } else if (l0 + r < a.N) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (c0 + j + q < a.M) store_y(a.y, (c0 + j + q) * a.ldy + l0 + r, v[q], a.dtype);
+                    store_rows16(a, s_warp + (warp - 4) * C::kWarpBytes, lane, l0 + r - lane, c0 + j, v);
+                } else {
+                    store_cols<16>(a, c0 + j, l0 + r, v);
                 }
             }
         }
         __syncwarp();
         cluster_sync();                              // no CTA leaves while another reads its part
     }
+    if ((warp == 0 || warp == 2) && lane == 0) issued_by[warp >> 1] = issued;
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
-    // a CTA that gave up lets every copy in flight land before it goes
-    if (warp == 0 && lane == 0 && *abort_flag)
-        for (int j = issued > C::kStages ? issued - C::kStages : 0; j < issued; ++j)
+    // A CTA that gave up lets every copy in flight land before it goes. Where one copy thread stopped ahead
+    // of the other, its arrivals are made up for first, so that the other's stages complete.
+    if (warp == 0 && lane == 0 && *abort_flag) {
+        const int less = min(issued_by[0], issued_by[1]), more = max(issued_by[0], issued_by[1]);
+        for (int j = less; j < more; ++j) mbar_arrive(full_bar(j % C::kStages));
+        for (int j = more > C::kStages ? more - C::kStages : 0; j < more; ++j)
             mbar_wait_plain(full_bar(j % C::kStages), (j / C::kStages) & 1, drain_limit(a.timeout_cycles));
+    }
 }
 
 bool encode_2d(EncodeTiledFn fn, CUtensorMap* map, CUtensorMapDataType type, const void* p, long long inner,
@@ -381,8 +509,7 @@ bool encode_2d(EncodeTiledFn fn, CUtensorMap* map, CUtensorMapDataType type, con
 
 struct BmCall {
     const void *X, *W;
-    const float* sx;
-    long long ldx, ldw, ldsx;
+    long long ldx, ldw;
     int K;
 };
 
@@ -404,9 +531,7 @@ int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) 
     const auto sw128 = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap *xmap = TOK_LANES ? &a.lane_map : &a.col_map, *wmap = TOK_LANES ? &a.col_map : &a.lane_map;
     if (!encode_2d(rt.encode, xmap, u8, c.X, c.K, a.M, c.ldx, kBmBlock, C::kTokens, sw128) ||
-        !encode_2d(rt.encode, wmap, u8, c.W, c.K, a.N, c.ldw, kBmBlock, TOK_LANES ? NT : kBmLanes, sw128) ||
-        !encode_2d(rt.encode, &a.sx_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, c.sx, a.M, a.kb, c.ldsx * 4, C::kTokens, 1,
-                   CU_TENSOR_MAP_SWIZZLE_NONE))
+        !encode_2d(rt.encode, wmap, u8, c.W, c.K, a.N, c.ldw, kBmBlock, TOK_LANES ? NT : kBmLanes, sw128))
         return WQ4_ERR_CUDA;
     const int lanes = TOK_LANES ? a.M : a.N, cols = TOK_LANES ? a.N : a.M;
     a.lane_tiles = (lanes + kBmLanes - 1) / kBmLanes;
@@ -445,9 +570,11 @@ extern "C" int wq4_block_mm(const void* X, long long ldx, const float* x_scales,
     if (ldx >= (1LL << 40) || ldw >= (1LL << 40) || ldsx >= (1LL << 38)) return WQ4_ERR_UNSUPPORTED;
     Runtime rt;
     if (const int rc = runtime(&rt)) return rc;
-    const BmCall c{X, W, x_scales, ldx, ldw, ldsx, K};
+    const BmCall c{X, W, ldx, ldw, K};
     BmArgs a{};
+    a.sx = x_scales;
     a.sw = w_scales;
+    a.ldsx = ldsx;
     a.y = Y;
     a.ldy = ldy;
     a.ldsw = ldsw;
@@ -455,7 +582,9 @@ extern "C" int wq4_block_mm(const void* X, long long ldx, const float* x_scales,
     a.N = N;
     a.kb = kb;
     a.dtype = dtype;
-    a.vec_store = aligned_to(Y, 16) && ldy * size % 16 == 0;
+    a.unit = 16;
+    while (a.unit > size && !(aligned_to(Y, a.unit) && ldy * size % a.unit == 0)) a.unit /= 2;
+    if (dtype == WQ4_FP32 && a.unit == 8) a.unit = 4;
     a.status = rt.status;
     a.timeout_cycles = rt.timeout_cycles;
     a.test_stall = rt.test_stall;
