@@ -21,8 +21,7 @@
 //                MMAs (K = 32) a block, then a commit to the fold warps. One thread issues an MMA in
 //                46 cycles and needs some 75 for each wait and commit besides, so that its own step of
 //                narrow MMAs takes longer than the tensor core does; two overlap.
-//   warps 4+     fold: read P_b, add it in, at a tile's end round once and store. They load the
-//                scales themselves, a few blocks ahead.
+//   warps 4+     fold: read P_b, add it in, at a tile's end round once and store
 // With fewer tiles than SMs, a cluster of CTAs shares each tile, cut along K; the parts are added in
 // rank order through distributed shared memory.
 //
@@ -42,10 +41,10 @@ namespace {
 constexpr int kBmBlock = 128;                  // K elements (bytes) of a block
 constexpr int kBmLanes = 128;                  // rows of the lane operand per tile
 constexpr int kBmMaxSmem = 232448;
-constexpr int kAhead = 4;                      // blocks whose scales are loaded together, one such group ahead
 
 struct BmArgs {
     CUtensorMap lane_map, col_map;             // e4m3 codes [rows][K], box 128 K x tile rows
+    CUtensorMap sx_map;                        // tokens on the lanes: token scales [blocks][M], box 128 tokens x 8 blocks
     const float *sx, *sw;                      // token scales, row b, column m; weight scales, row n / 128, column b
     void* y;
     long long ldsx, ldsw, ldy;
@@ -59,16 +58,19 @@ struct BmArgs {
     int test_stall;
 };
 
-// NT: columns of a tile; TOK_LANES: tokens on the lanes (else weight rows).
-template <int NT, bool TOK_LANES>
+// NT: columns of a tile; TOK_LANES: tokens on the lanes (else weight rows); PAIR: two CTAs of a cluster
+// share each tile of 256 lanes, 128 lanes and half the columns' copies each (cta_group::2).
+template <int NT, bool TOK_LANES, bool PAIR>
 struct BmCfg {
     static constexpr int kG = TOK_LANES ? 1 : 2;                // blocks of K per step of the pipeline
+    static constexpr int kAhead = 2 * kG;                       // blocks whose scales are loaded together, one such group ahead
     static constexpr int kFW = TOK_LANES ? 8 : 4;               // fold warps
     static constexpr int kParts = kFW / 4;                      // fold warps per lane quarter
     static constexpr int kNC = NT / kParts;                     // columns of a fold thread
     static constexpr int kThreads = 128 + 32 * kFW;
     static constexpr int kLaneBytes = kBmLanes * kBmBlock;
-    static constexpr int kColBytes = NT * kBmBlock;
+    static constexpr int kColRows = PAIR ? NT / 2 : NT;         // rows of the column operand a CTA copies
+    static constexpr int kColBytes = kColRows * kBmBlock;
     static constexpr int kTokens = TOK_LANES ? kBmLanes : NT;
     static constexpr int kBlockBytes = kLaneBytes + kColBytes;
     static constexpr int kStageBytes = kG * kBlockBytes;
@@ -76,14 +78,16 @@ struct BmCfg {
     // per fold warp: rows of an output chunk on their way to coalesced stores, 32 of 64 + 16 bytes (tokens on
     // the lanes), or the factors of a step's tokens, twice
     static constexpr int kWarpBytes = TOK_LANES ? 32 * 80 : 2 * kG * NT * 4;
+    // tokens on the lanes: the tokens' scales of 8 blocks at a time come as one copy, in a ring of their own
+    static constexpr int kScBlocks = 8, kScRing = TOK_LANES ? 3 : 0, kScBytes = kScBlocks * kBmLanes * 4;
     // An even number of stages and of P buffers: the MMA warps take alternate steps, so each walks every
     // phase of its own ones (a parity wait is unambiguous one phase ahead only).
-    static constexpr int kFit = (kBmMaxSmem - 1024 - kBarBytes - kFW * kWarpBytes) / kStageBytes;
+    static constexpr int kFit = (kBmMaxSmem - 1024 - kBarBytes - kScRing * kScBytes - kFW * kWarpBytes) / kStageBytes;
     static constexpr int kStages = (kFit > 12 ? 12 : kFit) & ~1;
     static constexpr int kPCols = kG * NT;                      // tensor-memory columns of a step's P buffer
     static constexpr int kPBufs = kPCols <= 128 ? 4 : 2;
-    static constexpr int kTmemCols = kPCols * kPBufs;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + kFW * kWarpBytes;
+    static constexpr int kTmemCols = kPCols * kPBufs > 256 ? 512 : kPCols * kPBufs;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kScRing * kScBytes + kBarBytes + kFW * kWarpBytes;
     // 128 fp32 accumulators per fold thread want more registers than an even share: 384 threads
     // launched with 168 each (64512 in all), of which the copy and MMA warps keep 56 and the fold
     // warps take 224 (128 x 56 + 256 x 224 = 64512).
@@ -92,16 +96,91 @@ struct BmCfg {
     static_assert(!kRegSplit || 128 * kRegWg0 + 32 * kFW * kRegFold <= kThreads * kLaunchRegs, "register split");
     static_assert(kStages >= 4 && kTmemCols <= 512 && kSmemBytes <= kBmMaxSmem, "tile");
     static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kAhead % kG == 0, "tensor memory, steps");
-    static_assert(kStages * kStageBytes >= kBmLanes * NT * 4, "cluster reduction buffer");
+    static_assert(PAIR || kStages * kStageBytes >= kBmLanes * NT * 4, "cluster reduction buffer");
+    static_assert(!PAIR || (TOK_LANES && kPBufs == 2), "pairs");
 };
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
+    if constexpr (PAIR) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    }
+}
+
+// The instructions of wq4_device.cuh as a pair of CTAs uses them: both allocate and free, a commit
+// arrives on the barrier of that offset in each, and a barrier of the leader's (rank 0) takes arrivals
+// from both.
+template <bool PAIR>
+__device__ __forceinline__ void bm_tmem_alloc(uint32_t dst, uint32_t cols) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(dst, cols);
+        tmem_relinquish();
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void bm_tmem_dealloc(uint32_t taddr, uint32_t cols) {
+    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+    else tmem_dealloc(taddr, cols);
+}
+template <bool PAIR>
+__device__ __forceinline__ void bm_commit(uint32_t bar) {
+    if constexpr (PAIR) {
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    } else {
+        mma_commit(bar);
+    }
+}
+__device__ __forceinline__ void mbar_arrive_leader(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, 0)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {   // (does not wait)
+    uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
         : "memory");
+    return ok != 0;
+}
+// mbar_wait of wq4_device.cuh for a barrier with arrivals from the other CTA of the pair.
+__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, const WaitCtl& ctl) {
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (*ctl.abort_flag) return false;
+        if (clock64() - t0 > ctl.limit) {
+            *ctl.abort_flag = 1;
+            atomicOr(ctl.status, kStatusTimeout);
+            return false;
+        }
+    }
 }
 
 // kind::f8f6f4: D fp32, A and B e4m3 (format code 0), both K-major, M x N.
@@ -118,6 +197,12 @@ __device__ __forceinline__ void fma_pair(float& d0, float& d1, float f0, float f
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(f), "l"(v));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
 }
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int dtype) {
@@ -147,11 +232,11 @@ __device__ __forceinline__ void copy_unit(void* to, uint32_t from) {
     }
 }
 
-// The 32 rows of 16 columns in `buf` (80 bytes a row) to rows m0.. of Y, columns n..: runs of a row
+// The 32 rows of CNT columns in `buf` (80 bytes a row) to rows m0.. of Y, columns n..: runs of a row
 // by neighbouring lanes, UNIT bytes each (what the rows of Y start on), SIZE bytes a value.
-template <int SIZE, int UNIT>
-__device__ __forceinline__ void copy_rows16(const BmArgs& a, uint32_t buf, int lane, int m0, int n) {
-    constexpr int kPerRow = 16 * SIZE / UNIT, kRows = 32 / kPerRow, kIn = UNIT / SIZE;
+template <int SIZE, int UNIT, int CNT>
+__device__ __forceinline__ void copy_rows(const BmArgs& a, uint32_t buf, int lane, int m0, int n) {
+    constexpr int kPerRow = CNT * SIZE / UNIT, kRows = 32 / kPerRow, kIn = UNIT / SIZE;
     const int c = lane % kPerRow * kIn, r0 = lane / kPerRow;
     const int cols = a.N - n - c, rows = a.M - m0;   // what exists from here on
     uint8_t* to = static_cast<uint8_t*>(a.y) + ((m0 + r0) * a.ldy + n + c) * SIZE;
@@ -168,30 +253,39 @@ __device__ __forceinline__ void copy_rows16(const BmArgs& a, uint32_t buf, int l
     }
 }
 
-// A warp's 32 rows from m0, one per lane, 16 columns from n, through `buf` in shared memory: stored by
+// A warp's 32 rows from m0, one per lane, CNT columns from n, through `buf` in shared memory: stored by
 // their lanes directly, rows would touch 32 lines with every instruction.
-__device__ __forceinline__ void store_rows16(const BmArgs& a, uint32_t buf, int lane, int m0, int n, const float* v) {
+template <int CNT>
+__device__ __forceinline__ void store_rows(const BmArgs& a, uint32_t buf, int lane, int m0, int n, const float* v) {
     const uint32_t mine = buf + lane * 80;
+    constexpr int kChunk = CNT < 32 ? CNT : 32;       // 16-bit columns that go through `buf` together
     if (a.dtype == WQ4_FP32) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4)
-            sts128(mine + 4 * j, __float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
-                   __float_as_uint(v[j + 3]));
-        __syncwarp();
-        if (a.unit == 16) copy_rows16<4, 16>(a, buf, lane, m0, n);
-        else copy_rows16<4, 4>(a, buf, lane, m0, n);
+        for (int c = 0; c < CNT; c += 16) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                sts128(mine + 4 * j, __float_as_uint(v[c + j]), __float_as_uint(v[c + j + 1]),
+                       __float_as_uint(v[c + j + 2]), __float_as_uint(v[c + j + 3]));
+            __syncwarp();
+            if (a.unit == 16) copy_rows<4, 16, 16>(a, buf, lane, m0, n + c);
+            else copy_rows<4, 4, 16>(a, buf, lane, m0, n + c);
+            __syncwarp();
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < 16; j += 8)
-            sts128(mine + 2 * j, pack16(v[j], v[j + 1], a.dtype), pack16(v[j + 2], v[j + 3], a.dtype),
-                   pack16(v[j + 4], v[j + 5], a.dtype), pack16(v[j + 6], v[j + 7], a.dtype));
-        __syncwarp();
-        if (a.unit == 16) copy_rows16<2, 16>(a, buf, lane, m0, n);
-        else if (a.unit == 8) copy_rows16<2, 8>(a, buf, lane, m0, n);
-        else if (a.unit == 4) copy_rows16<2, 4>(a, buf, lane, m0, n);
-        else copy_rows16<2, 2>(a, buf, lane, m0, n);
+        for (int c = 0; c < CNT; c += kChunk) {
+#pragma unroll
+            for (int j = 0; j < kChunk; j += 8)
+                sts128(mine + 2 * j, pack16(v[c + j], v[c + j + 1], a.dtype), pack16(v[c + j + 2], v[c + j + 3], a.dtype),
+                       pack16(v[c + j + 4], v[c + j + 5], a.dtype), pack16(v[c + j + 6], v[c + j + 7], a.dtype));
+            __syncwarp();
+            if (a.unit == 16) copy_rows<2, 16, kChunk>(a, buf, lane, m0, n + c);
+            else if (a.unit == 8) copy_rows<2, 8, kChunk>(a, buf, lane, m0, n + c);
+            else if (a.unit == 4) copy_rows<2, 4, kChunk>(a, buf, lane, m0, n + c);
+            else copy_rows<2, 2, kChunk>(a, buf, lane, m0, n + c);
+            __syncwarp();
+        }
     }
-    __syncwarp();
 }
 
 // One column n of Y per lane, CNT tokens from m: neighbouring lanes' columns are neighbours in memory.
@@ -216,7 +310,14 @@ __device__ __forceinline__ void store_cols(const BmArgs& a, int m, int n, const 
 // The tiles of one CTA, in order, and the part of K it takes of each.
 struct BmSched {
     int t, step, kb0, kb1;
-    __device__ BmSched(const BmArgs& a, int rank) {
+    __device__ BmSched(const BmArgs& a, int rank, bool pair) {
+        if (pair) {
+            t = blockIdx.x / 2;
+            step = gridDim.x / 2;
+            kb0 = 0;
+            kb1 = a.kb;
+            return;
+        }
         t = blockIdx.x / a.split;
         step = gridDim.x / a.split;
         kb0 = static_cast<int>(static_cast<long long>(a.kb) * rank / a.split);
@@ -224,34 +325,44 @@ struct BmSched {
     }
 };
 
-template <int NT, bool TOK_LANES>
-__global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_kernel(const __grid_constant__ BmArgs a) {
-    using C = BmCfg<NT, TOK_LANES>;
+template <int NT, bool TOK_LANES, bool PAIR>
+__global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
+    block_mm_kernel(const __grid_constant__ BmArgs a) {
+    using C = BmCfg<NT, TOK_LANES, PAIR>;
+    constexpr int kTileLanes = PAIR ? 2 * kBmLanes : kBmLanes, kAhead = C::kAhead;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t s_ring = (raw_s + 1023u) & ~1023u;
-    const uint32_t s_bar = s_ring + C::kStages * C::kStageBytes;
+    const uint32_t s_sc = s_ring + C::kStages * C::kStageBytes;      // token scales
+    const uint32_t s_bar = s_sc + C::kScRing * C::kScBytes;
     auto full_bar = [&](int s) { return s_bar + 8u * s; };
     auto empty_bar = [&](int s) { return s_bar + 8u * (16 + s); };
     const uint32_t s_warp = s_bar + C::kBarBytes;    // the fold warps' buffers
     auto pfull_bar = [&](int b) { return s_bar + 8u * (32 + b); };
     auto pempty_bar = [&](int b) { return s_bar + 8u * (36 + b); };
-    const uint32_t drain_bar = s_bar + 8u * 40, stall_bar = s_bar + 8u * 41;
-    uint8_t* const gmisc = smem_raw + (s_bar - raw_s) + 8 * 48;
+    auto scfull_bar = [&](int c) { return s_bar + 8u * (40 + c); };
+    auto scempty_bar = [&](int c) { return s_bar + 8u * (44 + c); };
+    const uint32_t drain_bar = s_bar + 8u * 48, stall_bar = s_bar + 8u * 49;
+    uint8_t* const gmisc = smem_raw + (s_bar - raw_s) + 8 * 56;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gmisc);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(gmisc + 4);
     volatile int* const issued_by = reinterpret_cast<volatile int*>(gmisc + 8);   // stages the two copy threads filled
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int rank = PAIR || a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int lane0 = PAIR ? rank * kBmLanes : 0;    // this CTA's first lane of a tile
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(full_bar(s), 2);               // both operands' copies
+            mbar_init(full_bar(s), PAIR && rank == 0 ? 3 : 2);   // both operands' copies (and the other CTA's)
             mbar_init(empty_bar(s), 1);
         }
         for (int b = 0; b < C::kPBufs; ++b) {
             mbar_init(pfull_bar(b), 1);
-            mbar_init(pempty_bar(b), C::kFW);
+            mbar_init(pempty_bar(b), PAIR ? 2 * C::kFW : C::kFW);
+        }
+        for (int c = 0; c < C::kScRing; ++c) {
+            mbar_init(scfull_bar(c), 1);
+            mbar_init(scempty_bar(c), C::kFW);
         }
         mbar_init(drain_bar, 2);                     // one commit from each MMA warp
         mbar_init(stall_bar, 1);
@@ -259,19 +370,24 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
         fence_mbar_init();
         prefetch_tensormap(&a.lane_map);
         prefetch_tensormap(&a.col_map);
+        if constexpr (TOK_LANES) prefetch_tensormap(&a.sx_map);
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
-        tmem_relinquish();
+        bm_tmem_alloc<PAIR>(smem_u32(tmem_slot), C::kTmemCols);
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR) {
+        __syncwarp();
+        cluster_sync();                              // (the other CTA's barriers are set up too)
+    } else {
+        __syncthreads();
+    }
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const WaitCtl ctl{abort_flag, a.status, a.timeout_cycles};
-    int issued = 0;                                  // stages a copy thread has filled
+    int issued = 0, sc_issued = 0;                   // stages a copy thread has filled, scale copies
 
     if (warp < 4) {
         if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegWg0));
@@ -283,11 +399,20 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
                 const CUtensorMap* map = lanes ? &a.lane_map : &a.col_map;
                 const uint32_t dst = s_ring + (lanes ? 0 : C::kLaneBytes), bytes = lanes ? C::kLaneBytes : C::kColBytes;
                 bool ok = true;
-                int st = 0, i = 0;
-                uint32_t phase = 1;
-                for (BmSched s(a, rank); s.t < a.tiles && ok; s.t += s.step) {
-                    const int row = lanes ? s.t % a.lane_tiles * kBmLanes : s.t / a.lane_tiles * NT;
+                int st = 0, i = 0, sc = 0;
+                uint32_t phase = 1, sc_phase = 1;
+                for (BmSched s(a, rank, PAIR); s.t < a.tiles && ok; s.t += s.step) {
+                    const int row = lanes ? s.t % a.lane_tiles * kTileLanes + lane0
+                                          : s.t / a.lane_tiles * NT + (PAIR ? rank * C::kColRows : 0);
                     for (int b = s.kb0; b < s.kb1; b += C::kG, ++i) {
+                        if (TOK_LANES && warp == 2 && (b - s.kb0) % C::kScBlocks == 0) {
+                            if (!mbar_wait(scempty_bar(sc), sc_phase, ctl)) { ok = false; break; }
+                            mbar_arrive_expect_tx(scfull_bar(sc), C::kScBytes);
+                            tma_load_2d(s_sc + sc * C::kScBytes, &a.sx_map, scfull_bar(sc),
+                                        s.t % a.lane_tiles * kTileLanes + lane0, b, policy_evict_last());
+                            ++sc_issued;
+                            if (++sc == C::kScRing) { sc = 0; sc_phase ^= 1; }
+                        }
                         if (!mbar_wait(empty_bar(st), phase, ctl)) { ok = false; break; }
                         const int n = min(C::kG, s.kb1 - b);
                         mbar_arrive_expect_tx(full_bar(st), n * bytes);
@@ -302,19 +427,37 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
                 issued = i;
             }
             __syncwarp();
+        } else if (PAIR && rank != 0) {
+            // The leader's MMAs read both CTAs' stages: warp 1 tells it of this one's.
+            if (warp == 1 && lane == 0) {
+                int st = 0;
+                uint32_t full = 0;
+                bool ok = true;
+                for (BmSched s(a, rank, PAIR); s.t < a.tiles && ok; s.t += s.step) {
+                    for (int b = s.kb0; b < s.kb1; ++b) {
+                        if (!mbar_wait(full_bar(st), full, ctl)) { ok = false; break; }
+                        mbar_arrive_leader(full_bar(st));
+                        if (++st == C::kStages) { st = 0; full ^= 1; }
+                    }
+                }
+            }
+            __syncwarp();
         } else {
             if (lane == 0) {
-                constexpr uint32_t idesc = f8_idesc(kBmLanes, NT);
+                constexpr uint32_t idesc = f8_idesc(kTileLanes, NT);
+                auto wait = [&](uint32_t bar, uint32_t parity) {
+                    return PAIR ? mbar_wait_pair(bar, parity, ctl) : mbar_wait(bar, parity, ctl);
+                };
                 const int mine = warp >> 1;          // this thread's steps: the even or the odd ones
                 bool ok = !(a.test_stall && mine == 0) || mbar_wait(stall_bar, 0, ctl);
                 const uint64_t desc0 = make_sdesc_sw128(s_ring);
                 int st = mine, p = mine, skip = mine;
                 uint32_t full = 0, free = 1;         // phase parities
-                for (BmSched s(a, rank); s.t < a.tiles && ok; s.t += s.step) {
+                for (BmSched s(a, rank, PAIR); s.t < a.tiles && ok; s.t += s.step) {
                     int b = s.kb0 + skip * C::kG;
                     for (; b < s.kb1; b += 2 * C::kG) {
-                        if (!mbar_wait(full_bar(st), full, ctl)) { ok = false; break; }
-                        if (!mbar_wait(pempty_bar(p), free, ctl)) { ok = false; break; }
+                        if (!wait(full_bar(st), full)) { ok = false; break; }
+                        if (!wait(pempty_bar(p), free)) { ok = false; break; }
                         tc_fence_after();
                         const uint64_t desc = desc0 + static_cast<uint32_t>(st * (C::kStageBytes >> 4));
                         const uint32_t d = tmem + p * C::kPCols;
@@ -323,17 +466,17 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
                             if (b + g >= s.kb1) break;
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_f8(d + g * NT, desc + (g * (C::kBlockBytes >> 4) + 2 * k),
+                                mma_f8<PAIR>(d + g * NT, desc + (g * (C::kBlockBytes >> 4) + 2 * k),
                                        desc + (g * (C::kBlockBytes >> 4) + (C::kLaneBytes >> 4) + 2 * k), idesc, k > 0);
                         }
-                        mma_commit(pfull_bar(p));
-                        mma_commit(empty_bar(st));
+                        bm_commit<PAIR>(pfull_bar(p));
+                        bm_commit<PAIR>(empty_bar(st));
                         if ((st += 2) >= C::kStages) { st = mine; full ^= 1; }
                         if ((p += 2) >= C::kPBufs) { p = mine; free ^= 1; }
                     }
                     skip = (b - s.kb1) / C::kG;      // (the turns go on over the tiles' ends)
                 }
-                mma_commit(drain_bar);               // every MMA is done before the tensor memory goes
+                bm_commit<PAIR>(drain_bar);               // every MMA is done before the tensor memory goes
                 mbar_wait_plain(drain_bar, 0, drain_limit(a.timeout_cycles));
             }
             __syncwarp();
@@ -348,45 +491,98 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
         const uint32_t buf = s_warp + (warp - 4) * C::kWarpBytes;
         const int sw_rows = (a.N + 127) / 128;
         bool ok = true;
-        int p = 0;
-        uint32_t phase = 0;
-        for (BmSched s(a, rank); s.t < a.tiles && ok; s.t += s.step) {
-            const int l0 = s.t % a.lane_tiles * kBmLanes, c0 = s.t / a.lane_tiles * NT;
+        int p = 0, sc = 0;
+        uint32_t phase = 0, sc_phase = 0;
+        for (BmSched s(a, rank, PAIR); s.t < a.tiles && ok; s.t += s.step) {
+            const int l0 = s.t % a.lane_tiles * kTileLanes + lane0, c0 = s.t / a.lane_tiles * NT;
             const float* sw = a.sw + min((TOK_LANES ? c0 + col0 : l0) / 128, sw_rows - 1) * a.ldsw;
-            // The tokens whose scales this thread loads (none past the last token: such values are not stored),
-            // and the scales of the kAhead blocks from `b` on; they are multiplied only when their turn
-            // comes, so that nothing waits for a load just issued.
-            constexpr int kPer = TOK_LANES ? 1 : (NT + 31) / 32;     // tokens per lane
-            const int token = TOK_LANES ? l0 + r : c0 + lane;
-            const bool loads = token < a.M && (TOK_LANES || lane < NT);
-            const bool loads2 = kPer > 1 && token + 32 < a.M;
-            float nsx[kAhead * kPer], nsw[kAhead];
-            auto load_scales = [&](int b) {
-                const float* x = a.sx + token + b * a.ldsx;
+            if constexpr (TOK_LANES) {
+                // A token per thread: its factor of a block is its scale (from the ring; 0 past the last token)
+                // times the weight's, of which the warp's lanes load 32 blocks at a time. While one piece of P is added
+                // in, the next is read.
+                constexpr int kCols = 16, kPieces = C::kNC / kCols;
+                const int nb = s.kb1 - s.kb0;
+                float w32 = lane < nb ? __ldg(sw + s.kb0 + lane) : 0.f;
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j, x += a.ldsx) {
-                    const bool in = b + j < s.kb1;
-                    nsw[j] = in ? __ldg(sw + b + j) : 0.f;
-                    nsx[j * kPer] = in && loads ? __ldg(x) : 0.f;
-                    if constexpr (kPer > 1) nsx[j * kPer + 1] = in && loads2 ? __ldg(x + 32) : 0.f;
+                for (int j = 0; j < C::kNC; ++j) acc[j] = 0.f;
+                uint32_t v[2][kCols];
+#pragma unroll 1
+                for (int b = 0; b < nb; ++b) {
+                    if (b % C::kScBlocks == 0) {
+                        if (b % 32 == 0 && b) w32 = b + lane < nb ? __ldg(sw + s.kb0 + b + lane) : 0.f;
+                        if (!mbar_wait(scfull_bar(sc), sc_phase, ctl)) { ok = false; break; }
+                    }
+                    const float f = lds_f32(s_sc + sc * C::kScBytes + (b % C::kScBlocks) * (kBmLanes * 4) + 4 * r) *
+                                    __shfl_sync(0xffffffffu, w32, b % 32);
+                    const uint32_t from = t_addr + p * C::kPCols, freed = pempty_bar(p);
+                    if (!mbar_wait(pfull_bar(p), phase, ctl)) { ok = false; break; }
+                    tc_fence_after();
+                    tmem_ldn(from, v[0]);
+                    if (++p == C::kPBufs) { p = 0; phase ^= 1; }
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c) {
+                        tmem_ld_wait();
+                        if (c + 1 < kPieces) {
+                            tmem_ldn(from + (c + 1) * kCols, v[(c + 1) & 1]);
+                        } else {                     // all of the block's P is in registers: the buffer is free
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if constexpr (PAIR) mbar_arrive_leader(freed);
+                                else mbar_arrive(freed);
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < kCols; q += 2)
+                            fma_pair(acc[c * kCols + q], acc[c * kCols + q + 1], f, f, v[c & 1][q], v[c & 1][q + 1]);
+                    }
+                    if (b % C::kScBlocks == C::kScBlocks - 1 || b + 1 == nb) {
+                        __syncwarp();                // (every lane has its last factor)
+                        if (lane == 0) mbar_arrive(scempty_bar(sc));
+                        if (++sc == C::kScRing) { sc = 0; sc_phase ^= 1; }
+                    }
                 }
-            };
+            } else {
+                // The tokens whose scales this thread loads (none past the last token: such values are not stored),
+                // and the scales of the kAhead blocks from `b` on; they are multiplied only when their turn
+                // comes, so that nothing waits for a load just issued.
+                constexpr int kCols = NT < 32 ? 16 : 32, kPieces = C::kNC / kCols;   // pieces of a block's P per thread
+                constexpr int kPer = (NT + 31) / 32;     // tokens per lane
+                const int token = c0 + lane;
+                const bool loads = token < a.M && lane < NT;
+                const bool loads2 = kPer > 1 && token + 32 < a.M;
+                float nsx[kAhead * kPer], nsw[kAhead];
+                const float *px = a.sx + token + s.kb0 * a.ldsx, *pw = sw + s.kb0;
 #pragma unroll
-            for (int j = 0; j < C::kNC; ++j) acc[j] = 0.f;
-            load_scales(s.kb0);
-            __syncwarp();                            // (no lane still reads the last tile's factors)
-            for (int b0 = s.kb0; b0 < s.kb1 && ok; b0 += kAhead) {
-                float f[kAhead * kPer];
+                for (int j = 0; j < kAhead * kPer; ++j) nsx[j] = 0.f;
+                auto load_scales = [&](int n) {          // of the next n blocks (kAhead at most)
 #pragma unroll
-                for (int j = 0; j < kAhead * kPer; ++j) f[j] = nsx[j] * nsw[j / kPer];
-                load_scales(b0 + kAhead);
+                    for (int j = 0; j < kAhead; ++j, px += a.ldsx) {
+                        if (j >= n) break;
+                        nsw[j] = __ldg(pw + j);
+                        if (loads) nsx[j * kPer] = __ldg(px);
+                        if constexpr (kPer > 1)
+                            if (loads2) nsx[j * kPer + 1] = __ldg(px + 32);
+                    }
+                    pw += kAhead;
+                };
 #pragma unroll
-                for (int j = 0; j < kAhead; j += C::kG) {
-                    if (b0 + j >= s.kb1) break;
-                    const uint32_t factors = buf + (j / C::kG & 1) * (C::kG * NT * 4);
-                    if (!TOK_LANES) {                // the step's factors, where every lane can read them
+                for (int j = 0; j < C::kNC; ++j) acc[j] = 0.f;
+                load_scales(s.kb1 - s.kb0);
+                uint32_t v[2][kCols];
+                bool primed = false;                     // the step's first piece of P is on its way
+                __syncwarp();                            // (no lane still reads the last tile's factors)
+                for (int b0 = s.kb0; b0 < s.kb1 && ok; b0 += kAhead) {
+                    float f[kAhead * kPer];
 #pragma unroll
-                        for (int g = 0; g < C::kG; ++g)
+                    for (int j = 0; j < kAhead * kPer; ++j) f[j] = nsx[j] * nsw[j / kPer];
+                    load_scales(s.kb1 - b0 - kAhead);
+#pragma unroll
+                    for (int j = 0; j < kAhead; j += C::kG) {
+                        if (b0 + j >= s.kb1) break;
+                        const uint32_t factors = buf + (j / C::kG & 1) * (C::kG * NT * 4);
+#pragma unroll
+                        for (int g = 0; g < C::kG; ++g)  // the step's factors, where every lane can read them
 #pragma unroll
                             for (int q = 0; q < kPer; ++q)
                                 if (lane + 32 * q < NT)
@@ -394,56 +590,57 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
                                                  "f"(f[(j + g) * kPer + q])
                                                  : "memory");
                         __syncwarp();
-                    }
-                    if (!mbar_wait(pfull_bar(p), phase, ctl)) { ok = false; break; }
-                    tc_fence_after();
-                    // the step's columns of P, in pieces: the next piece is read while this one is added in. (A step's
-                    // second block past the end of K is left out: its buffer holds an earlier step's values.)
-                    constexpr int kCols = NT < 32 ? 16 : 32, kPieces = C::kNC / kCols;
-                    const int pieces = kPieces * (C::kG == 1 || b0 + j + 1 < s.kb1 ? C::kG : 1);
-                    uint32_t v[2][kCols];
-                    tmem_ldn(t_addr + p * C::kPCols, v[0]);
-#pragma unroll
-                    for (int c = 0; c < kPieces * C::kG; ++c) {
-                        if (c >= pieces) break;
-                        uint32_t(&now)[kCols] = v[c & 1];
-                        const int g = c / kPieces, at = c % kPieces * kCols;
-                        tmem_ld_wait();
-                        if (c + 1 < pieces) {
-                            tmem_ldn(t_addr + p * C::kPCols + (c + 1) / kPieces * NT + (c + 1) % kPieces * kCols, v[c + 1 & 1]);
-                        } else {                     // all of the step's P is in registers: the buffer is free
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(pempty_bar(p));
+                        // the step's columns of P, in pieces: the next piece is read while this one is added in. (A step's
+                        // second block past the end of K is left out: its buffer holds an earlier step's values.)
+                        const int pieces = kPieces * (C::kG == 1 || b0 + j + 1 < s.kb1 ? C::kG : 1);
+                        if (!primed) {
+                            if (!mbar_wait(pfull_bar(p), phase, ctl)) { ok = false; break; }
+                            tc_fence_after();
+                            tmem_ldn(t_addr + p * C::kPCols, v[0]);
                         }
+                        const int p0 = p;
+                        if (++p == C::kPBufs) { p = 0; phase ^= 1; }
+                        bool next = false;
 #pragma unroll
-                        for (int q = 0; q < kCols; q += 4) {
-                            float w[4];
-                            if constexpr (TOK_LANES) {
-                                w[0] = w[1] = w[2] = w[3] = f[j];
-                            } else {
-                                const uint4 u = lds128(factors + (g * NT + at + q) * 4);
-                                w[0] = __uint_as_float(u.x), w[1] = __uint_as_float(u.y);
-                                w[2] = __uint_as_float(u.z), w[3] = __uint_as_float(u.w);
+                        for (int c = 0; c < kPieces * C::kG; ++c) {
+                            if (c >= pieces) break;
+                            uint32_t(&now)[kCols] = v[c & 1];
+                            const int g = c / kPieces, at = c % kPieces * kCols;
+                            tmem_ld_wait();
+                            if (c + 1 < pieces) {
+                                tmem_ldn(t_addr + p0 * C::kPCols + (c + 1) / kPieces * NT + (c + 1) % kPieces * kCols, v[c + 1 & 1]);
+                            } else {                     // all of the step's P is in registers: the buffer is free
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(pempty_bar(p0));
+                                // (whether the next step is there already, asked while this piece is added in)
+                                next = c % 2 == 1 && b0 + j + C::kG < s.kb1 && mbar_test(pfull_bar(p), phase);
                             }
-                            fma_pair(acc[at + q], acc[at + q + 1], w[0], w[1], now[q], now[q + 1]);
-                            fma_pair(acc[at + q + 2], acc[at + q + 3], w[2], w[3], now[q + 2], now[q + 3]);
+#pragma unroll
+                            for (int q = 0; q < kCols; q += 4) {
+                                const uint4 u = lds128(factors + (g * NT + at + q) * 4);
+                                const float w[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+                                fma_pair(acc[at + q], acc[at + q + 1], w[0], w[1], now[q], now[q + 1]);
+                                fma_pair(acc[at + q + 2], acc[at + q + 3], w[2], w[3], now[q + 2], now[q + 3]);
+                            }
+                        }
+                        primed = __all_sync(0xffffffffu, next);
+                        if (primed) {
+                            tc_fence_after();
+                            tmem_ldn(t_addr + p * C::kPCols, v[0]);
                         }
                     }
-                    if (++p == C::kPBufs) { p = 0; phase ^= 1; }
                 }
             }
             if (!ok) break;
-            if (a.split > 1) continue;               // (one tile per cluster: the loop ends here)
+            if (!PAIR && a.split > 1) continue;               // (one tile per cluster: the loop ends here)
             if constexpr (TOK_LANES) {
-#pragma unroll
-                for (int j = 0; j < C::kNC; j += 16)
-                    store_rows16(a, buf, lane, l0 + 32 * quarter, c0 + col0 + j, acc + j);
+                store_rows<C::kNC>(a, buf, lane, l0 + 32 * quarter, c0 + col0, acc);
             } else {
                 store_cols<C::kNC>(a, c0 + col0, l0 + r, acc);
             }
         }
-        if (a.split > 1) {
+        if (!PAIR && a.split > 1) {
             // This CTA's part, [column][lane], over the ring: its MMAs and with them its copies are done. (Of
             // a CTA that gave up the parts are undefined, as its outputs are; its copies still land in its
             // own shared memory.)
@@ -453,27 +650,28 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
                              : "memory");
         }
     }
-    if (a.split > 1) {
+    if (!PAIR && a.split > 1) {
         __syncwarp();
         cluster_sync();                              // every part of the tile is in its CTA's shared memory
         if (warp >= 4) {
             const int t = blockIdx.x / a.split;      // (one tile per cluster)
             const int l0 = t % a.lane_tiles * kBmLanes, c0 = t / a.lane_tiles * NT;
             const int r = 32 * (warp & 3) + lane;
-            // sixteen columns at a time, dealt out over the ranks and their warps
-            for (int j = (rank * C::kParts + ((warp - 4) >> 2)) * 16; j < NT; j += a.split * C::kParts * 16) {
-                float v[16];
+            // a few columns at a time, dealt out over the ranks and their warps
+            constexpr int kCnt = TOK_LANES ? 16 : 8;
+            for (int j = (rank * C::kParts + ((warp - 4) >> 2)) * kCnt; j < NT; j += a.split * C::kParts * kCnt) {
+                float v[kCnt];
 #pragma unroll
-                for (int q = 0; q < 16; ++q) v[q] = 0.f;
+                for (int q = 0; q < kCnt; ++q) v[q] = 0.f;
                 for (int o = 0; o < a.split; ++o) {
                     const uint32_t base = map_to_rank(s_ring, o);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) v[q] += ld_cluster_f32(base + ((j + q) * kBmLanes + r) * 4);
+                    for (int q = 0; q < kCnt; ++q) v[q] += ld_cluster_f32(base + ((j + q) * kBmLanes + r) * 4);
                 }
                 if constexpr (TOK_LANES) {
-                    store_rows16(a, s_warp + (warp - 4) * C::kWarpBytes, lane, l0 + r - lane, c0 + j, v);
+                    store_rows<kCnt>(a, s_warp + (warp - 4) * C::kWarpBytes, lane, l0 + r - lane, c0 + j, v);
                 } else {
-                    store_cols<16>(a, c0 + j, l0 + r, v);
+                    store_cols<kCnt>(a, c0 + j, l0 + r, v);
                 }
             }
         }
@@ -482,16 +680,29 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES>::kThreads, 1) block_mm_ke
     }
     if ((warp == 0 || warp == 2) && lane == 0) issued_by[warp >> 1] = issued;
     tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR) {
+        __syncwarp();
+        cluster_sync();                              // the leader's MMAs are done, and every arrival on its barriers
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::kTmemCols);
+        bm_tmem_dealloc<PAIR>(tmem, C::kTmemCols);
+    }
+    if constexpr (TOK_LANES) {
+        if (warp == 2 && lane == 0 && *abort_flag)
+            for (int j = sc_issued > C::kScRing ? sc_issued - C::kScRing : 0; j < sc_issued; ++j)
+                mbar_wait_plain(scfull_bar(j % C::kScRing), (j / C::kScRing) & 1, drain_limit(a.timeout_cycles));
     }
     // A CTA that gave up lets every copy in flight land before it goes. Where one copy thread stopped ahead
     // of the other, its arrivals are made up for first, so that the other's stages complete.
     if (warp == 0 && lane == 0 && *abort_flag) {
         const int less = min(issued_by[0], issued_by[1]), more = max(issued_by[0], issued_by[1]);
         for (int j = less; j < more; ++j) mbar_arrive(full_bar(j % C::kStages));
+        if (PAIR && rank == 0)                       // (nor can it be told whether the other CTA's arrivals came)
+            for (int j = more > C::kStages ? more - C::kStages : 0; j < more; ++j)
+                if (!mbar_test(full_bar(j % C::kStages), (j / C::kStages) & 1)) mbar_arrive(full_bar(j % C::kStages));
         for (int j = more > C::kStages ? more - C::kStages : 0; j < more; ++j)
             mbar_wait_plain(full_bar(j % C::kStages), (j / C::kStages) & 1, drain_limit(a.timeout_cycles));
     }
@@ -513,10 +724,10 @@ struct BmCall {
     int K;
 };
 
-template <int NT, bool TOK_LANES>
+template <int NT, bool TOK_LANES, bool PAIR>
 int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) {
-    using C = BmCfg<NT, TOK_LANES>;
-    auto kern = block_mm_kernel<NT, TOK_LANES>;
+    using C = BmCfg<NT, TOK_LANES, PAIR>;
+    auto kern = block_mm_kernel<NT, TOK_LANES, PAIR>;
     static int regs = -1;                            // (one value per kernel, whoever writes it)
     if (regs < 0) {
         cudaFuncAttributes fa;
@@ -531,20 +742,24 @@ int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) 
     const auto sw128 = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap *xmap = TOK_LANES ? &a.lane_map : &a.col_map, *wmap = TOK_LANES ? &a.col_map : &a.lane_map;
     if (!encode_2d(rt.encode, xmap, u8, c.X, c.K, a.M, c.ldx, kBmBlock, C::kTokens, sw128) ||
-        !encode_2d(rt.encode, wmap, u8, c.W, c.K, a.N, c.ldw, kBmBlock, TOK_LANES ? NT : kBmLanes, sw128))
+        !encode_2d(rt.encode, wmap, u8, c.W, c.K, a.N, c.ldw, kBmBlock, TOK_LANES ? C::kColRows : kBmLanes, sw128) ||
+        (TOK_LANES && !encode_2d(rt.encode, &a.sx_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.sx, a.M, a.kb, a.ldsx * 4, kBmLanes,
+                                 C::kScBlocks, CU_TENSOR_MAP_SWIZZLE_NONE)))
         return WQ4_ERR_CUDA;
     const int lanes = TOK_LANES ? a.M : a.N, cols = TOK_LANES ? a.N : a.M;
-    a.lane_tiles = (lanes + kBmLanes - 1) / kBmLanes;
+    constexpr int kTileLanes = PAIR ? 2 * kBmLanes : kBmLanes;
+    a.lane_tiles = (lanes + kTileLanes - 1) / kTileLanes;
     const long long tiles = static_cast<long long>(a.lane_tiles) * ((cols + NT - 1) / NT);
     if (tiles > (1 << 30)) return WQ4_ERR_UNSUPPORTED;
     a.tiles = static_cast<int>(tiles);
     a.split = 1;
-    while (a.split < 8 && 2 * a.split * tiles <= rt.sm_count && 2 * a.split <= a.kb) a.split *= 2;
-    const int grid = a.split > 1 ? a.tiles * a.split : (a.tiles < rt.sm_count ? a.tiles : rt.sm_count);
+    while (!PAIR && a.split < 8 && 2 * a.split * tiles <= rt.sm_count && 2 * a.split <= a.kb) a.split *= 2;
+    const int most = PAIR ? rt.sm_count / 2 : rt.sm_count;   // tiles at a time
+    const int grid = PAIR ? 2 * (a.tiles < most ? a.tiles : most) : a.split > 1 ? a.tiles * a.split : a.tiles < most ? a.tiles : most;
     if (rt.trace)
-        std::fprintf(stderr, "wq4: block_mm M=%d N=%d K=%d lanes=%s columns=%d grid=%d split=%d\n", a.M, a.N, c.K,
-                     TOK_LANES ? "tokens" : "weights", NT, grid, a.split);
-    return launch(rt, kern, dim3(grid), C::kThreads, C::kSmemBytes, a.split, st, a);
+        std::fprintf(stderr, "wq4: block_mm M=%d N=%d K=%d lanes=%s columns=%d pair=%d grid=%d split=%d\n", a.M, a.N, c.K,
+                     TOK_LANES ? "tokens" : "weights", NT, PAIR ? 1 : 0, grid, a.split);
+    return launch(rt, kern, dim3(grid), C::kThreads, C::kSmemBytes, PAIR ? 2 : a.split, st, a);
 }
 
 }  // namespace
@@ -588,10 +803,10 @@ extern "C" int wq4_block_mm(const void* X, long long ldx, const float* x_scales,
     a.status = rt.status;
     a.timeout_cycles = rt.timeout_cycles;
     a.test_stall = rt.test_stall;
-    if (M <= 16) return go_block_mm<16, false>(rt, c, a, stream);
-    if (M <= 32) return go_block_mm<32, false>(rt, c, a, stream);
-    if (M <= 64) return go_block_mm<64, false>(rt, c, a, stream);
+    if (M <= 16) return go_block_mm<16, false, false>(rt, c, a, stream);
+    if (M <= 32) return go_block_mm<32, false, false>(rt, c, a, stream);
+    if (M <= 64) return go_block_mm<64, false, false>(rt, c, a, stream);
     const long long wide = static_cast<long long>((M + 127) / 128) * ((N + 255) / 256);
-    if (2 * wide > rt.sm_count) return go_block_mm<256, true>(rt, c, a, stream);
-    return go_block_mm<128, true>(rt, c, a, stream);
+    if (2 * wide > rt.sm_count) return go_block_mm<256, true, true>(rt, c, a, stream);
+    return go_block_mm<128, true, false>(rt, c, a, stream);
 }
