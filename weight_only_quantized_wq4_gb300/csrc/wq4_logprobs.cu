@@ -1,12 +1,19 @@
 // Log probabilities of given tokens, the entropy of each row and its most likely tokens, in one pass
 // over the logits.
 //
-// For a row x of V logits, with m = max x, d_i = x_i - m, z = sum exp(d_i), s = sum d_i exp(d_i):
-//     log p_i = d_i - log z            H = -sum p_i log p_i = log z - s / z
-// The pass keeps (m, z, s) of what a thread has seen, in fp32; when its m grows by D, z and s become
-// exp(-D) z and exp(-D) (s - D z), and parts are joined by the same rule. d is bounded below by
-// -kFar, where exp is 0, so that a logit of -inf (or of the type's lowest value) adds 0 and not
-// 0 * inf; a NaN passes the bound and makes the row NaN.
+// For a row x of V logits, with m = max x, t_i = (x_i - m) log2(e), z = sum 2^t_i, s = sum t_i 2^t_i:
+//     log p_i = x_i - m - ln z            H = -sum p_i log p_i = ln z - ln(2) s / z
+// The pass keeps (m, z, s) of what a thread has seen, in fp32; when its m grows by D / log2(e), z and s
+// become 2^-D z and 2^-D (s - D z), and parts are joined by the same rule. What limits the pass is
+// instructions per logit (at the rate of HBM an SM sees 12 bf16 logits a cycle, and has 4 issue slots of
+// 32 lanes), so two logits share each packed operation:
+//   clamp  a 16-bit maximum with a large negative number: -inf (and the type's lowest value) then
+//          add 0 and not 0 * inf; NaN passes and makes the row NaN
+//   t      one packed fp32 FMA, x log2(e) - R with R = m log2(e) rounded; what the rounding of R leaves
+//          out of z and s is put right once per thread at the end
+//   2^t    one exponential each; then one packed addition and one packed FMA
+// Where m is so large or so low that R or the clamp would not do (a row of the type's lowest value
+// only), a thread subtracts and multiplies instead.
 //
 // The k most likely tokens need no second pass over the row. A thread remembers the largest vector
 // it saw (its maximum and where, the first among equals). 64 groups of 8 threads make 64 such
@@ -36,7 +43,7 @@ constexpr int kLpGroups = 64;                 // bests that bound the k-th large
 constexpr int kLpMaxTop = 32;
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpUnroll = 4;                  // vectors of a thread in flight
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFar = 150.f;                 // exp(-150) is below the smallest fp32
 constexpr float kNegInf = -INFINITY;
 
@@ -145,42 +152,119 @@ struct LpRow {
     }
 };
 
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Two logits of word w of a vector (fp32: of words w and w + 1), at least the clamp.
+template <int DT>
+__device__ __forceinline__ uint64_t clamped_pair(const uint32_t (&u)[4], int i) {
+    if constexpr (DT == kLpFp32) {
+        return pair(max_nan(__uint_as_float(u[2 * i]), -1e30f), max_nan(__uint_as_float(u[2 * i + 1]), -1e30f));
+    } else if constexpr (DT == kLpBf16) {
+        uint32_t w;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(u[i]), "r"(0xf149f149u));       // -1e30
+        return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    } else {
+        uint32_t w;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(w) : "r"(u[i]), "r"(0xfbfffbffu));        // -65504
+        return pair(__half2float(__ushort_as_half(static_cast<uint16_t>(w & 0xffffu))),
+                    __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16))));
+    }
+}
+
 // Softmax statistics of a set of logits; m = -inf: nothing but -inf (and NaN) so far.
 struct LpStat {
     float m, z, s;
     // to a reference n >= m
     __device__ void move(float n) {
         if (n > m) {
-            const float d = m == kNegInf ? -kFar : fmaxf(m - n, -kFar);
-            const float f = ex2(d * kLog2e);
+            const float d = fmaxf(m - n, -kFar) * kLog2e;      // (m = -inf: z and s are 0, or NaN)
+            const float f = ex2(d);
             s = f * fmaf(d, z, s);
             z = f * z;
             m = n;
         }
     }
-    __device__ void join(float m2, float z2, float s2) {
-        LpStat o{m2, z2, s2};
-        const float n = fmaxf(m, m2);
-        move(n);
-        o.move(n);
-        z += o.z;
-        s += o.s;
+};
+
+// A thread's statistics as the pass builds them: even and odd elements' sums apart.
+template <int DT>
+struct LpAcc {
+    float m = kNegInf;
+    uint64_t z = 0, s = 0;
+    // whether R = m log2(e) is no use as a reference, or m is not well above the clamp
+    __device__ bool slow() const {
+        constexpr float low = DT == kLpFp16 ? -6e4f : -1e29f;
+        return (m < low && m != kNegInf) || m > 1e38f;
     }
-    template <int DT>
+    __device__ float ref() const { return m == kNegInf ? 0.f : m * kLog2e; }
+    __device__ void move(float n) {
+        float z0, z1, s0, s1;
+        unpair(z, z0, z1);
+        unpair(s, s0, s1);
+        LpStat a{m, z0, s0}, b{m, z1, s1};
+        a.move(n);
+        b.move(n);
+        m = n;
+        z = pair(a.z, b.z);
+        s = pair(a.s, b.s);
+    }
     __device__ void add(const uint4& v) {            // (m already covers v)
-        const float ref = m == kNegInf ? 0.f : m;
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        if (slow()) {
+            float z0, z1, s0, s1;
+            unpair(z, z0, z1);
+            unpair(s, s0, s1);
 #pragma unroll
-        for (int j = 0; j < LpVec<DT>::kN; ++j) {
-            const float d = max_nan(LpVec<DT>::at(v, j) - ref, -kFar);
-            const float e = ex2(d * kLog2e);
-            z += e;
-            s = fmaf(d, e, s);
+            for (int j = 0; j < LpVec<DT>::kN; ++j) {
+                const float t = max_nan(LpVec<DT>::at(v, j) - m, -kFar) * kLog2e, e = ex2(t);
+                z0 += e;
+                s0 = fmaf(t, e, s0);
+            }
+            z = pair(z0, z1);
+            s = pair(s0, s1);
+            return;
         }
+        const uint64_t minus_r = pair(-ref(), -ref()), l2e = pair(kLog2e, kLog2e);
+#pragma unroll
+        for (int i = 0; i < LpVec<DT>::kN / 2; ++i) {
+            const uint64_t t = fma2(clamped_pair<DT>(u, i), l2e, minus_r);
+            float t0, t1;
+            unpair(t, t0, t1);
+            const uint64_t e = pair(ex2(t0), ex2(t1));
+            z = add2(z, e);
+            s = fma2(t, e, s);
+        }
+    }
+    // The whole, with m itself as the reference: t was off by r, the part of m log2(e) that R leaves out.
+    __device__ LpStat done() const {
+        float z0, z1, s0, s1;
+        unpair(z, z0, z1);
+        unpair(s, s0, s1);
+        const float r = m == kNegInf || slow() ? 0.f : fmaf(m, kLog2e, -ref());
+        const float f = 1.f - r * kLn2, zz = (z0 + z1) * f;
+        return LpStat{m, zz, fmaf(-r, zz, (s0 + s1) * f)};
     }
 };
 
 struct LpShared {
-    LpStat stat[kLpWarps];
+    float2 stat[kLpWarps];                           // warps' z and s, with the CTA's m
     LpStat total;
     unsigned long long best[kLpGroups];
     unsigned long long tau;
@@ -189,129 +273,152 @@ struct LpShared {
     unsigned long long top[kLpMaxTop];               // this CTA's best, in order, 0 where there are fewer
 };
 
+__device__ __forceinline__ unsigned long long shfl_xor_max(unsigned long long v, int d) {
+    const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, d);
+    return o > v ? o : v;
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a) {
     using Vec = LpVec<DT>;
     __shared__ LpShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const long long t = blockIdx.x / C;
+    const long long t = C > 1 ? blockIdx.x / C : blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const LpRow<DT> row(a.logits, a.ld, t, a.V);
-    const int v0 = static_cast<int>(static_cast<long long>(row.nv) * rank / C);
-    const int v1 = static_cast<int>(static_cast<long long>(row.nv) * (rank + 1) / C);
+    const int v0 = C > 1 ? static_cast<int>(static_cast<long long>(row.nv) * rank / C) : 0;
+    const int v1 = C > 1 ? static_cast<int>(static_cast<long long>(row.nv) * (rank + 1) / C) : row.nv;
 
-    LpStat st{kNegInf, 0.f, 0.f};
-    int bv = -1;                                     // the vector of this thread's maximum, st.m
+    LpAcc<DT> acc;
+    int bv = -1;                                     // the vector of this thread's maximum, acc.m
     int v = v0 + tid;
-    // the vectors between the row's first and last, which may be partial
-    if (v == 0 && v < v1) {
-        const uint4 x = row.load_edge(0);
+    // one vector, which may be the row's first or last and partly outside it
+    auto edge = [&](int i) {
+        const uint4 x = row.load_edge(i);
         const float n = Vec::max(x);
-        if (n > st.m) bv = 0;
-        st.move(n);
-        st.add<DT>(x);
+        if (n > acc.m) {
+            bv = i;
+            acc.move(n);
+        }
+        acc.add(x);
+    };
+    if (v == 0 && v < v1) {
+        edge(0);
         v += kLpThreads;
     }
-    const int last = min(v1, row.nv - 1);
-    for (; v + (kLpUnroll - 1) * kLpThreads < last; v += kLpUnroll * kLpThreads) {
-        uint4 x[kLpUnroll];
+    const int last = min(v1, row.nv - 1);            // whole vectors end here
+    uint4 x[kLpUnroll];
+    bool more = v + (kLpUnroll - 1) * kLpThreads < last;
+    if (more)
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) x[u] = row.load(v + u * kLpThreads);
-        float n = st.m;
+    while (more) {
+        uint4 y[kLpUnroll];
+        const int at = v;
+        v += kLpUnroll * kLpThreads;
+        more = v + (kLpUnroll - 1) * kLpThreads < last;
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) y[u] = x[u];
+        if (more)                                    // the next batch is on its way while this one is added in
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) x[u] = row.load(v + u * kLpThreads);
+        float n = acc.m;
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) {
-            const float vm = Vec::max(x[u]);
+            const float vm = Vec::max(y[u]);
             if (vm > n) {
                 n = vm;
-                bv = v + u * kLpThreads;
+                bv = at + u * kLpThreads;
             }
         }
-        st.move(n);
+        if (n > acc.m) acc.move(n);
 #pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) st.add<DT>(x[u]);
+        for (int u = 0; u < kLpUnroll; ++u) acc.add(y[u]);
     }
-    for (; v < v1; v += kLpThreads) {
-        const uint4 x = row.load_edge(v);
-        const float n = Vec::max(x);
-        if (n > st.m) bv = v;
-        st.move(n);
-        st.add<DT>(x);
-    }
+    for (; v < v1; v += kLpThreads) edge(v);
     // this thread's best as a bound for elements: its value and its vector's last index
-    unsigned long long best = bv < 0 ? 0ull : key_of(st.m, min(bv * Vec::kN + Vec::kN - 1 - row.head, a.V - 1));
-
-    // ---- the CTA's statistics
+    const unsigned long long best =
+        bv < 0 ? 0ull : key_of(acc.m, min(bv * Vec::kN + Vec::kN - 1 - row.head, a.V - 1));
+    unsigned long long g = best;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, st.m, d), z2 = __shfl_xor_sync(0xffffffffu, st.z, d),
-                    s2 = __shfl_xor_sync(0xffffffffu, st.s, d);
-        st.join(m2, z2, s2);
-    }
-    if (lane == 0) sh.stat[warp] = st;
+    for (int d = 1; d < kLpThreads / kLpGroups; d <<= 1) g = shfl_xor_max(g, d);
+    if (tid % (kLpThreads / kLpGroups) == 0) sh.best[tid / (kLpThreads / kLpGroups)] = g;
     if (tid == 0) {
         sh.tau = 0;
         sh.n = 0;
     }
     if (tid < kLpMaxTop) sh.top[tid] = 0;
-    if (a.k > 0) {
-        unsigned long long g = best;
+    __syncthreads();
+
+    // ---- the CTA's m, every thread's sums with it, and tau
+    const uint32_t top_order = __reduce_max_sync(
+        0xffffffffu, max(static_cast<uint32_t>(sh.best[lane] >> 32), static_cast<uint32_t>(sh.best[lane + 32] >> 32)));
+    LpStat st = acc.done();
+    const float m = top_order ? value_of(top_order) : kNegInf;
+    st.move(m);
 #pragma unroll
-        for (int d = 1; d < kLpThreads / kLpGroups; d <<= 1) {
-            const unsigned long long o = __shfl_xor_sync(0xffffffffu, g, d);
-            g = o > g ? o : g;
-        }
-        if (tid % (kLpThreads / kLpGroups) == 0) sh.best[tid / (kLpThreads / kLpGroups)] = g;
+    for (int d = 16; d; d >>= 1) {
+        st.z += __shfl_xor_sync(0xffffffffu, st.z, d);
+        st.s += __shfl_xor_sync(0xffffffffu, st.s, d);
+    }
+    if (lane == 0) sh.stat[warp] = make_float2(st.z, st.s);
+    if (a.k > 0 && tid < kLpGroups) {
+        const unsigned long long mine = sh.best[tid];
+        int above = 0;
+#pragma unroll 8
+        for (int i = 0; i < kLpGroups; ++i) above += sh.best[i] > mine ? 1 : 0;
+        if (mine && above == a.k - 1) sh.tau = mine;
     }
     __syncthreads();
     if (warp == kLpWarps - 1) {
-        LpStat w = sh.stat[lane % kLpWarps];
+        float2 w = lane < kLpWarps ? sh.stat[lane] : make_float2(0.f, 0.f);
 #pragma unroll
         for (int d = kLpWarps / 2; d; d >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, w.m, d), z2 = __shfl_xor_sync(0xffffffffu, w.z, d),
-                        s2 = __shfl_xor_sync(0xffffffffu, w.s, d);
-            w.join(m2, z2, s2);
+            w.x += __shfl_xor_sync(0xffffffffu, w.x, d);
+            w.y += __shfl_xor_sync(0xffffffffu, w.y, d);
         }
-        if (lane == 0) sh.total = w;
+        if (lane == 0) sh.total = LpStat{m, w.x, w.y};
     }
 
-    // ---- the CTA's k best
+    // ---- the CTA's k best: the flagged threads' vectors once more
     if (a.k > 0) {
-        if (tid < kLpGroups) {
-            const unsigned long long mine = sh.best[tid];
-            int above = 0;
-            for (int i = 0; i < kLpGroups; ++i) above += sh.best[i] > mine ? 1 : 0;
-            if (mine && above == a.k - 1) sh.tau = mine;
-        }
-        __syncthreads();
         const unsigned long long tau = sh.tau;
         unsigned long long list = 0;                 // lane i: the warp's i-th best so far
         unsigned long long floor = tau ? tau - 1 : 0;   // what an element has to be above
         unsigned int todo = __ballot_sync(0xffffffffu, best != 0 && best >= tau);
-        while (todo) {
-            const int from = __ffs(todo) - 1;
-            todo &= todo - 1;
-            for (int w0 = v0 + warp * 32 + from; w0 < v1; w0 += 32 * kLpThreads) {
-                const int w = w0 + lane * kLpThreads;
-                const uint4 x = w < v1 ? row.load_edge(w) : Vec::none();
+        auto offer = [&](const uint4& x, int w) {
 #pragma unroll
-                for (int j = 0; j < Vec::kN; ++j) {
-                    const float f = Vec::at(x, j);
-                    const unsigned long long key = f > kNegInf ? key_of(f, w * Vec::kN - row.head + j) : 0ull;
-                    unsigned int in = __ballot_sync(0xffffffffu, key > floor);
-                    while (in) {
-                        const unsigned long long c = __shfl_sync(0xffffffffu, key, __ffs(in) - 1);
-                        in &= in - 1;
-                        if (c <= floor) continue;
-                        const int at = __popc(__ballot_sync(0xffffffffu, list > c));
-                        const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
-                        if (lane == at) list = c;
-                        else if (lane > at) list = up;
-                        const unsigned long long kth = __shfl_sync(0xffffffffu, list, a.k - 1);
-                        if (kth > floor) floor = kth;
-                    }
+            for (int j = 0; j < Vec::kN; ++j) {
+                const float f = Vec::at(x, j);
+                const unsigned long long key = f > kNegInf ? key_of(f, w * Vec::kN - row.head + j) : 0ull;
+                unsigned int in = __ballot_sync(0xffffffffu, key > floor);
+                while (in) {
+                    const unsigned long long c = __shfl_sync(0xffffffffu, key, __ffs(in) - 1);
+                    in &= in - 1;
+                    if (c <= floor) continue;
+                    const int at = __popc(__ballot_sync(0xffffffffu, list > c));
+                    const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
+                    if (lane == at) list = c;
+                    else if (lane > at) list = up;
+                    const unsigned long long kth = __shfl_sync(0xffffffffu, list, a.k - 1);
+                    if (kth > floor) floor = kth;
                 }
+            }
+        };
+        // A flagged thread has `per` vectors; as many such threads as fit 32 lanes are read at once.
+        const int per = (v1 - v0 + kLpThreads - 1) / kLpThreads;
+        const int shift = per <= 1 ? 0 : per >= 32 ? 5 : 32 - __clz(per - 1);
+        const int sub = lane >> shift, vec = lane & ((1 << shift) - 1);
+        while (todo) {
+            unsigned int left = todo;                // the sub-th of the flagged lanes that are left
+            for (int i = 0; i < sub; ++i) left &= left - 1;
+            const int from = left ? __ffs(left) - 1 : -1;
+            for (int i = 0; i < (32 >> shift) && todo; ++i) todo &= todo - 1;
+            for (int r = 0; r < per; r += 32) {
+                const int w = v0 + warp * 32 + from + (r + vec) * kLpThreads;
+                offer(from >= 0 && w < v1 ? row.load_edge(w) : Vec::none(), w);
             }
         }
         const int have = min(__popc(__ballot_sync(0xffffffffu, list != 0)), a.k);
@@ -336,20 +443,22 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
     if (C > 1) {
         cluster_sync();
         if (rank == 0) {
-            if (tid < 32) {
+            if (warp == 0) {
                 LpStat w{kNegInf, 0.f, 0.f};
                 if (lane < C) {
                     const uint32_t p = map_to_rank(smem_u32(&sh.total), lane);
                     w = LpStat{ld_cluster_f32(p), ld_cluster_f32(p + 4), ld_cluster_f32(p + 8)};
                 }
+                float n = w.m;
+#pragma unroll
+                for (int d = kLpMaxCluster / 2; d; d >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
+                w.move(n);
 #pragma unroll
                 for (int d = kLpMaxCluster / 2; d; d >>= 1) {
-                    const float m2 = __shfl_xor_sync(0xffffffffu, w.m, d), z2 = __shfl_xor_sync(0xffffffffu, w.z, d),
-                                s2 = __shfl_xor_sync(0xffffffffu, w.s, d);
-                    w.join(m2, z2, s2);
+                    w.z += __shfl_xor_sync(0xffffffffu, w.z, d);
+                    w.s += __shfl_xor_sync(0xffffffffu, w.s, d);
                 }
-                __syncwarp();
-                if (lane == 0) sh.stat[0] = w;
+                if (lane == 0) sh.stat[0] = make_float2(w.z, w.s), sh.tau = __float_as_uint(n);
             }
             for (int i = tid; i < C * kLpMaxTop; i += kLpThreads) {
                 const uint32_t p = map_to_rank(smem_u32(&sh.top[i % kLpMaxTop]), i / kLpMaxTop);
@@ -362,13 +471,13 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
         if (rank != 0) return;
         if (tid < kLpMaxTop) sh.top[tid] = 0;
         __syncthreads();
-        for (int i = tid; i < C * kLpMaxTop; i += kLpThreads) {
+        for (int i = tid; a.k > 0 && i < C * kLpMaxTop; i += kLpThreads) {
             const unsigned long long mine = sh.cand[i];
             int above = 0;
             for (int q = 0; q < C * kLpMaxTop; ++q) above += sh.cand[q] > mine ? 1 : 0;
             if (mine && above < a.k) sh.top[above] = mine;
         }
-        if (tid == 0) sh.total = sh.stat[0];
+        if (tid == 0) sh.total = LpStat{__uint_as_float(static_cast<uint32_t>(sh.tau)), sh.stat[0].x, sh.stat[0].y};
         __syncthreads();
     }
 
@@ -381,7 +490,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
         a.top_ids[t * a.k + tid] = key ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
         a.top_logprobs[t * a.k + tid] = logp(key ? value_of(static_cast<uint32_t>(key >> 32)) : kNegInf);
     }
-    if (tid == 32 && a.entropy) a.entropy[t] = nothing ? 0.f : logz - all.s / all.z;
+    if (tid == 32 && a.entropy) a.entropy[t] = nothing ? 0.f : logz - kLn2 * (all.s / all.z);
     if (tid == 64 && a.logprobs) {
         const long long id = a.tokens[t];
         float r = NAN;
