@@ -19,8 +19,9 @@
 // it saw (its maximum and where, the first among equals). 64 groups of 8 threads make 64 such
 // bests; the k-th largest of them, tau, is a bound that at least k elements reach, so only threads
 // whose own best reaches it can hold an answer, about k of 512. Their vectors (V / 512 elements each)
-// are read again by whole warps, which keep the best k in order, one per lane; the warps' lists, a
-// few dozen entries, are ranked by counting. An element's order is one 64-bit key: the float
+// are read again by whole warps; of the few that reach tau, the elements go one to a lane, and the
+// warp keeps the best k in order, one per lane; the warps' lists, a few dozen entries, are ranked by
+// counting. An element's order is one 64-bit key: the float
 // as an unsigned integer of the same order, then the complement of its index, so that equal logits
 // rank by the lower index and no two keys are equal.
 //
@@ -40,6 +41,7 @@ namespace {
 constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpGroups = 64;                 // bests that bound the k-th largest
+constexpr int kLpParts = kLpThreads / kLpGroups;
 constexpr int kLpMaxTop = 32;
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpUnroll = 4;                  // vectors of a thread in flight
@@ -267,9 +269,11 @@ struct LpShared {
     float2 stat[kLpWarps];                           // warps' z and s, with the CTA's m
     LpStat total;
     unsigned long long best[kLpGroups];
-    unsigned long long tau;
-    int n;
+    int above[kLpGroups];                            // bests above each
+    int n, flagged;
+    uint16_t flag[kLpThreads];                       // threads whose best reaches tau
     unsigned long long cand[kLpWarps * kLpMaxTop];
+    int rank[kLpMaxCluster * kLpMaxTop];             // of the clusters' lists
     unsigned long long top[kLpMaxTop];               // this CTA's best, in order, 0 where there are fewer
 };
 
@@ -291,6 +295,16 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
     const int v0 = C > 1 ? static_cast<int>(static_cast<long long>(row.nv) * rank / C) : 0;
     const int v1 = C > 1 ? static_cast<int>(static_cast<long long>(row.nv) * (rank + 1) / C) : row.nv;
 
+    // the asked token's logit, on its way while the row is read (NaN: no such token)
+    float asked = NAN;
+    if (tid == 64 && rank == 0 && a.logprobs) {
+        const long long id = a.tokens[t];
+        if (id >= 0 && id < a.V) {
+            const char* p = static_cast<const char*>(a.logits) + (t * a.ld + id) * Vec::kSize;
+            const uint32_t u = DT == kLpFp32 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
+            asked = Vec::at(make_uint4(u, 0, 0, 0), 0);
+        }
+    }
     LpAcc<DT> acc;
     int bv = -1;                                     // the vector of this thread's maximum, acc.m
     int v = v0 + tid;
@@ -346,10 +360,11 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
     for (int d = 1; d < kLpThreads / kLpGroups; d <<= 1) g = shfl_xor_max(g, d);
     if (tid % (kLpThreads / kLpGroups) == 0) sh.best[tid / (kLpThreads / kLpGroups)] = g;
     if (tid == 0) {
-        sh.tau = 0;
         sh.n = 0;
+        sh.flagged = 0;
     }
     if (tid < kLpMaxTop) sh.top[tid] = 0;
+    if (tid < kLpGroups) sh.above[tid] = 0;
     __syncthreads();
 
     // ---- the CTA's m, every thread's sums with it, and tau
@@ -364,12 +379,13 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
         st.s += __shfl_xor_sync(0xffffffffu, st.s, d);
     }
     if (lane == 0) sh.stat[warp] = make_float2(st.z, st.s);
-    if (a.k > 0 && tid < kLpGroups) {
-        const unsigned long long mine = sh.best[tid];
+    if (a.k > 0) {                                   // how many bests are above each: an eighth of them per thread
+        const unsigned long long mine = sh.best[tid % kLpGroups];
         int above = 0;
-#pragma unroll 8
-        for (int i = 0; i < kLpGroups; ++i) above += sh.best[i] > mine ? 1 : 0;
-        if (mine && above == a.k - 1) sh.tau = mine;
+#pragma unroll
+        for (int i = 0; i < kLpGroups / kLpParts; ++i)
+            above += sh.best[tid / kLpGroups * (kLpGroups / kLpParts) + i] > mine ? 1 : 0;
+        if (above) atomicAdd(&sh.above[tid % kLpGroups], above);
     }
     __syncthreads();
     if (warp == kLpWarps - 1) {
@@ -384,15 +400,41 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
 
     // ---- the CTA's k best: the flagged threads' vectors once more
     if (a.k > 0) {
-        const unsigned long long tau = sh.tau;
+        // tau: the best with k - 1 above it (none, so 0, where fewer than k groups have one)
+        const unsigned long long b0 = sh.above[lane] == a.k - 1 ? sh.best[lane] : 0,
+                                 b1 = sh.above[lane + 32] == a.k - 1 ? sh.best[lane + 32] : 0;
+        const unsigned int h0 = __ballot_sync(0xffffffffu, b0 != 0), h1 = __ballot_sync(0xffffffffu, b1 != 0);
+        const unsigned long long tau = h0   ? __shfl_sync(0xffffffffu, b0, __ffs(h0) - 1)
+                                       : h1 ? __shfl_sync(0xffffffffu, b1, __ffs(h1) - 1)
+                                            : 0;
+        const unsigned int mine = __ballot_sync(0xffffffffu, best != 0 && best >= tau);
+        if (mine) {
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&sh.flagged, __popc(mine));
+            at = __shfl_sync(0xffffffffu, at, 0);
+            if (mine >> lane & 1) sh.flag[at + __popc(mine & ((1u << lane) - 1))] = static_cast<uint16_t>(tid);
+        }
+        __syncthreads();
         unsigned long long list = 0;                 // lane i: the warp's i-th best so far
         unsigned long long floor = tau ? tau - 1 : 0;   // what an element has to be above
-        unsigned int todo = __ballot_sync(0xffffffffu, best != 0 && best >= tau);
+        const uint32_t tau_order = static_cast<uint32_t>(tau >> 32);
+        // a vector per lane, vector index w: the elements of those that hold tau's value or a larger one, one
+        // per lane
         auto offer = [&](const uint4& x, int w) {
-#pragma unroll
-            for (int j = 0; j < Vec::kN; ++j) {
-                const float f = Vec::at(x, j);
-                const unsigned long long key = f > kNegInf ? key_of(f, w * Vec::kN - row.head + j) : 0ull;
+            const float most = Vec::max(x);
+            unsigned int hit = __ballot_sync(0xffffffffu, most > kNegInf && order_of(most) >= tau_order);
+            while (hit) {
+                const int from = __ffs(hit) - 1;
+                hit &= hit - 1;
+                const uint32_t u0 = __shfl_sync(0xffffffffu, x.x, from), u1 = __shfl_sync(0xffffffffu, x.y, from),
+                               u2 = __shfl_sync(0xffffffffu, x.z, from), u3 = __shfl_sync(0xffffffffu, x.w, from);
+                const int at_w = __shfl_sync(0xffffffffu, w, from);
+                const int j = lane & (Vec::kN - 1), word = DT == kLpFp32 ? j : j >> 1;
+                const uint32_t u = word == 0 ? u0 : word == 1 ? u1 : word == 2 ? u2 : u3;
+                // (its logit in the low half: element 0 of a vector of it)
+                const float f = Vec::at(make_uint4(DT != kLpFp32 && (j & 1) ? u >> 16 : u, 0, 0, 0), 0);
+                const unsigned long long key =
+                    lane < Vec::kN && f > kNegInf ? key_of(f, at_w * Vec::kN - row.head + j) : 0ull;
                 unsigned int in = __ballot_sync(0xffffffffu, key > floor);
                 while (in) {
                     const unsigned long long c = __shfl_sync(0xffffffffu, key, __ffs(in) - 1);
@@ -407,18 +449,27 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
                 }
             }
         };
-        // A flagged thread has `per` vectors; as many such threads as fit 32 lanes are read at once.
+        // The flagged threads' vectors, dealt out over the warps in units of 32: a thread has `per`, and as many
+        // threads as fit share a unit. A warp's loads are under way together, kUnits at a time.
         const int per = (v1 - v0 + kLpThreads - 1) / kLpThreads;
         const int shift = per <= 1 ? 0 : per >= 32 ? 5 : 32 - __clz(per - 1);
-        const int sub = lane >> shift, vec = lane & ((1 << shift) - 1);
-        while (todo) {
-            unsigned int left = todo;                // the sub-th of the flagged lanes that are left
-            for (int i = 0; i < sub; ++i) left &= left - 1;
-            const int from = left ? __ffs(left) - 1 : -1;
-            for (int i = 0; i < (32 >> shift) && todo; ++i) todo &= todo - 1;
-            for (int r = 0; r < per; r += 32) {
-                const int w = v0 + warp * 32 + from + (r + vec) * kLpThreads;
-                offer(from >= 0 && w < v1 ? row.load_edge(w) : Vec::none(), w);
+        const int rounds = (per + 31) >> 5, flagged = sh.flagged;
+        const int units = (flagged << shift) + 31 >> 5;
+        constexpr int kUnits = 4;
+        for (int r = 0; r < rounds; ++r) {
+            for (int u0 = warp; u0 < units; u0 += kUnits * kLpWarps) {
+                uint4 y[kUnits];
+                int w[kUnits];
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    const int slot = (u0 + i * kLpWarps) * 32 + lane;     // of the flagged threads' vectors
+                    const int who = slot >> shift;
+                    w[i] = who < flagged ? v0 + sh.flag[who] + (r * 32 + (slot & ((1 << shift) - 1))) * kLpThreads : v1;
+                    y[i] = w[i] < v1 ? row.load_edge(w[i]) : Vec::none();
+                }
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i)
+                    if (u0 + i * kLpWarps < units) offer(y[i], w[i]);
             }
         }
         const int have = min(__popc(__ballot_sync(0xffffffffu, list != 0)), a.k);
@@ -458,26 +509,36 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
                     w.z += __shfl_xor_sync(0xffffffffu, w.z, d);
                     w.s += __shfl_xor_sync(0xffffffffu, w.s, d);
                 }
-                if (lane == 0) sh.stat[0] = make_float2(w.z, w.s), sh.tau = __float_as_uint(n);
+                if (lane == 0) sh.total = LpStat{n, w.z, w.s};
             }
             for (int i = tid; i < C * kLpMaxTop; i += kLpThreads) {
                 const uint32_t p = map_to_rank(smem_u32(&sh.top[i % kLpMaxTop]), i / kLpMaxTop);
                 unsigned long long key;
                 asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(p) : "memory");
                 sh.cand[i] = key;
+                sh.rank[i] = 0;
             }
         }
         cluster_sync();                              // every part is read: the other CTAs may leave
         if (rank != 0) return;
         if (tid < kLpMaxTop) sh.top[tid] = 0;
         __syncthreads();
-        for (int i = tid; a.k > 0 && i < C * kLpMaxTop; i += kLpThreads) {
-            const unsigned long long mine = sh.cand[i];
-            int above = 0;
-            for (int q = 0; q < C * kLpMaxTop; ++q) above += sh.cand[q] > mine ? 1 : 0;
-            if (mine && above < a.k) sh.top[above] = mine;
+        // Each list is in order, so a key's rank is the sum over the lists of how many of each are above it,
+        // found by halving: a thread per key and list.
+        if (a.k > 0) {
+            for (int i = tid; i < C * kLpMaxTop * C; i += kLpThreads) {
+                const unsigned long long mine = sh.cand[i % (C * kLpMaxTop)];
+                const unsigned long long* list = sh.cand + i / (C * kLpMaxTop) * kLpMaxTop;
+                int n = 0;                           // list[0 .. n) are above mine
+#pragma unroll
+                for (int half = kLpMaxTop / 2; half; half >>= 1) n += list[n + half - 1] > mine ? half : 0;
+                n += list[n] > mine ? 1 : 0;
+                if (n) atomicAdd(&sh.rank[i % (C * kLpMaxTop)], n);
+            }
+            __syncthreads();
+            for (int i = tid; i < C * kLpMaxTop; i += kLpThreads)
+                if (sh.cand[i] && sh.rank[i] < a.k) sh.top[sh.rank[i]] = sh.cand[i];
         }
-        if (tid == 0) sh.total = LpStat{__uint_as_float(static_cast<uint32_t>(sh.tau)), sh.stat[0].x, sh.stat[0].y};
         __syncthreads();
     }
 
@@ -491,17 +552,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
         a.top_logprobs[t * a.k + tid] = logp(key ? value_of(static_cast<uint32_t>(key >> 32)) : kNegInf);
     }
     if (tid == 32 && a.entropy) a.entropy[t] = nothing ? 0.f : logz - kLn2 * (all.s / all.z);
-    if (tid == 64 && a.logprobs) {
-        const long long id = a.tokens[t];
-        float r = NAN;
-        if (id >= 0 && id < a.V) {
-            const char* p = static_cast<const char*>(a.logits) + (t * a.ld + id) * Vec::kSize;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            x.x = DT == kLpFp32 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
-            r = logp(Vec::at(x, 0));
-        }
-        a.logprobs[t] = r;
-    }
+    if (tid == 64 && a.logprobs) a.logprobs[t] = asked == asked ? logp(asked) : asked;
 }
 
 }  // namespace
