@@ -19,9 +19,7 @@
 // it saw (its maximum and where, the first among equals). 64 groups of 8 threads make 64 such
 // bests; the k-th largest of them, tau, is a bound that at least k elements reach, so only threads
 // whose own best reaches it can hold an answer, about k of 512. Their vectors (V / 512 elements each)
-// are read again by whole warps; of the few that reach tau, the elements go one to a lane, and the
-// warp keeps the best k in order, one per lane; the warps' lists, a few dozen entries, are ranked by
-// counting. An element's order is one 64-bit key: the float
+// are read again by whole warps; the elements that reach tau, a few dozen, are ranked by counting. An element's order is one 64-bit key: the float
 // as an unsigned integer of the same order, then the complement of its index, so that equal logits
 // rank by the lower index and no two keys are equal.
 //
@@ -415,40 +413,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
             if (mine >> lane & 1) sh.flag[at + __popc(mine & ((1u << lane) - 1))] = static_cast<uint16_t>(tid);
         }
         __syncthreads();
-        unsigned long long list = 0;                 // lane i: the warp's i-th best so far
-        unsigned long long floor = tau ? tau - 1 : 0;   // what an element has to be above
         const uint32_t tau_order = static_cast<uint32_t>(tau >> 32);
-        // a vector per lane, vector index w: the elements of those that hold tau's value or a larger one, one
-        // per lane
-        auto offer = [&](const uint4& x, int w) {
-            const float most = Vec::max(x);
-            unsigned int hit = __ballot_sync(0xffffffffu, most > kNegInf && order_of(most) >= tau_order);
-            while (hit) {
-                const int from = __ffs(hit) - 1;
-                hit &= hit - 1;
-                const uint32_t u0 = __shfl_sync(0xffffffffu, x.x, from), u1 = __shfl_sync(0xffffffffu, x.y, from),
-                               u2 = __shfl_sync(0xffffffffu, x.z, from), u3 = __shfl_sync(0xffffffffu, x.w, from);
-                const int at_w = __shfl_sync(0xffffffffu, w, from);
-                const int j = lane & (Vec::kN - 1), word = DT == kLpFp32 ? j : j >> 1;
-                const uint32_t u = word == 0 ? u0 : word == 1 ? u1 : word == 2 ? u2 : u3;
-                // (its logit in the low half: element 0 of a vector of it)
-                const float f = Vec::at(make_uint4(DT != kLpFp32 && (j & 1) ? u >> 16 : u, 0, 0, 0), 0);
-                const unsigned long long key =
-                    lane < Vec::kN && f > kNegInf ? key_of(f, at_w * Vec::kN - row.head + j) : 0ull;
-                unsigned int in = __ballot_sync(0xffffffffu, key > floor);
-                while (in) {
-                    const unsigned long long c = __shfl_sync(0xffffffffu, key, __ffs(in) - 1);
-                    in &= in - 1;
-                    if (c <= floor) continue;
-                    const int at = __popc(__ballot_sync(0xffffffffu, list > c));
-                    const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
-                    if (lane == at) list = c;
-                    else if (lane > at) list = up;
-                    const unsigned long long kth = __shfl_sync(0xffffffffu, list, a.k - 1);
-                    if (kth > floor) floor = kth;
-                }
-            }
-        };
         // The flagged threads' vectors, dealt out over the warps in units of 32: a thread has `per`, and as many
         // threads as fit share a unit. A warp's loads are under way together, kUnits at a time.
         const int per = (v1 - v0 + kLpThreads - 1) / kLpThreads;
@@ -456,30 +421,88 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
         const int rounds = (per + 31) >> 5, flagged = sh.flagged;
         const int units = (flagged << shift) + 31 >> 5;
         constexpr int kUnits = 4;
-        for (int r = 0; r < rounds; ++r) {
-            for (int u0 = warp; u0 < units; u0 += kUnits * kLpWarps) {
-                uint4 y[kUnits];
-                int w[kUnits];
+        auto second_look = [&](auto&& offer) {
+            for (int r = 0; r < rounds; ++r) {
+                for (int u0 = warp; u0 < units; u0 += kUnits * kLpWarps) {
+                    uint4 y[kUnits];
+                    int w[kUnits];
 #pragma unroll
-                for (int i = 0; i < kUnits; ++i) {
-                    const int slot = (u0 + i * kLpWarps) * 32 + lane;     // of the flagged threads' vectors
-                    const int who = slot >> shift;
-                    w[i] = who < flagged ? v0 + sh.flag[who] + (r * 32 + (slot & ((1 << shift) - 1))) * kLpThreads : v1;
-                    y[i] = w[i] < v1 ? row.load_edge(w[i]) : Vec::none();
+                    for (int i = 0; i < kUnits; ++i) {
+                        const int slot = (u0 + i * kLpWarps) * 32 + lane;     // of the flagged threads' vectors
+                        const int who = slot >> shift;
+                        w[i] = who < flagged ? v0 + sh.flag[who] + (r * 32 + (slot & ((1 << shift) - 1))) * kLpThreads : v1;
+                        y[i] = w[i] < v1 ? row.load_edge(w[i]) : Vec::none();
+                    }
+#pragma unroll
+                    for (int i = 0; i < kUnits; ++i)
+                        if (u0 + i * kLpWarps < units) offer(y[i], w[i]);
                 }
-#pragma unroll
-                for (int i = 0; i < kUnits; ++i)
-                    if (u0 + i * kLpWarps < units) offer(y[i], w[i]);
             }
-        }
-        const int have = min(__popc(__ballot_sync(0xffffffffu, list != 0)), a.k);
-        if (have) {
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&sh.n, have);
-            at = __shfl_sync(0xffffffffu, at, 0);
-            if (lane < have) sh.cand[at + lane] = list;
-        }
+        };
+        // A vector per lane, vector index w: what reaches tau is noted, a few dozen elements in all.
+        const unsigned long long floor0 = tau ? tau - 1 : 0;     // what an element has to be above
+        second_look([&](const uint4& x, int w) {
+            const float most = Vec::max(x);
+            if (most > kNegInf && order_of(most) >= tau_order) {
+#pragma unroll
+                for (int j = 0; j < Vec::kN; ++j) {
+                    const float f = Vec::at(x, j);
+                    const unsigned long long key = f > kNegInf ? key_of(f, w * Vec::kN - row.head + j) : 0ull;
+                    if (key > floor0) {
+                        const int at = atomicAdd(&sh.n, 1);
+                        if (at < kLpWarps * kLpMaxTop) sh.cand[at] = key;
+                    }
+                }
+            }
+        });
         __syncthreads();
+        if (sh.n > kLpWarps * kLpMaxTop) {           // (the same for every thread)
+            __syncthreads();
+            if (tid == 0) sh.n = 0;
+            __syncthreads();
+            unsigned long long list = 0;                 // lane i: the warp's i-th best so far
+            unsigned long long floor = floor0;
+            // More than fit (equal or steadily larger logits in one thread's share): each warp keeps the best k of
+            // what it sees in order, one per lane; the elements of a vector that reaches tau go one to a lane.
+            auto keep = [&](const uint4& x, int w) {
+                const float most = Vec::max(x);
+                unsigned int hit = __ballot_sync(0xffffffffu, most > kNegInf && order_of(most) >= tau_order);
+                while (hit) {
+                    const int from = __ffs(hit) - 1;
+                    hit &= hit - 1;
+                    const uint32_t u0 = __shfl_sync(0xffffffffu, x.x, from), u1 = __shfl_sync(0xffffffffu, x.y, from),
+                                   u2 = __shfl_sync(0xffffffffu, x.z, from), u3 = __shfl_sync(0xffffffffu, x.w, from);
+                    const int at_w = __shfl_sync(0xffffffffu, w, from);
+                    const int j = lane & (Vec::kN - 1), word = DT == kLpFp32 ? j : j >> 1;
+                    const uint32_t u = word == 0 ? u0 : word == 1 ? u1 : word == 2 ? u2 : u3;
+                    // (its logit in the low half: element 0 of a vector of it)
+                    const float f = Vec::at(make_uint4(DT != kLpFp32 && (j & 1) ? u >> 16 : u, 0, 0, 0), 0);
+                    const unsigned long long key =
+                        lane < Vec::kN && f > kNegInf ? key_of(f, at_w * Vec::kN - row.head + j) : 0ull;
+                    unsigned int in = __ballot_sync(0xffffffffu, key > floor);
+                    while (in) {
+                        const unsigned long long c = __shfl_sync(0xffffffffu, key, __ffs(in) - 1);
+                        in &= in - 1;
+                        if (c <= floor) continue;
+                        const int at = __popc(__ballot_sync(0xffffffffu, list > c));
+                        const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
+                        if (lane == at) list = c;
+                        else if (lane > at) list = up;
+                        const unsigned long long kth = __shfl_sync(0xffffffffu, list, a.k - 1);
+                        if (kth > floor) floor = kth;
+                    }
+                }
+            };
+            second_look(keep);
+            const int have = min(__popc(__ballot_sync(0xffffffffu, list != 0)), a.k);
+            if (have) {
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&sh.n, have);
+                at = __shfl_sync(0xffffffffu, at, 0);
+                if (lane < have) sh.cand[at + lane] = list;
+            }
+            __syncthreads();
+        }
         const int n = sh.n;
         if (tid < n) {
             const unsigned long long mine = sh.cand[tid];
