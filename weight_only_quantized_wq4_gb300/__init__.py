@@ -365,64 +365,28 @@ def grouped_mm_dev_ptrs(M: Sequence[int], N: Sequence[int], K: Sequence[int], X_
 
 
 # ------------------------------------------------------------------------------------ 8-bit rows
-# A decode step calls these every few microseconds, so the checks below read each tensor attribute
-# once, compare device numbers, and leave to the library what it checks itself (strides against
-# sizes, alignment).
-_t = None               # torch, and its types by the library's codes, once the first call has them
-_HALF = _OUT = _F8 = _F32 = None
+# A decode step makes these calls every few microseconds, so their tensors are checked and passed on by
+# _wq4_binding.so (csrc/wq4_binding.cpp), which calls the C ABI of the library in use.
+_binding = None         # the module, and the library it is bound to
+_bound = None
 
 
-def _types():
-    global _t, _HALF, _OUT, _F8, _F32
-    torch = _torch()
-    _HALF = {torch.bfloat16: 0, torch.float16: 1}
-    _OUT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    _F8, _F32 = torch.float8_e4m3fn, torch.float32
-    _t = torch
-    return load_library()
-
-
-def _refuse(t, name: str, shape, dtype, dev: int):
-    """Raises for the first thing wrong with tensor t; called when _rows or _vector found something."""
-    if t.dim() != len(shape) or tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be of shape %s" % (name, list(shape)))
-    if t.dtype != dtype:
-        raise ValueError("%s must be of type %s" % (name, str(dtype)[6:]))
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
-    raise ValueError("%s must be contiguous along its last dimension" % name)
-
-
-def _rows(t, name: str, rows: int, cols: int, dtype, dev: int):
-    """Pointer and row stride (in elements) of a [rows][cols] CUDA tensor whose rows are contiguous."""
-    if t.shape != (rows, cols) or t.dtype != dtype or t.get_device() != dev or dev < 0:
-        _refuse(t, name, (rows, cols), dtype, dev)
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        _refuse(t, name, (rows, cols), dtype, dev)
-    if rows <= 1:                                     # (the stride of a single row is never used)
-        ld = (cols + 15) // 16 * 16
-    return t.data_ptr(), ld
-
-
-def _vector(t, name: str, n: int, dtype, dev: int):
-    """Pointer of a contiguous CUDA tensor of n elements."""
-    if t.shape != (n,) or t.dtype != dtype or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
-        _refuse(t, name, (n,), dtype, dev)
-    return t.data_ptr()
-
-
-def _two_d(t, name: str, types):
-    """(rows, columns, type code, device number) of a 2-D CUDA tensor of one of `types`."""
-    code = types.get(t.dtype)
-    if code is None or t.dim() != 2 or not t.is_cuda:
-        raise ValueError("%s must be a 2-D CUDA tensor of %s" % (name, " or ".join(str(d)[6:] for d in types)))
-    rows, cols = t.shape
-    return rows, cols, code, t.get_device()
-
-
-def _raw_stream(dev: int) -> int:
-    return _t._C._cuda_getCurrentRawStream(dev)       # current_stream(dev).cuda_stream without its object
+def _bind():
+    global _binding, _bound
+    lib = load_library()
+    _torch()                                          # (the module needs torch's libraries)
+    if _binding is None:
+        path = os.path.join(PKG, "_wq4_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError("_wq4_binding.so is not built: run `python -m weight_only_quantized_wq4_gb300.builder`")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location(__name__ + "._wq4_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding = module
+    _binding.bind(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+        lib.wq4_add_rmsnorm_quant, lib.wq4_silu_mul_quant, lib.wq4_block_mm, lib.wq4_token_logprobs)])
+    _bound = lib
 
 
 def alloc_quant_rows(T: int, D: int, device="cuda"):
@@ -434,6 +398,17 @@ def alloc_quant_rows(T: int, D: int, device="cuda"):
     return q[:, :D], scales[:, :T]
 
 
+def _row_buffers(x, D: int, q, scales):
+    """q and scales as given, or new ones for x's rows."""
+    if q is not None and scales is not None:
+        return q, scales
+    if q is not scales:
+        raise ValueError("q and scales are given together")
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D CUDA tensor")
+    return alloc_quant_rows(x.shape[0], D, x.device)
+
+
 def add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, q=None, scales=None, residual_out=None, y=None):
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, quantised by rows (wq4_add_rmsnorm_quant).
 
@@ -441,29 +416,13 @@ def add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, q=None, scale
     [ceil(D/128)][T], and h in x's type (None without a residual). Buffers that are not given are
     allocated (alloc_quant_rows); residual_out may be x or residual itself. y: also write the
     16-bit y there (what mm reads)."""
-    lib = _types() if _t is None or _lib is None else _lib
-    T, D, code, dev = _two_d(x, "x", _HALF)
-    half = x.dtype
-    xp, ldx = _rows(x, "x", T, D, half, dev)
-    wp = _vector(weight, "weight", D, half, dev)
-    rp = rop = yp = None
-    ldr = ldro = ldy = 0
-    if residual is not None:
-        rp, ldr = _rows(residual, "residual", T, D, half, dev)
-        if residual_out is None:
-            residual_out = _t.empty((T, D), dtype=half, device=x.device)
-    if residual_out is not None:
-        rop, ldro = _rows(residual_out, "residual_out", T, D, half, dev)
-    if y is not None:
-        yp, ldy = _rows(y, "y", T, D, half, dev)
+    if _bound is not _lib or _lib is None:
+        _bind()
     if q is None or scales is None:
-        if q is not scales:
-            raise ValueError("q and scales are given together")
-        q, scales = alloc_quant_rows(T, D, x.device)
-    qp, ldq = _rows(q, "q", T, D, _F8, dev)
-    sp, lds = _rows(scales, "scales", (D + 127) // 128, T, _F32, dev)
-    rc = lib.wq4_add_rmsnorm_quant(xp, ldx, rp, ldr, wp, T, D, eps, code, rop, ldro, yp, ldy, qp, ldq, sp, lds,
-                                   _raw_stream(dev))
+        q, scales = _row_buffers(x, x.shape[-1], q, scales)
+    if residual is not None and residual_out is None:
+        residual_out = _torch().empty(tuple(x.shape), dtype=x.dtype, device=x.device)
+    rc = _binding.add_rmsnorm_quant(x, weight, residual, eps, q, scales, residual_out, y)
     if rc:
         raise Wq4Error(rc, "wq4_add_rmsnorm_quant")
     return q, scales, residual_out
@@ -472,19 +431,11 @@ def add_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, q=None, scale
 def silu_mul_quant(x, q=None, scales=None):
     """y = silu(x[:, :D]) * x[:, D:] for x bf16/fp16 [T][2 D], quantised by rows (wq4_silu_mul_quant):
     returns (q, scales) as add_rmsnorm_quant does."""
-    lib = _types() if _t is None or _lib is None else _lib
-    T, D2, code, dev = _two_d(x, "x", _HALF)
-    D = D2 // 2
-    if D2 != 2 * D:
-        raise ValueError("x must hold a gate and an up half")
-    xp, ldx = _rows(x, "x", T, D2, x.dtype, dev)
+    if _bound is not _lib or _lib is None:
+        _bind()
     if q is None or scales is None:
-        if q is not scales:
-            raise ValueError("q and scales are given together")
-        q, scales = alloc_quant_rows(T, D, x.device)
-    qp, ldq = _rows(q, "q", T, D, _F8, dev)
-    sp, lds = _rows(scales, "scales", (D + 127) // 128, T, _F32, dev)
-    rc = lib.wq4_silu_mul_quant(xp, ldx, T, D, code, qp, ldq, sp, lds, _raw_stream(dev))
+        q, scales = _row_buffers(x, x.shape[-1] // 2, q, scales)
+    rc = _binding.silu_mul_quant(x, q, scales)
     if rc:
         raise Wq4Error(rc, "wq4_silu_mul_quant")
     return q, scales
@@ -494,23 +445,14 @@ def block_mm(q, scales, W, W_scales, out=None, dtype=None):
     """Y[M,N] = X . W^T of quantised rows (q, scales) [M][K] with an e4m3 weight W [N][K] and its fp32 scales
     [ceil(N/128)][ceil(K/128)] (wq4_block_mm). Y is bf16, fp16 or fp32: out's type, or dtype (a
     torch type, bfloat16 by default)."""
-    lib = _types() if _t is None or _lib is None else _lib
-    M, K, _, dev = _two_d(q, "q", {_F8: 0})
-    N = W.shape[0]
-    kb = (K + 127) // 128
-    qp, ldq = _rows(q, "q", M, K, _F8, dev)
-    sp, lds = _rows(scales, "scales", kb, M, _F32, dev)
-    wp, ldw = _rows(W, "W", N, K, _F8, dev)
-    wsp, ldws = _rows(W_scales, "W_scales", (N + 127) // 128, kb, _F32, dev)
+    if _bound is not _lib or _lib is None:
+        _bind()
     if out is None:
-        out = _t.empty((M, N), dtype=dtype or _t.bfloat16, device=q.device)
+        torch = _torch()
+        out = torch.empty((q.shape[0], W.shape[0]), dtype=dtype or torch.bfloat16, device=q.device)
     elif dtype is not None and out.dtype != dtype:
         raise ValueError("out is not of the dtype asked for")
-    code = _OUT.get(out.dtype)
-    if code is None:
-        raise ValueError("the product's type must be bfloat16, float16 or float32")
-    yp, ldy = _rows(out, "out", M, N, out.dtype, dev)
-    rc = lib.wq4_block_mm(qp, ldq, sp, lds, wp, ldw, wsp, ldws, yp, ldy, M, N, K, code, _raw_stream(dev))
+    rc = _binding.block_mm(q, scales, W, W_scales, out)
     if rc:
         raise Wq4Error(rc, "wq4_block_mm")
     return out
@@ -521,34 +463,24 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entropy=N
     and its top_k most likely tokens (wq4_token_logprobs). Returns (logprobs [T] or None, entropy [T], top_ids
     int32 [T][top_k], top_logprobs [T][top_k]); the last two are None with top_k = 0. Buffers that are
     not given are allocated."""
-    lib = _types() if _t is None or _lib is None else _lib
-    T, V, code, dev = _two_d(logits, "logits", _OUT)
-    lp, ld = _rows(logits, "logits", T, V, logits.dtype, dev)
-    if T == 1:
-        ld = V
-    tp = lpp = tip = tlp = None
-    if tokens is not None:
-        tp = _vector(tokens, "tokens", T, _t.int64, dev)
-        if logprobs is None:
-            logprobs = _t.empty(T, dtype=_F32, device=logits.device)
-        lpp = _vector(logprobs, "logprobs", T, _F32, dev)
-    elif logprobs is not None:
+    if _bound is not _lib or _lib is None:
+        _bind()
+    if entropy is None or (tokens is not None and logprobs is None) or (top_k > 0 and (top_ids is None or top_logprobs is None)):
+        torch = _torch()
+        T, dev = logits.shape[0], logits.device
+        if entropy is None:
+            entropy = torch.empty(T, dtype=torch.float32, device=dev)
+        if tokens is not None and logprobs is None:
+            logprobs = torch.empty(T, dtype=torch.float32, device=dev)
+        if top_k > 0 and top_ids is None:
+            top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        if top_k > 0 and top_logprobs is None:
+            top_logprobs = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    if tokens is None and logprobs is not None:
         raise ValueError("logprobs needs tokens")
-    if entropy is None:
-        entropy = _t.empty(T, dtype=_F32, device=logits.device)
-    ep = _vector(entropy, "entropy", T, _F32, dev)
-    if top_k > 0:
-        if top_ids is None:
-            top_ids = _t.empty((T, top_k), dtype=_t.int32, device=logits.device)
-        if top_logprobs is None:
-            top_logprobs = _t.empty((T, top_k), dtype=_F32, device=logits.device)
-        tip, ldi = _rows(top_ids, "top_ids", T, top_k, _t.int32, dev)
-        tlp, ldl = _rows(top_logprobs, "top_logprobs", T, top_k, _F32, dev)
-        if T > 1 and (ldi != top_k or ldl != top_k):
-            raise ValueError("top_ids and top_logprobs must be contiguous")
-    elif top_ids is not None or top_logprobs is not None:
+    if top_k <= 0 and (top_ids is not None or top_logprobs is not None):
         raise ValueError("top_ids and top_logprobs need top_k")
-    rc = lib.wq4_token_logprobs(lp, ld, tp, T, V, code, top_k, lpp, ep, tip, tlp, _raw_stream(dev))
+    rc = _binding.token_logprobs(logits, tokens, top_k, logprobs, entropy, top_ids, top_logprobs)
     if rc:
         raise Wq4Error(rc, "wq4_token_logprobs")
     return logprobs, entropy, top_ids, top_logprobs
