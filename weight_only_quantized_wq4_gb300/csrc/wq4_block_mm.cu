@@ -17,13 +17,12 @@
 //   warps 0, 2   copies: per block of K, one operand's 128-byte row pieces each as a 2-D tensor copy with
 //                the 128-byte swizzle (rows and K past the end read as zero), into a ring of stages. A
 //                thread alone cannot issue both operands' copies as fast as a block is used.
-//   warps 1, 3   MMAs: one thread each, taking steps (one block, or two with few tokens) in turn; four
-//                MMAs (K = 32) a block, then a commit to the fold warps. One thread issues an MMA in
-//                46 cycles and needs some 75 for each wait and commit besides, so that its own step of
-//                narrow MMAs takes longer than the tensor core does; two overlap.
+//   warps 1, 3   MMAs: one thread each, taking blocks in turn; four MMAs (K = 32) a block, then a commit
+//                to the fold warps. A thread issues an MMA in 46 cycles and needs some 75 for each wait
+//                and commit besides, longer than the tensor core takes for narrow tiles; two overlap.
 //   warps 4+     fold: read P_b, add it in, at a tile's end round once and store
-// With fewer tiles than SMs, a cluster of CTAs shares each tile, cut along K; the parts are added in
-// rank order through distributed shared memory.
+// With fewer tiles than SMs, a cluster of CTAs shares each tile, cut along K; the parts are sent
+// through distributed shared memory to the CTA that joins them, which adds them in rank order.
 //
 // Every wait is bounded, as in wq4_gemm.cuh: one that runs out is recorded in the status word and the
 // CTA drains its copies and MMAs, frees its tensor memory and returns.
@@ -51,6 +50,8 @@ struct BmArgs {
     int M, N, kb;                              // kb: blocks of K
     int lane_tiles, tiles;                     // tile t: lane tile t % lane_tiles, column tile t / lane_tiles
     int split;                                 // CTAs per cluster, each with a part of K (1: none)
+    int stages;                                // of the ring: an even number
+    int red_cols, red_shift;                   // split: columns of a tile that are joined, and by how many (2^shift) per CTA
     int dtype;
     int unit;                                  // bytes that a row of Y is stored by: 16, or what its start allows
     unsigned int* status;
@@ -62,8 +63,7 @@ struct BmArgs {
 // share each tile of 256 lanes, 128 lanes and half the columns' copies each (cta_group::2).
 template <int NT, bool TOK_LANES, bool PAIR>
 struct BmCfg {
-    static constexpr int kG = TOK_LANES ? 1 : 2;                // blocks of K per step of the pipeline
-    static constexpr int kAhead = 2 * kG;                       // blocks whose scales are loaded together, one such group ahead
+    static constexpr int kAhead = 4;                            // blocks whose scales are loaded together, one such group ahead
     static constexpr int kFW = TOK_LANES ? 8 : 4;               // fold warps
     static constexpr int kParts = kFW / 4;                      // fold warps per lane quarter
     static constexpr int kNC = NT / kParts;                     // columns of a fold thread
@@ -72,31 +72,30 @@ struct BmCfg {
     static constexpr int kColRows = PAIR ? NT / 2 : NT;         // rows of the column operand a CTA copies
     static constexpr int kColBytes = kColRows * kBmBlock;
     static constexpr int kTokens = TOK_LANES ? kBmLanes : NT;
-    static constexpr int kBlockBytes = kLaneBytes + kColBytes;
-    static constexpr int kStageBytes = kG * kBlockBytes;
+    static constexpr int kStageBytes = kLaneBytes + kColBytes;
     static constexpr int kBarBytes = 1024;
     // per fold warp: rows of an output chunk on their way to coalesced stores, 32 of 64 + 16 bytes (tokens on
-    // the lanes), or the factors of a step's tokens, twice
-    static constexpr int kWarpBytes = TOK_LANES ? 32 * 80 : 2 * kG * NT * 4;
+    // the lanes), or the factors of a block's tokens, twice
+    static constexpr int kWarpBytes = TOK_LANES ? 32 * 80 : 2 * NT * 4;
     // tokens on the lanes: the tokens' scales of 8 blocks at a time come as one copy, in a ring of their own
     static constexpr int kScBlocks = 8, kScRing = TOK_LANES ? 3 : 0, kScBytes = kScBlocks * kBmLanes * 4;
-    // An even number of stages and of P buffers: the MMA warps take alternate steps, so each walks every
-    // phase of its own ones (a parity wait is unambiguous one phase ahead only).
-    static constexpr int kFit = (kBmMaxSmem - 1024 - kBarBytes - kScRing * kScBytes - kFW * kWarpBytes) / kStageBytes;
-    static constexpr int kStages = (kFit > 12 ? 12 : kFit) & ~1;
-    static constexpr int kPCols = kG * NT;                      // tensor-memory columns of a step's P buffer
-    static constexpr int kPBufs = kPCols <= 128 ? 4 : 2;
-    static constexpr int kTmemCols = kPCols * kPBufs > 256 ? 512 : kPCols * kPBufs;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kScRing * kScBytes + kBarBytes + kFW * kWarpBytes;
+    // An even number of stages (fit) and of P buffers: the MMA warps take alternate blocks, so each walks
+    // every phase of its own ones (a parity wait is unambiguous one phase ahead only).
+    // Shared memory before the stages, and the parts of a tile that other CTAs of a cluster send (kRedBytes)
+    static constexpr int kHeadBytes = 128 + 1024 + kBarBytes + kScRing * kScBytes + kFW * kWarpBytes;
+    static constexpr int kRedBytes = PAIR ? 0 : NT * kBmLanes * 4;
+    static constexpr int fit(int red) { return ((kBmMaxSmem - kHeadBytes - red) / kStageBytes > 12 ? 12 : (kBmMaxSmem - kHeadBytes - red) / kStageBytes) & ~1; }
+    static constexpr int kHalfStages = ((115712 - kHeadBytes) / kStageBytes) & ~1;   // two CTAs of an SM: that many bytes each
+    static constexpr int kPBufs = NT <= 128 ? 4 : 2;
+    static constexpr int kTmemCols = NT * kPBufs > 256 ? 512 : NT * kPBufs;
     // 128 fp32 accumulators per fold thread want more registers than an even share: 384 threads
     // launched with 168 each (64512 in all), of which the copy and MMA warps keep 56 and the fold
     // warps take 224 (128 x 56 + 256 x 224 = 64512).
     static constexpr bool kRegSplit = kNC > 64;
     static constexpr int kLaunchRegs = 168, kRegWg0 = 56, kRegFold = 224;
     static_assert(!kRegSplit || 128 * kRegWg0 + 32 * kFW * kRegFold <= kThreads * kLaunchRegs, "register split");
-    static_assert(kStages >= 4 && kTmemCols <= 512 && kSmemBytes <= kBmMaxSmem, "tile");
-    static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kAhead % kG == 0, "tensor memory, steps");
-    static_assert(PAIR || kStages * kStageBytes >= kBmLanes * NT * 4, "cluster reduction buffer");
+    static_assert(fit(kRedBytes) >= 4 && fit(0) <= 16 && kTmemCols <= 512, "tile");
+    static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
     static_assert(!PAIR || (TOK_LANES && kPBufs == 2), "pairs");
 };
 
@@ -147,6 +146,12 @@ __device__ __forceinline__ void bm_commit(uint32_t bar) {
         mma_commit(bar);
     }
 }
+// One value to shared memory of a CTA of the cluster; its bytes count on that CTA's barrier.
+__device__ __forceinline__ void st_async(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+                 "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_leader(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, 0)) : "memory");
 }
@@ -185,9 +190,6 @@ __device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, co
 
 // kind::f8f6f4: D fp32, A and B e4m3 (format code 0), both K-major, M x N.
 __device__ constexpr uint32_t f8_idesc(uint32_t M, uint32_t N) { return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24); }
-
-__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
-__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
 
 // (d0, d1) += (f0, f1) * (v0, v1), one packed fp32 FMA.
 __device__ __forceinline__ void fma_pair(float& d0, float& d1, float f0, float f1, uint32_t v0, uint32_t v1) {
@@ -241,14 +243,19 @@ __device__ __forceinline__ void copy_rows(const BmArgs& a, uint32_t buf, int lan
     const int cols = a.N - n - c, rows = a.M - m0;   // what exists from here on
     uint8_t* to = static_cast<uint8_t*>(a.y) + ((m0 + r0) * a.ldy + n + c) * SIZE;
     const long long step = a.ldy * (kRows * SIZE);
-    uint32_t from = buf + r0 * 80 + c * SIZE;
+    const uint32_t from = buf + r0 * 80 + c * SIZE;
+    if (rows >= 32 && a.N - n >= CNT) {              // all of it exists
 #pragma unroll
-    for (int r = r0; r < 32; r += kRows, to += step, from += kRows * 80) {
-        if (r >= rows) break;
+        for (int p = 0; p < 32 / kRows; ++p) copy_unit<UNIT>(to + p * step, from + p * kRows * 80);
+        return;
+    }
+#pragma unroll 1
+    for (int p = 0; p < 32 / kRows; ++p, to += step) {
+        if (r0 + p * kRows >= rows) break;
         if (cols >= kIn) {
-            copy_unit<UNIT>(to, from);
+            copy_unit<UNIT>(to, from + p * kRows * 80);
         } else {                                     // the row ends inside the unit
-            for (int j = 0; j < cols; ++j) copy_unit<SIZE>(to + j * SIZE, from + j * SIZE);
+            for (int j = 0; j < cols; ++j) copy_unit<SIZE>(to + j * SIZE, from + p * kRows * 80 + j * SIZE);
         }
     }
 }
@@ -288,11 +295,11 @@ __device__ __forceinline__ void store_rows(const BmArgs& a, uint32_t buf, int la
     }
 }
 
-// One column n of Y per lane, CNT tokens from m: neighbouring lanes' columns are neighbours in memory.
+// One column n of Y per lane, `rows` tokens (CNT at most) from m: neighbouring lanes' columns are neighbours
+// in memory.
 template <int CNT>
-__device__ __forceinline__ void store_cols(const BmArgs& a, int m, int n, const float* v) {
+__device__ __forceinline__ void store_cols(const BmArgs& a, int m, int rows, int n, const float* v) {
     if (n >= a.N) return;
-    const int rows = a.M - m;
     const long long at = m * a.ldy + n;
     if (a.dtype == WQ4_FP32) {
         float* y = static_cast<float*>(a.y) + at;
@@ -326,23 +333,24 @@ struct BmSched {
 };
 
 template <int NT, bool TOK_LANES, bool PAIR>
-__global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
+__global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LANES && NT <= 32 ? 2 : 1)
     block_mm_kernel(const __grid_constant__ BmArgs a) {
     using C = BmCfg<NT, TOK_LANES, PAIR>;
     constexpr int kTileLanes = PAIR ? 2 * kBmLanes : kBmLanes, kAhead = C::kAhead;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
-    const uint32_t s_ring = (raw_s + 1023u) & ~1023u;
-    const uint32_t s_sc = s_ring + C::kStages * C::kStageBytes;      // token scales
-    const uint32_t s_bar = s_sc + C::kScRing * C::kScBytes;
+    const uint32_t s_bar = (raw_s + 127u) & ~127u;
+    const uint32_t s_sc = s_bar + C::kBarBytes;                       // token scales
+    const uint32_t s_warp = s_sc + C::kScRing * C::kScBytes;          // the fold warps' buffers
+    const uint32_t s_ring = (s_warp + C::kFW * C::kWarpBytes + 1023u) & ~1023u;
+    const uint32_t s_red = s_ring + a.stages * C::kStageBytes;        // parts from the cluster's CTAs
     auto full_bar = [&](int s) { return s_bar + 8u * s; };
     auto empty_bar = [&](int s) { return s_bar + 8u * (16 + s); };
-    const uint32_t s_warp = s_bar + C::kBarBytes;    // the fold warps' buffers
     auto pfull_bar = [&](int b) { return s_bar + 8u * (32 + b); };
     auto pempty_bar = [&](int b) { return s_bar + 8u * (36 + b); };
     auto scfull_bar = [&](int c) { return s_bar + 8u * (40 + c); };
     auto scempty_bar = [&](int c) { return s_bar + 8u * (44 + c); };
-    const uint32_t drain_bar = s_bar + 8u * 48, stall_bar = s_bar + 8u * 49;
+    const uint32_t drain_bar = s_bar + 8u * 48, stall_bar = s_bar + 8u * 49, red_bar = s_bar + 8u * 50;
     uint8_t* const gmisc = smem_raw + (s_bar - raw_s) + 8 * 56;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gmisc);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(gmisc + 4);
@@ -352,7 +360,7 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
     const int lane0 = PAIR ? rank * kBmLanes : 0;    // this CTA's first lane of a tile
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < a.stages; ++s) {
             mbar_init(full_bar(s), PAIR && rank == 0 ? 3 : 2);   // both operands' copies (and the other CTA's)
             mbar_init(empty_bar(s), 1);
         }
@@ -366,6 +374,11 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
         }
         mbar_init(drain_bar, 2);                     // one commit from each MMA warp
         mbar_init(stall_bar, 1);
+        if (!PAIR && a.split > 1) {                  // the bytes of the parts of this CTA's columns
+            mbar_init(red_bar, 1);
+            const int own = min(max(a.red_cols - (rank << a.red_shift), 0), 1 << a.red_shift);
+            mbar_arrive_expect_tx(red_bar, own * a.split * kBmLanes * 4);
+        }
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&a.lane_map);
@@ -376,9 +389,9 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
         bm_tmem_alloc<PAIR>(smem_u32(tmem_slot), C::kTmemCols);
     }
     tc_fence_before();
-    if constexpr (PAIR) {
+    if (PAIR || a.split > 1) {
         __syncwarp();
-        cluster_sync();                              // (the other CTA's barriers are set up too)
+        cluster_sync();                              // (the other CTAs' barriers are set up too)
     } else {
         __syncthreads();
     }
@@ -404,7 +417,7 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
                 for (BmSched s(a, rank, PAIR); s.t < a.tiles && ok; s.t += s.step) {
                     const int row = lanes ? s.t % a.lane_tiles * kTileLanes + lane0
                                           : s.t / a.lane_tiles * NT + (PAIR ? rank * C::kColRows : 0);
-                    for (int b = s.kb0; b < s.kb1; b += C::kG, ++i) {
+                    for (int b = s.kb0; b < s.kb1; ++b, ++i) {
                         if (TOK_LANES && warp == 2 && (b - s.kb0) % C::kScBlocks == 0) {
                             if (!mbar_wait(scempty_bar(sc), sc_phase, ctl)) { ok = false; break; }
                             mbar_arrive_expect_tx(scfull_bar(sc), C::kScBytes);
@@ -414,14 +427,9 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
                             if (++sc == C::kScRing) { sc = 0; sc_phase ^= 1; }
                         }
                         if (!mbar_wait(empty_bar(st), phase, ctl)) { ok = false; break; }
-                        const int n = min(C::kG, s.kb1 - b);
-                        mbar_arrive_expect_tx(full_bar(st), n * bytes);
-#pragma unroll
-                        for (int g = 0; g < C::kG; ++g)
-                            if (g < n)
-                                tma_load_2d(dst + st * C::kStageBytes + g * C::kBlockBytes, map, full_bar(st),
-                                            (b + g) * kBmBlock, row, policy);
-                        if (++st == C::kStages) { st = 0; phase ^= 1; }
+                        mbar_arrive_expect_tx(full_bar(st), bytes);
+                        tma_load_2d(dst + st * C::kStageBytes, map, full_bar(st), b * kBmBlock, row, policy);
+                        if (++st == a.stages) { st = 0; phase ^= 1; }
                     }
                 }
                 issued = i;
@@ -437,7 +445,7 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
                     for (int b = s.kb0; b < s.kb1; ++b) {
                         if (!mbar_wait(full_bar(st), full, ctl)) { ok = false; break; }
                         mbar_arrive_leader(full_bar(st));
-                        if (++st == C::kStages) { st = 0; full ^= 1; }
+                        if (++st == a.stages) { st = 0; full ^= 1; }
                     }
                 }
             }
@@ -448,33 +456,28 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
                 auto wait = [&](uint32_t bar, uint32_t parity) {
                     return PAIR ? mbar_wait_pair(bar, parity, ctl) : mbar_wait(bar, parity, ctl);
                 };
-                const int mine = warp >> 1;          // this thread's steps: the even or the odd ones
+                const int mine = warp >> 1;          // this thread's blocks: the even or the odd ones
                 bool ok = !(a.test_stall && mine == 0) || mbar_wait(stall_bar, 0, ctl);
                 const uint64_t desc0 = make_sdesc_sw128(s_ring);
                 int st = mine, p = mine, skip = mine;
                 uint32_t full = 0, free = 1;         // phase parities
                 for (BmSched s(a, rank, PAIR); s.t < a.tiles && ok; s.t += s.step) {
-                    int b = s.kb0 + skip * C::kG;
-                    for (; b < s.kb1; b += 2 * C::kG) {
+                    int b = s.kb0 + skip;
+                    for (; b < s.kb1; b += 2) {
                         if (!wait(full_bar(st), full)) { ok = false; break; }
                         if (!wait(pempty_bar(p), free)) { ok = false; break; }
                         tc_fence_after();
                         const uint64_t desc = desc0 + static_cast<uint32_t>(st * (C::kStageBytes >> 4));
-                        const uint32_t d = tmem + p * C::kPCols;
+                        const uint32_t d = tmem + p * NT;
 #pragma unroll
-                        for (int g = 0; g < C::kG; ++g) {
-                            if (b + g >= s.kb1) break;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f8<PAIR>(d + g * NT, desc + (g * (C::kBlockBytes >> 4) + 2 * k),
-                                       desc + (g * (C::kBlockBytes >> 4) + (C::kLaneBytes >> 4) + 2 * k), idesc, k > 0);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            mma_f8<PAIR>(d, desc + 2 * k, desc + (C::kLaneBytes >> 4) + 2 * k, idesc, k > 0);
                         bm_commit<PAIR>(pfull_bar(p));
                         bm_commit<PAIR>(empty_bar(st));
-                        if ((st += 2) >= C::kStages) { st = mine; full ^= 1; }
+                        if ((st += 2) >= a.stages) { st = mine; full ^= 1; }
                         if ((p += 2) >= C::kPBufs) { p = mine; free ^= 1; }
                     }
-                    skip = (b - s.kb1) / C::kG;      // (the turns go on over the tiles' ends)
+                    skip = b - s.kb1;                // (the turns go on over the tiles' ends)
                 }
                 bm_commit<PAIR>(drain_bar);               // every MMA is done before the tensor memory goes
                 mbar_wait_plain(drain_bar, 0, drain_limit(a.timeout_cycles));
@@ -514,16 +517,16 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
                     }
                     const float f = lds_f32(s_sc + sc * C::kScBytes + (b % C::kScBlocks) * (kBmLanes * 4) + 4 * r) *
                                     __shfl_sync(0xffffffffu, w32, b % 32);
-                    const uint32_t from = t_addr + p * C::kPCols, freed = pempty_bar(p);
+                    const uint32_t from = t_addr + p * NT, freed = pempty_bar(p);
                     if (!mbar_wait(pfull_bar(p), phase, ctl)) { ok = false; break; }
                     tc_fence_after();
-                    tmem_ldn(from, v[0]);
+                    tmem_ld16(from, v[0]);
                     if (++p == C::kPBufs) { p = 0; phase ^= 1; }
 #pragma unroll
                     for (int c = 0; c < kPieces; ++c) {
                         tmem_ld_wait();
                         if (c + 1 < kPieces) {
-                            tmem_ldn(from + (c + 1) * kCols, v[(c + 1) & 1]);
+                            tmem_ld16(from + (c + 1) * kCols, v[(c + 1) & 1]);
                         } else {                     // all of the block's P is in registers: the buffer is free
                             tc_fence_before();
                             __syncwarp();
@@ -543,19 +546,15 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
                     }
                 }
             } else {
-                // The tokens whose scales this thread loads (none past the last token: such values are not stored),
-                // and the scales of the kAhead blocks from `b` on; they are multiplied only when their turn
-                // comes, so that nothing waits for a load just issued.
-                constexpr int kCols = NT < 32 ? 16 : 32, kPieces = C::kNC / kCols;   // pieces of a block's P per thread
-                constexpr int kPer = (NT + 31) / 32;     // tokens per lane
-                const int token = c0 + lane;
-                const bool loads = token < a.M && lane < NT;
-                const bool loads2 = kPer > 1 && token + 32 < a.M;
-                float nsx[kAhead * kPer], nsw[kAhead];
-                const float *px = a.sx + token + s.kb0 * a.ldsx, *pw = sw + s.kb0;
-#pragma unroll
-                for (int j = 0; j < kAhead * kPer; ++j) nsx[j] = 0.f;
-                auto load_scales = [&](int n) {          // of the next n blocks (kAhead at most)
+                // A lane loads the scales of one token (two at NT = 64; none past the last token, whose values are
+                // not stored), kAhead blocks at a time and one such group ahead; they are multiplied only
+                // when their turn comes, so that nothing waits for a load just issued. A block's factors
+                // then go to shared memory, where every lane reads all of them.
+                constexpr int kCols = 16, kPieces = NT / kCols, kPer = (NT + 31) / 32;
+                const bool loads = c0 + lane < a.M && lane < NT, loads2 = kPer > 1 && c0 + lane + 32 < a.M;
+                const float *px = a.sx + (c0 + lane) + s.kb0 * a.ldsx, *pw = sw + s.kb0;
+                float nsx[kAhead * kPer] = {}, nsw[kAhead] = {};
+                auto load_scales = [&](int n) {      // of the next n blocks (kAhead at most)
 #pragma unroll
                     for (int j = 0; j < kAhead; ++j, px += a.ldsx) {
                         if (j >= n) break;
@@ -567,67 +566,48 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
                     pw += kAhead;
                 };
 #pragma unroll
-                for (int j = 0; j < C::kNC; ++j) acc[j] = 0.f;
-                load_scales(s.kb1 - s.kb0);
+                for (int j = 0; j < NT; ++j) acc[j] = 0.f;
                 uint32_t v[2][kCols];
-                bool primed = false;                     // the step's first piece of P is on its way
-                __syncwarp();                            // (no lane still reads the last tile's factors)
+                load_scales(s.kb1 - s.kb0);
+                __syncwarp();                        // (no lane still reads the last tile's factors)
                 for (int b0 = s.kb0; b0 < s.kb1 && ok; b0 += kAhead) {
                     float f[kAhead * kPer];
 #pragma unroll
                     for (int j = 0; j < kAhead * kPer; ++j) f[j] = nsx[j] * nsw[j / kPer];
                     load_scales(s.kb1 - b0 - kAhead);
 #pragma unroll
-                    for (int j = 0; j < kAhead; j += C::kG) {
+                    for (int j = 0; j < kAhead; ++j) {
                         if (b0 + j >= s.kb1) break;
-                        const uint32_t factors = buf + (j / C::kG & 1) * (C::kG * NT * 4);
+                        const uint32_t factors = buf + (j & 1) * (NT * 4);
 #pragma unroll
-                        for (int g = 0; g < C::kG; ++g)  // the step's factors, where every lane can read them
-#pragma unroll
-                            for (int q = 0; q < kPer; ++q)
-                                if (lane + 32 * q < NT)
-                                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(factors + (g * NT + lane + 32 * q) * 4),
-                                                 "f"(f[(j + g) * kPer + q])
-                                                 : "memory");
+                        for (int q = 0; q < kPer; ++q)
+                            if (lane + 32 * q < NT)
+                                asm volatile("st.shared.f32 [%0], %1;" ::"r"(factors + (lane + 32 * q) * 4), "f"(f[j * kPer + q])
+                                             : "memory");
                         __syncwarp();
-                        // the step's columns of P, in pieces: the next piece is read while this one is added in. (A step's
-                        // second block past the end of K is left out: its buffer holds an earlier step's values.)
-                        const int pieces = kPieces * (C::kG == 1 || b0 + j + 1 < s.kb1 ? C::kG : 1);
-                        if (!primed) {
-                            if (!mbar_wait(pfull_bar(p), phase, ctl)) { ok = false; break; }
-                            tc_fence_after();
-                            tmem_ldn(t_addr + p * C::kPCols, v[0]);
-                        }
-                        const int p0 = p;
+                        if (!mbar_wait(pfull_bar(p), phase, ctl)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t from = t_addr + p * NT, freed = pempty_bar(p);
                         if (++p == C::kPBufs) { p = 0; phase ^= 1; }
-                        bool next = false;
+                        tmem_ld16(from, v[0]);
 #pragma unroll
-                        for (int c = 0; c < kPieces * C::kG; ++c) {
-                            if (c >= pieces) break;
-                            uint32_t(&now)[kCols] = v[c & 1];
-                            const int g = c / kPieces, at = c % kPieces * kCols;
+                        for (int c = 0; c < kPieces; ++c) {
                             tmem_ld_wait();
-                            if (c + 1 < pieces) {
-                                tmem_ldn(t_addr + p0 * C::kPCols + (c + 1) / kPieces * NT + (c + 1) % kPieces * kCols, v[c + 1 & 1]);
-                            } else {                     // all of the step's P is in registers: the buffer is free
+                            if (c + 1 < kPieces) {
+                                tmem_ld16(from + (c + 1) * kCols, v[(c + 1) & 1]);
+                            } else {                 // all of the block's P is in registers: the buffer is free
                                 tc_fence_before();
                                 __syncwarp();
-                                if (lane == 0) mbar_arrive(pempty_bar(p0));
-                                // (whether the next step is there already, asked while this piece is added in)
-                                next = c % 2 == 1 && b0 + j + C::kG < s.kb1 && mbar_test(pfull_bar(p), phase);
+                                if (lane == 0) mbar_arrive(freed);
                             }
 #pragma unroll
                             for (int q = 0; q < kCols; q += 4) {
-                                const uint4 u = lds128(factors + (g * NT + at + q) * 4);
-                                const float w[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-                                fma_pair(acc[at + q], acc[at + q + 1], w[0], w[1], now[q], now[q + 1]);
-                                fma_pair(acc[at + q + 2], acc[at + q + 3], w[2], w[3], now[q + 2], now[q + 3]);
+                                const uint4 w = lds128(factors + (c * kCols + q) * 4);
+                                float* d = acc + c * kCols + q;
+                                const uint32_t* x = v[c & 1] + q;
+                                fma_pair(d[0], d[1], __uint_as_float(w.x), __uint_as_float(w.y), x[0], x[1]);
+                                fma_pair(d[2], d[3], __uint_as_float(w.z), __uint_as_float(w.w), x[2], x[3]);
                             }
-                        }
-                        primed = __all_sync(0xffffffffu, next);
-                        if (primed) {
-                            tc_fence_after();
-                            tmem_ldn(t_addr + p * C::kPCols, v[0]);
                         }
                     }
                 }
@@ -637,46 +617,42 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
             if constexpr (TOK_LANES) {
                 store_rows<C::kNC>(a, buf, lane, l0 + 32 * quarter, c0 + col0, acc);
             } else {
-                store_cols<C::kNC>(a, c0 + col0, l0 + r, acc);
+                store_cols<C::kNC>(a, c0 + col0, a.M - c0 - col0, l0 + r, acc);
             }
         }
         if (!PAIR && a.split > 1) {
-            // This CTA's part, [column][lane], over the ring: its MMAs and with them its copies are done. (Of
-            // a CTA that gave up the parts are undefined, as its outputs are; its copies still land in its
-            // own shared memory.)
+            // Every CTA sends its part of each column to the CTA that joins it (to itself too), which adds the
+            // ranks' parts in order once all their bytes have come. (A CTA that gave up sends what it has.)
 #pragma unroll
-            for (int j = 0; j < C::kNC; ++j)
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_ring + ((col0 + j) * kBmLanes + r) * 4), "f"(acc[j])
-                             : "memory");
-        }
-    }
-    if (!PAIR && a.split > 1) {
-        __syncwarp();
-        cluster_sync();                              // every part of the tile is in its CTA's shared memory
-        if (warp >= 4) {
-            const int t = blockIdx.x / a.split;      // (one tile per cluster)
-            const int l0 = t % a.lane_tiles * kBmLanes, c0 = t / a.lane_tiles * NT;
-            const int r = 32 * (warp & 3) + lane;
-            // a few columns at a time, dealt out over the ranks and their warps
-            constexpr int kCnt = TOK_LANES ? 16 : 8;
-            for (int j = (rank * C::kParts + ((warp - 4) >> 2)) * kCnt; j < NT; j += a.split * C::kParts * kCnt) {
-                float v[kCnt];
+            for (int j = 0; j < C::kNC; ++j) {
+                const int col = col0 + j, owner = col >> a.red_shift, at = col & ((1 << a.red_shift) - 1);
+                if (col >= a.red_cols) break;
+                st_async(map_to_rank(s_red + ((((rank << a.red_shift) + at) * kBmLanes) + r) * 4, owner), acc[j],
+                         map_to_rank(red_bar, owner));
+            }
+            const int first = rank << a.red_shift, own = min(a.red_cols - first, 1 << a.red_shift);
+            if (own > 0 && mbar_wait(red_bar, 0, ctl)) {
+                const int t = blockIdx.x / a.split;  // (one tile per cluster)
+                const int l0 = t % a.lane_tiles * kBmLanes, c0 = t / a.lane_tiles * NT;
+                constexpr int kCnt = TOK_LANES ? 16 : 4;
+                for (int c = part * kCnt; c < own; c += C::kParts * kCnt) {
+                    float v[kCnt];
 #pragma unroll
-                for (int q = 0; q < kCnt; ++q) v[q] = 0.f;
-                for (int o = 0; o < a.split; ++o) {
-                    const uint32_t base = map_to_rank(s_ring, o);
+                    for (int q = 0; q < kCnt; ++q) v[q] = 0.f;
+                    for (int o = 0; o < a.split; ++o) {
+                        const uint32_t from = s_red + ((((o << a.red_shift) + c) * kBmLanes) + r) * 4;
 #pragma unroll
-                    for (int q = 0; q < kCnt; ++q) v[q] += ld_cluster_f32(base + ((j + q) * kBmLanes + r) * 4);
-                }
-                if constexpr (TOK_LANES) {
-                    store_rows<kCnt>(a, s_warp + (warp - 4) * C::kWarpBytes, lane, l0 + r - lane, c0 + j, v);
-                } else {
-                    store_cols<kCnt>(a, c0 + j, l0 + r, v);
+                        for (int q = 0; q < kCnt; ++q)
+                            if (c + q < own) v[q] += lds_f32(from + q * (kBmLanes * 4));
+                    }
+                    if constexpr (TOK_LANES) {
+                        store_rows<kCnt>(a, buf, lane, l0 + r - lane, c0 + first + c, v);
+                    } else {
+                        store_cols<kCnt>(a, c0 + first + c, own - c, l0 + r, v);
+                    }
                 }
             }
         }
-        __syncwarp();
-        cluster_sync();                              // no CTA leaves while another reads its part
     }
     if ((warp == 0 || warp == 2) && lane == 0) issued_by[warp >> 1] = issued;
     tc_fence_before();
@@ -690,6 +666,12 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
         tc_fence_after();
         bm_tmem_dealloc<PAIR>(tmem, C::kTmemCols);
     }
+    // A CTA whose parts all came is sent nothing more. One that gave up stays until the others, which may still
+    // send to it, have gone or given up too.
+    if (!PAIR && a.split > 1 && *abort_flag) {
+        __syncwarp();
+        cluster_sync();
+    }
     if constexpr (TOK_LANES) {
         if (warp == 2 && lane == 0 && *abort_flag)
             for (int j = sc_issued > C::kScRing ? sc_issued - C::kScRing : 0; j < sc_issued; ++j)
@@ -699,12 +681,12 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, 1)
     // of the other, its arrivals are made up for first, so that the other's stages complete.
     if (warp == 0 && lane == 0 && *abort_flag) {
         const int less = min(issued_by[0], issued_by[1]), more = max(issued_by[0], issued_by[1]);
-        for (int j = less; j < more; ++j) mbar_arrive(full_bar(j % C::kStages));
+        for (int j = less; j < more; ++j) mbar_arrive(full_bar(j % a.stages));
         if (PAIR && rank == 0)                       // (nor can it be told whether the other CTA's arrivals came)
-            for (int j = more > C::kStages ? more - C::kStages : 0; j < more; ++j)
-                if (!mbar_test(full_bar(j % C::kStages), (j / C::kStages) & 1)) mbar_arrive(full_bar(j % C::kStages));
-        for (int j = more > C::kStages ? more - C::kStages : 0; j < more; ++j)
-            mbar_wait_plain(full_bar(j % C::kStages), (j / C::kStages) & 1, drain_limit(a.timeout_cycles));
+            for (int j = more > a.stages ? more - a.stages : 0; j < more; ++j)
+                if (!mbar_test(full_bar(j % a.stages), (j / a.stages) & 1)) mbar_arrive(full_bar(j % a.stages));
+        for (int j = more > a.stages ? more - a.stages : 0; j < more; ++j)
+            mbar_wait_plain(full_bar(j % a.stages), (j / a.stages) & 1, drain_limit(a.timeout_cycles));
     }
 }
 
@@ -732,7 +714,7 @@ int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) 
     if (regs < 0) {
         cudaFuncAttributes fa;
         if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBmMaxSmem) != cudaSuccess)
             return WQ4_ERR_CUDA;
         regs = fa.numRegs;
     }
@@ -754,12 +736,23 @@ int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) 
     a.tiles = static_cast<int>(tiles);
     a.split = 1;
     while (!PAIR && a.split < 8 && 2 * a.split * tiles <= rt.sm_count && 2 * a.split <= a.kb) a.split *= 2;
-    const int most = PAIR ? rt.sm_count / 2 : rt.sm_count;   // tiles at a time
+    // More narrow tiles than SMs (and no whole number of waves of them): rings of half the size, two CTAs per SM
+    // (4 x 28672 x 4096: 21.1 us; one CTA with the whole ring 23.6).
+    constexpr bool kHalf = !TOK_LANES && NT <= 32;
+    const bool half = kHalf && tiles > rt.sm_count;
+    const int most = PAIR ? rt.sm_count / 2 : half ? 2 * rt.sm_count : rt.sm_count;   // tiles at a time
     const int grid = PAIR ? 2 * (a.tiles < most ? a.tiles : most) : a.split > 1 ? a.tiles * a.split : a.tiles < most ? a.tiles : most;
+    // no more stages than a CTA has blocks: with few, the next launch's CTAs fit beside this one's
+    const int red = a.split > 1 ? C::kRedBytes : 0, blocks = (a.kb + a.split - 1) / a.split;
+    a.stages = half ? C::kHalfStages : C::fit(red);
+    if (a.split > 1 && blocks < a.stages) a.stages = blocks < 4 ? 4 : (blocks + 1) & ~1;
+    const int smem = C::kHeadBytes + a.stages * C::kStageBytes + red;
+    a.red_cols = TOK_LANES || a.M > NT ? NT : a.M;
+    while ((a.split << a.red_shift) < a.red_cols) ++a.red_shift;
     if (rt.trace)
         std::fprintf(stderr, "wq4: block_mm M=%d N=%d K=%d lanes=%s columns=%d pair=%d grid=%d split=%d\n", a.M, a.N, c.K,
                      TOK_LANES ? "tokens" : "weights", NT, PAIR ? 1 : 0, grid, a.split);
-    return launch(rt, kern, dim3(grid), C::kThreads, C::kSmemBytes, PAIR ? 2 : a.split, st, a);
+    return launch(rt, kern, dim3(grid), C::kThreads, smem, PAIR ? 2 : a.split, st, a);
 }
 
 }  // namespace
