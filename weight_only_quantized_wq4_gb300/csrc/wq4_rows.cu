@@ -119,7 +119,9 @@ struct NormArgs {
 };
 
 // One CTA per row; a thread holds VPT vectors of it in registers, so the row is read once although
-// its norm has to be known before the first value can be scaled.
+// its norm has to be known before the first value can be scaled. With one vector per thread (few rows: the
+// time is the latency of one row) the weight is loaded ahead of the sum; with two (many rows: 256 threads hold
+// a row of 4096) its registers are better spent on more rows per SM.
 template <bool BF16, bool VEC, int VPT>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
     __shared__ float part[32];
@@ -129,8 +131,9 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    float h[VPT][kVec];
+    float h[VPT][kVec], w0[kVec];
     float ss = 0.f;
+    if constexpr (VPT == 1) load8<BF16, VEC>(a.w, tid * kVec, D, w0);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int col = (i * blockDim.x + tid) * kVec;
@@ -161,9 +164,9 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
     for (int i = 0; i < VPT; ++i) {
         const int col = (i * blockDim.x + tid) * kVec;
         float w[kVec];
-        load8<BF16, VEC>(a.w, col, D, w);
+        if constexpr (VPT > 1) load8<BF16, VEC>(a.w, col, D, w);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) h[i][j] = h[i][j] * rstd * w[j];
+        for (int j = 0; j < kVec; ++j) h[i][j] = h[i][j] * rstd * (VPT == 1 ? w0[j] : w[j]);
         if (a.y) store8<BF16, VEC>(a.y + t * a.ldy, col, D, h[i]);
         if (a.q) quantise8<VEC>(h[i], col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
     }
@@ -172,7 +175,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
 template <bool BF16, bool VEC>
 int go_norm(const Runtime& rt, const NormArgs& a, int T, wq4_stream_t st) {
     const int nv = (a.D + kVec - 1) / kVec;
-    const int vpt = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4;
+    // Measured: 4096 x 4096 bf16 with the residual, one vector per thread 26.0 us, two 21.6, four 22.6; 1 x 4096
+    // 1.9 / 2.3 / 3.0 us; 517 x 2064 fp16 2.6 / 3.3 / 4.0 us.
+    const int fewest = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4;
+    const int vpt = fewest == 1 && nv > 256 && T > 4 * rt.sm_count ? 2 : fewest;
     const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
     switch (vpt) {
         case 1: return launch(rt, norm_kernel<BF16, VEC, 1>, dim3(T), threads, 0, 1, st, a);
@@ -192,23 +198,42 @@ struct GatedArgs {
     int D, chunks;                      // chunks: CTAs per row
 };
 
-constexpr int kGatedThreads = 256;
+constexpr int kGatedVecs = 256;         // vectors of each half that a CTA takes: 2048 columns of one row
 
-template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kGatedThreads) gated_kernel(const GatedArgs a) {
+// VPT vectors of each half per thread, all loaded before the first is used.
+template <bool BF16, bool VEC, int VPT>
+__global__ void __launch_bounds__(kGatedVecs / VPT) gated_kernel(const GatedArgs a) {
+    constexpr int kThreads = kGatedVecs / VPT;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long t = blockIdx.x / a.chunks;
-    const int col = ((blockIdx.x % a.chunks) * kGatedThreads + threadIdx.x) * kVec;
-    const int D = a.D;
+    const int D = a.D, col0 = ((blockIdx.x % a.chunks) * kGatedVecs + threadIdx.x) * kVec;
     const uint16_t* row = a.x + t * a.ldx;
-    float g[kVec], u[kVec];
-    load8<BF16, VEC>(row, col, D, g);
-    load8<BF16, VEC>(row + D, col, D, u);
-    // silu(g) = g / (1 + exp(-g)); where exp(-g) is infinite the quotient is the limit, 0
+    float g[VPT][kVec], u[VPT][kVec];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) g[j] = __fdividef(g[j], 1.f + __expf(-g[j])) * u[j];
-    quantise8<VEC>(g, col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
+    for (int i = 0; i < VPT; ++i) {
+        load8<BF16, VEC>(row, col0 + i * kThreads * kVec, D, g[i]);
+        load8<BF16, VEC>(row + D, col0 + i * kThreads * kVec, D, u[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int col = col0 + i * kThreads * kVec;
+        // silu(g) = g / (1 + exp(-g)); where exp(-g) is infinite the quotient is the limit, 0
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) g[i][j] = __fdividef(g[i][j], 1.f + __expf(-g[i][j])) * u[i][j];
+        quantise8<VEC>(g[i], col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
+    }
+}
+
+// With more CTAs than the SMs hold at once, 64 threads with four vectors each keep more loads under way
+// (4096 x 14336 bf16: 45.1 us; 128 with two 47.2, 256 with one 52.3); with fewer, one vector each is sooner
+// done (16 x 14336: 1.4 us against 2.0).
+template <bool BF16, bool VEC>
+int go_gated(const Runtime& rt, const GatedArgs& a, int T, wq4_stream_t st) {
+    const dim3 grid(static_cast<unsigned>(T) * a.chunks);
+    if (static_cast<long long>(T) * a.chunks > 8LL * rt.sm_count)
+        return launch(rt, gated_kernel<BF16, VEC, 4>, grid, kGatedVecs / 4, 0, 1, st, a);
+    return launch(rt, gated_kernel<BF16, VEC, 1>, grid, kGatedVecs, 0, 1, st, a);
 }
 
 // The quantised rows an operator writes and the product reads: rows of codes on 16-byte boundaries,
@@ -260,18 +285,14 @@ int wq4_silu_mul_quant(const void* X, long long ldx, int T, int D, int dtype, vo
     if (!X || ldx < 2LL * D) return WQ4_ERR_INVALID;
     if (!aligned_to(X, 2)) return WQ4_ERR_ALIGN;
     if (const int rc = check_rows(Q, ldq, scales, lds, T, D)) return rc;
-    const int chunks = (D + kGatedThreads * kVec - 1) / (kGatedThreads * kVec);
+    const int chunks = (D + kGatedVecs * kVec - 1) / (kGatedVecs * kVec);
     if (static_cast<long long>(T) * chunks > 0x7fffffffLL) return WQ4_ERR_UNSUPPORTED;
     Runtime rt;
     if (const int rc = runtime(&rt)) return rc;
     const GatedArgs a{static_cast<const uint16_t*>(X), static_cast<uint8_t*>(Q), scales, ldx, ldq, lds, D, chunks};
     const bool vec = D % kVec == 0 && vec_ok(X, ldx);
-    const dim3 grid(static_cast<unsigned>(T) * chunks);
-    if (dtype == WQ4_BF16)
-        return vec ? launch(rt, gated_kernel<true, true>, grid, kGatedThreads, 0, 1, stream, a)
-                   : launch(rt, gated_kernel<true, false>, grid, kGatedThreads, 0, 1, stream, a);
-    return vec ? launch(rt, gated_kernel<false, true>, grid, kGatedThreads, 0, 1, stream, a)
-               : launch(rt, gated_kernel<false, false>, grid, kGatedThreads, 0, 1, stream, a);
+    if (dtype == WQ4_BF16) return vec ? go_gated<true, true>(rt, a, T, stream) : go_gated<true, false>(rt, a, T, stream);
+    return vec ? go_gated<false, true>(rt, a, T, stream) : go_gated<false, false>(rt, a, T, stream);
 }
 
 }  // extern "C"
