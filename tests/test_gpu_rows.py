@@ -44,7 +44,9 @@ def make(T, D, dtype, seed, scale=1.0):
 
 
 SIZES = [(1, 1), (3, 7), (2, 8), (5, 120), (1, 128), (4, 129), (7, 136), (1, 4096), (33, 2064), (3, 4100), (2, 8192),
-         (3, 8200), (2, 16384), (1, 16385), (2, 32768), (300, 512)]
+         (3, 8200), (2, 16384), (1, 16385), (2, 32768), (300, 512),
+         # more rows than the SMs hold at once: a warp per row, two and four vectors per thread
+         (613, 1), (700, 250), (641, 507), (620, 4104), (611, 5003), (609, 8193), (609, 16380)]
 
 
 @pytest.mark.parametrize("T,D", SIZES)

@@ -8,8 +8,7 @@
 // value read back from it (q s) is NaN.
 //
 // Both are bound by memory: each element is read and written once, in 16-byte vectors of 8 elements
-// where sizes, strides and pointers allow (single elements otherwise), and everything in between
-// stays in registers. 16 neighbouring lanes hold one block of 128, so a block's maximum takes four
+// (across boundaries where rows do not start on one), and everything in between stays in registers. 16 neighbouring lanes hold one block of 128, so a block's maximum takes four
 // shuffles and no shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,36 +38,111 @@ __device__ __forceinline__ uint32_t from_f32(float v) {
     else return __half_as_ushort(__float2half_rn(v));
 }
 
-// Eight elements from column `col` of a row of D: one 16-byte load (VEC) or single ones; zeros past
-// the row's end.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void load8(const uint16_t* row, int col, int D, float (&v)[kVec]) {
-    if constexpr (VEC) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (col < D) w = *reinterpret_cast<const uint4*>(row + col);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint32_t (&u)[4], float (&v)[kVec]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = to_f32<BF16>(u[j] & 0xffffu);
-            v[2 * j + 1] = to_f32<BF16>(u[j] >> 16);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = col + j < D ? to_f32<BF16>(row[col + j]) : 0.f;
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = to_f32<BF16>(u[j] & 0xffffu);
+        v[2 * j + 1] = to_f32<BF16>(u[j] >> 16);
     }
 }
 
+// Four words from byte `at` (a multiple of 2, at most 16) of the eight in c.
+__device__ __forceinline__ void words_from(const uint32_t (&c)[8], uint32_t at, uint32_t (&d)[4]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = c[j];
+#pragma unroll
+    for (int step = 4; step; step >>= 1)
+        if (at & (4 * step)) {
+#pragma unroll
+            for (int j = 0; j + step < 8; ++j) w[j] = w[j + step];
+        }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = at & 2 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+}
+
+// Eight elements from column `col` (a multiple of 8) of a row of D, zeros past its end, in two steps, so that
+// a thread's loads are all under way before the first is used. VEC: the row starts and ends on
+// 16-byte boundaries, one load. Otherwise two aligned loads that the eight lie across, where both are
+// inside the row, and single elements at its ends (in the second step).
+template <bool VEC>
+struct Raw8 {
+    uint4 lo, hi;
+};
+template <bool VEC>
+__device__ __forceinline__ bool inside(uint32_t off, int col, int D) {
+    return VEC ? col < D : off ? col > 0 && col + 2 * kVec <= D : col + kVec <= D;
+}
+__device__ __forceinline__ uint32_t row_off(const uint16_t* row) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u);
+}
+template <bool VEC>
+__device__ __forceinline__ Raw8<VEC> begin8(const uint16_t* row, int col, int D) {
+    Raw8<VEC> r;
+    r.lo = r.hi = make_uint4(0, 0, 0, 0);
+    const uint32_t off = VEC ? 0 : row_off(row);
+    const bool in = inside<VEC>(off, col, D);
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row + col) - off);
+    if (in) r.lo = p[0];
+    if (!VEC && in && off) r.hi = p[1];
+    return r;
+}
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void end8(const Raw8<VEC>& r, const uint16_t* row, int col, int D, float (&v)[kVec]) {
+    if constexpr (VEC) {
+        const uint32_t u[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w};
+        unpack8<BF16>(u, v);
+    } else {
+        const uint32_t off = row_off(row), c[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+        uint32_t u[4];
+        words_from(c, off, u);
+        unpack8<BF16>(u, v);
+        if (!inside<VEC>(off, col, D) && col < D) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[j] = col + j < D ? to_f32<BF16>(row[col + j]) : 0.f;
+        }
+    }
+}
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8(const uint16_t* row, int col, int D, float (&v)[kVec]) {
+    end8<BF16, VEC>(begin8<VEC>(row, col, D), row, col, D, v);
+}
+
+// The reverse, for a warp whose lanes hold neighbouring eights: off a boundary, each lane stores the aligned
+// sixteen bytes that end inside its eight, of which the first come from the lane below, and what
+// has no lane below or above in the warp goes in single elements. Every lane of the warp calls it.
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void store8(uint16_t* row, int col, int D, const float (&v)[kVec]) {
-    if constexpr (VEC) {
-        uint32_t u[4];
+    uint32_t u[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = from_f32<BF16>(v[2 * j]) | (from_f32<BF16>(v[2 * j + 1]) << 16);
+    for (int j = 0; j < 4; ++j) u[j] = from_f32<BF16>(v[2 * j]) | (from_f32<BF16>(v[2 * j + 1]) << 16);
+    if constexpr (VEC) {
         if (col < D) *reinterpret_cast<uint4*>(row + col) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u);
+        const int lane = threadIdx.x & 31, back = off / 2;       // elements of the lane below
+        uint32_t c[8], w[4];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (col + j < D) row[col + j] = static_cast<uint16_t>(from_f32<BF16>(v[j]));
+        for (int j = 0; j < 4; ++j) {
+            c[j] = __shfl_up_sync(0xffffffffu, u[j], 1);
+            c[4 + j] = u[j];
+        }
+        words_from(c, 16 - off, w);
+        const int first = col - back;                            // the column w starts with
+        if ((lane || !off) && first + kVec <= D) {
+            *reinterpret_cast<uint4*>(row + first) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if ((lane || j >= back) && first + j < D)
+                    row[first + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+        }
+        if (lane == 31) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (j >= kVec - back && col + j < D) row[col + j] = static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1)));
+        }
     }
 }
 
@@ -95,8 +169,8 @@ __device__ __forceinline__ void quantise8(const float (&y)[kVec], int col, int D
     uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = e4m3x2(y[2 * j] * inv, y[2 * j + 1] * inv);
-    if (col < D) {
-        if constexpr (VEC) {
+    if (col < D) {                                   // (rows of codes start on 16-byte boundaries)
+        if (VEC || col + kVec <= D) {
             *reinterpret_cast<uint2*>(q_row + col) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
         } else {
 #pragma unroll
@@ -114,35 +188,59 @@ struct NormArgs {
     uint8_t* q;                         // null where not asked for
     float* scales;
     long long ldx, ldr, ldro, ldy, ldq, lds;
-    int D;
+    int T, D;
     float eps;
 };
 
-// One CTA per row; a thread holds VPT vectors of it in registers, so the row is read once although
-// its norm has to be known before the first value can be scaled. With one vector per thread (few rows: the
-// time is the latency of one row) the weight is loaded ahead of the sum; with two (many rows: 256 threads hold
-// a row of 4096) its registers are better spent on more rows per SM.
-template <bool BF16, bool VEC, int VPT>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
+// A thread holds VPT vectors of a row in registers, so the row is read once although its norm has to be known
+// before the first value can be scaled. WARP: one warp per row, kNormRows rows per CTA; else one CTA per
+// row. With one vector per thread (few rows: the time is the latency of one row) the weight is loaded ahead
+// of the sum; with more its registers are better spent on more rows per SM.
+constexpr int kNormRows = 4;
+
+template <bool BF16, bool VEC, int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kNormRows : VPT >= 4 ? 512 : 1024) norm_kernel(const NormArgs a) {
     __shared__ float part[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long t = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = WARP ? lane : threadIdx.x, n = WARP ? 32 : blockDim.x;
+    const long long t = WARP ? static_cast<long long>(blockIdx.x) * kNormRows + warp : blockIdx.x;
     const int D = a.D;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (WARP && t >= a.T) return;
 
     float h[VPT][kVec], w0[kVec];
     float ss = 0.f;
-    if constexpr (VPT == 1) load8<BF16, VEC>(a.w, tid * kVec, D, w0);
+    auto col_of = [&](int i) { return (i * n + tid) * kVec; };
+    if constexpr (VEC || VPT > 4) {
+        if constexpr (VPT == 1) load8<BF16, VEC>(a.w, col_of(0), D, w0);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int col = (i * blockDim.x + tid) * kVec;
-        load8<BF16, VEC>(a.x + t * a.ldx, col, D, h[i]);
-        if (a.r) {
-            float r[kVec];
-            load8<BF16, VEC>(a.r + t * a.ldr, col, D, r);
+        for (int i = 0; i < VPT; ++i) {
+            load8<BF16, VEC>(a.x + t * a.ldx, col_of(i), D, h[i]);
+            if (a.r) {
+                float r[kVec];
+                load8<BF16, VEC>(a.r + t * a.ldr, col_of(i), D, r);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) h[i][j] += r[j];
+                for (int j = 0; j < kVec; ++j) h[i][j] += r[j];
+            }
+        }
+    } else {                                         // (single elements only after every vector is under way)
+        Raw8<VEC> x[VPT], r[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            x[i] = begin8<VEC>(a.x + t * a.ldx, col_of(i), D);
+            if (a.r) r[i] = begin8<VEC>(a.r + t * a.ldr, col_of(i), D);
+        }
+        if constexpr (VPT == 1) load8<BF16, VEC>(a.w, col_of(0), D, w0);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            end8<BF16, VEC>(x[i], a.x + t * a.ldx, col_of(i), D, h[i]);
+            if (a.r) {
+                float v[kVec];
+                end8<BF16, VEC>(r[i], a.r + t * a.ldr, col_of(i), D, v);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) h[i][j] += v[j];
+            }
         }
     }
 #pragma unroll
@@ -150,19 +248,21 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) ss = fmaf(h[i][j], h[i][j], ss);
         // the sum in the 16-bit type is for the next layer; the norm goes by the unrounded one
-        if (a.r_out) store8<BF16, VEC>(a.r_out + t * a.ldro, (i * blockDim.x + tid) * kVec, D, h[i]);
+        if (a.r_out) store8<BF16, VEC>(a.r_out + t * a.ldro, col_of(i), D, h[i]);
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    if (lane == 0) part[warp] = ss;
-    __syncthreads();
-    ss = lane < (blockDim.x >> 5) ? part[lane] : 0.f;
+    if constexpr (!WARP) {
+        if (lane == 0) part[warp] = ss;
+        __syncthreads();
+        ss = lane < (n >> 5) ? part[lane] : 0.f;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    }
     const float rstd = 1.f / sqrtf(ss / static_cast<float>(D) + a.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int col = (i * blockDim.x + tid) * kVec;
+        const int col = col_of(i);
         float w[kVec];
         if constexpr (VPT > 1) load8<BF16, VEC>(a.w, col, D, w);
 #pragma unroll
@@ -173,21 +273,29 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
 }
 
 template <bool BF16, bool VEC>
-int go_norm(const Runtime& rt, const NormArgs& a, int T, wq4_stream_t st) {
+int go_norm(const Runtime& rt, const NormArgs& a, wq4_stream_t st) {
     const int nv = (a.D + kVec - 1) / kVec;
-    // Measured: 4096 x 4096 bf16 with the residual, one vector per thread 26.0 us, two 21.6, four 22.6; 1 x 4096
-    // 1.9 / 2.3 / 3.0 us; 517 x 2064 fp16 2.6 / 3.3 / 4.0 us.
-    const int fewest = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4;
-    const int vpt = fewest == 1 && nv > 256 && T > 4 * rt.sm_count ? 2 : fewest;
+    const bool many = a.T > 4 * rt.sm_count;
+    // Many short rows: a warp each (8192 x 256: 4.5 us against 8.6 with a CTA each; 1 x 1024 2.7 against 1.6).
+    if (many && nv <= 64) {
+        const dim3 grid((static_cast<unsigned>(a.T) + kNormRows - 1) / kNormRows);
+        if (nv <= 32) return launch(rt, norm_kernel<BF16, VEC, 1, true>, grid, 32 * kNormRows, 0, 1, st, a);
+        return launch(rt, norm_kernel<BF16, VEC, 2, true>, grid, 32 * kNormRows, 0, 1, st, a);
+    }
+    // Vectors per thread. Measured with the residual, bf16: 4096 x 4096, one 26.0 us, two 21.6, four 22.6;
+    // 1 x 4096, 1.9 / 2.3 / 3.0 us; 517 x 2064 fp16 without it 2.6 / 3.3 / 4.0; 1000 x 16384, two 28.4,
+    // four 24.1; 2000 x 8192, one 22.0, two 24.6, four 22.8.
+    const int vpt = nv > 2048 ? 8 : nv > 1024 ? (many ? 4 : 2) : many && nv > 256 && nv <= 768 ? 2 : 1;
     const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
     switch (vpt) {
-        case 1: return launch(rt, norm_kernel<BF16, VEC, 1>, dim3(T), threads, 0, 1, st, a);
-        case 2: return launch(rt, norm_kernel<BF16, VEC, 2>, dim3(T), threads, 0, 1, st, a);
-        default: return launch(rt, norm_kernel<BF16, VEC, 4>, dim3(T), threads, 0, 1, st, a);
+        case 1: return launch(rt, norm_kernel<BF16, VEC, 1, false>, dim3(a.T), threads, 0, 1, st, a);
+        case 2: return launch(rt, norm_kernel<BF16, VEC, 2, false>, dim3(a.T), threads, 0, 1, st, a);
+        case 4: return launch(rt, norm_kernel<BF16, VEC, 4, false>, dim3(a.T), threads, 0, 1, st, a);
+        default: return launch(rt, norm_kernel<BF16, VEC, 8, false>, dim3(a.T), threads, 0, 1, st, a);
     }
 }
 
-constexpr int kNormMaxD = 1024 * 4 * kVec;
+constexpr int kNormMaxD = 512 * 8 * kVec;
 
 // ------------------------------------------------------------------------------ gated activation
 struct GatedArgs {
@@ -209,19 +317,22 @@ __global__ void __launch_bounds__(kGatedVecs / VPT) gated_kernel(const GatedArgs
     const long long t = blockIdx.x / a.chunks;
     const int D = a.D, col0 = ((blockIdx.x % a.chunks) * kGatedVecs + threadIdx.x) * kVec;
     const uint16_t* row = a.x + t * a.ldx;
-    float g[VPT][kVec], u[VPT][kVec];
+    Raw8<VEC> rg[VPT], ru[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        load8<BF16, VEC>(row, col0 + i * kThreads * kVec, D, g[i]);
-        load8<BF16, VEC>(row + D, col0 + i * kThreads * kVec, D, u[i]);
+        rg[i] = begin8<VEC>(row, col0 + i * kThreads * kVec, D);
+        ru[i] = begin8<VEC>(row + D, col0 + i * kThreads * kVec, D);
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int col = col0 + i * kThreads * kVec;
+        float g[kVec], u[kVec];
+        end8<BF16, VEC>(rg[i], row, col, D, g);
+        end8<BF16, VEC>(ru[i], row + D, col, D, u);
         // silu(g) = g / (1 + exp(-g)); where exp(-g) is infinite the quotient is the limit, 0
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) g[i][j] = __fdividef(g[i][j], 1.f + __expf(-g[i][j])) * u[i][j];
-        quantise8<VEC>(g[i], col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
+        for (int j = 0; j < kVec; ++j) g[j] = __fdividef(g[j], 1.f + __expf(-g[j])) * u[j];
+        quantise8<VEC>(g, col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
     }
 }
 
@@ -270,11 +381,11 @@ int wq4_add_rmsnorm_quant(const void* X, long long ldx, const void* R, long long
     if (const int rc = runtime(&rt)) return rc;
     const NormArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(R),
                      static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(R_out), static_cast<uint16_t*>(Y),
-                     static_cast<uint8_t*>(Q), scales, ldx, ldr, ldro, ldy, ldq, lds, D, eps};
+                     static_cast<uint8_t*>(Q), scales, ldx, ldr, ldro, ldy, ldq, lds, T, D, eps};
     const bool vec = D % kVec == 0 && vec_ok(X, ldx) && vec_ok(R, ldr) && vec_ok(weight, 0) && vec_ok(R_out, ldro) &&
                      vec_ok(Y, ldy);
-    if (dtype == WQ4_BF16) return vec ? go_norm<true, true>(rt, a, T, stream) : go_norm<true, false>(rt, a, T, stream);
-    return vec ? go_norm<false, true>(rt, a, T, stream) : go_norm<false, false>(rt, a, T, stream);
+    if (dtype == WQ4_BF16) return vec ? go_norm<true, true>(rt, a, stream) : go_norm<true, false>(rt, a, stream);
+    return vec ? go_norm<false, true>(rt, a, stream) : go_norm<false, false>(rt, a, stream);
 }
 
 int wq4_silu_mul_quant(const void* X, long long ldx, int T, int D, int dtype, void* Q, long long ldq, float* scales,
