@@ -198,8 +198,12 @@ struct NormArgs {
 // of the sum; with more its registers are better spent on more rows per SM.
 constexpr int kNormRows = 4;
 
+// CTAs of the largest size that an SM holds, by their registers.
+constexpr int norm_ctas(bool vec, int vpt) { return vpt == 1 ? (vec ? 2 : 1) : vpt == 2 ? (vec ? 3 : 2) : vec && vpt == 4 ? 2 : 1; }
+
 template <bool BF16, bool VEC, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kNormRows : VPT >= 4 ? 512 : 1024) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(WARP ? 32 * kNormRows : VPT > 1 ? 512 : 1024, WARP ? (VEC ? 16 : 8) : norm_ctas(VEC, VPT))
+    norm_kernel(const NormArgs a) {
     __shared__ float part[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tid = WARP ? lane : threadIdx.x, n = WARP ? 32 : blockDim.x;
@@ -284,8 +288,8 @@ int go_norm(const Runtime& rt, const NormArgs& a, wq4_stream_t st) {
     }
     // Vectors per thread. Measured with the residual, bf16: 4096 x 4096, one 26.0 us, two 21.6, four 22.6;
     // 1 x 4096, 1.9 / 2.3 / 3.0 us; 517 x 2064 fp16 without it 2.6 / 3.3 / 4.0; 1000 x 16384, two 28.4,
-    // four 24.1; 2000 x 8192, one 22.0, two 24.6, four 22.8.
-    const int vpt = nv > 2048 ? 8 : nv > 1024 ? (many ? 4 : 2) : many && nv > 256 && nv <= 768 ? 2 : 1;
+    // four 24.1; 2000 x 8192, one 28.3, two 22.0, four 22.8. (Two: at most 40 registers, three CTAs of 512.)
+    const int vpt = nv > 2048 ? 8 : nv > 1024 ? 4 : many && nv > 256 ? 2 : 1;
     const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
     switch (vpt) {
         case 1: return launch(rt, norm_kernel<BF16, VEC, 1, false>, dim3(a.T), threads, 0, 1, st, a);
