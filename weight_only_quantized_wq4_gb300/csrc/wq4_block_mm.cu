@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdio>
+#include <type_traits>
 
 #include "wq4_device.cuh"
 #include "wq4_runtime.h"
@@ -51,7 +52,8 @@ struct BmArgs {
     int lane_tiles, tiles;                     // tile t: lane tile t % lane_tiles, column tile t / lane_tiles
     int split;                                 // CTAs per cluster, each with a part of K (1: none)
     int stages;                                // of the ring: an even number
-    int red_cols, red_shift;                   // split: columns of a tile that are joined, and by how many (2^shift) per CTA
+    int red_cols, red_shift;                   // split: weights on the lanes: columns of a tile that are joined, and
+                                               // how many (2^shift) per CTA; tokens on the lanes: split = 2^shift
     int dtype;
     int unit;                                  // bytes that a row of Y is stored by: 16, or what its start allows
     unsigned int* status;
@@ -150,6 +152,12 @@ __device__ __forceinline__ void bm_commit(uint32_t bar) {
 __device__ __forceinline__ void st_async(uint32_t addr, float v, uint32_t bar) {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
                  "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async4(uint32_t addr, const float* v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                 "r"(__float_as_uint(v[3])), "r"(bar)
                  : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_leader(uint32_t bar) {
@@ -265,17 +273,17 @@ __device__ __forceinline__ void copy_rows(const BmArgs& a, uint32_t buf, int lan
 template <int CNT>
 __device__ __forceinline__ void store_rows(const BmArgs& a, uint32_t buf, int lane, int m0, int n, const float* v) {
     const uint32_t mine = buf + lane * 80;
-    constexpr int kChunk = CNT < 32 ? CNT : 32;       // 16-bit columns that go through `buf` together
+    constexpr int kChunk = CNT < 32 ? CNT : 32, kWide = CNT < 16 ? CNT : 16;   // columns of 16, 32 bits at a time
     if (a.dtype == WQ4_FP32) {
 #pragma unroll
-        for (int c = 0; c < CNT; c += 16) {
+        for (int c = 0; c < CNT; c += kWide) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4)
+            for (int j = 0; j < kWide; j += 4)
                 sts128(mine + 4 * j, __float_as_uint(v[c + j]), __float_as_uint(v[c + j + 1]),
                        __float_as_uint(v[c + j + 2]), __float_as_uint(v[c + j + 3]));
             __syncwarp();
-            if (a.unit == 16) copy_rows<4, 16, 16>(a, buf, lane, m0, n + c);
-            else copy_rows<4, 4, 16>(a, buf, lane, m0, n + c);
+            if (a.unit == 16) copy_rows<4, 16, kWide>(a, buf, lane, m0, n + c);
+            else copy_rows<4, 4, kWide>(a, buf, lane, m0, n + c);
             __syncwarp();
         }
     } else {
@@ -377,7 +385,8 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
         if (!PAIR && a.split > 1) {                  // the bytes of the parts of this CTA's columns
             mbar_init(red_bar, 1);
             const int own = min(max(a.red_cols - (rank << a.red_shift), 0), 1 << a.red_shift);
-            mbar_arrive_expect_tx(red_bar, own * a.split * kBmLanes * 4);
+            mbar_arrive_expect_tx(red_bar, TOK_LANES ? (a.split - 1) * (NT / a.split) * kBmLanes * 4
+                                                     : own * a.split * kBmLanes * 4);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -621,33 +630,67 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
             }
         }
         if (!PAIR && a.split > 1) {
-            // Every CTA sends its part of each column to the CTA that joins it (to itself too), which adds the
-            // ranks' parts in order once all their bytes have come. (A CTA that gave up sends what it has.)
+            // Every CTA sends its part of each column to the CTA that joins it, which adds the ranks' parts in order
+            // once all their bytes have come. (A CTA that gave up sends what it has.)
+            const BmSched s(a, rank, PAIR);          // (one tile per cluster)
+            const int l0 = s.t % a.lane_tiles * kBmLanes, c0 = s.t / a.lane_tiles * NT;
+            if constexpr (TOK_LANES) {
+                // Each rank joins a 1 / split of every fold thread's columns, so that the thread that holds a column's
+                // part here joins it there: [rank][fold part][four columns][lane], its own part by a plain store.
+                constexpr int kQuads = C::kNC / 4, kLog = kQuads == 16 ? 4 : 5;
+                static_assert(kQuads == 1 << kLog, "columns of a fold thread");
+                const int lg = kLog - a.red_shift;                           // 2^lg: a rank's share, in fours
+                const int me = s_red + ((part << lg) * kBmLanes + r) * 16, step = (C::kParts << lg) * kBmLanes * 16;
+                auto slot = [&](int src, int q) { return static_cast<uint32_t>(me + src * step + q * (kBmLanes * 16)); };
 #pragma unroll
-            for (int j = 0; j < C::kNC; ++j) {
-                const int col = col0 + j, owner = col >> a.red_shift, at = col & ((1 << a.red_shift) - 1);
-                if (col >= a.red_cols) break;
-                st_async(map_to_rank(s_red + ((((rank << a.red_shift) + at) * kBmLanes) + r) * 4, owner), acc[j],
-                         map_to_rank(red_bar, owner));
-            }
-            const int first = rank << a.red_shift, own = min(a.red_cols - first, 1 << a.red_shift);
-            if (own > 0 && mbar_wait(red_bar, 0, ctl)) {
-                const int t = blockIdx.x / a.split;  // (one tile per cluster)
-                const int l0 = t % a.lane_tiles * kBmLanes, c0 = t / a.lane_tiles * NT;
-                constexpr int kCnt = TOK_LANES ? 16 : 4;
-                for (int c = part * kCnt; c < own; c += C::kParts * kCnt) {
-                    float v[kCnt];
+                for (int j = 0; j < C::kNC; j += 4) {
+                    const int owner = (j / 4) >> lg, q = (j / 4) & ((1 << lg) - 1);
+                    if (owner == rank)
+                        sts128(slot(rank, q), __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
+                               __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3]));
+                    else
+                        st_async4(map_to_rank(slot(rank, q), owner), acc + j, map_to_rank(red_bar, owner));
+                }
+                if (mbar_wait(red_bar, 0, ctl)) {
+                    auto join = [&](auto columns) {
+                        constexpr int kCnt = decltype(columns)::value;
+                        float v[kCnt];
 #pragma unroll
-                    for (int q = 0; q < kCnt; ++q) v[q] = 0.f;
-                    for (int o = 0; o < a.split; ++o) {
-                        const uint32_t from = s_red + ((((o << a.red_shift) + c) * kBmLanes) + r) * 4;
+                        for (int q = 0; q < kCnt; ++q) v[q] = 0.f;
+                        for (int o = 0; o < a.split; ++o)
 #pragma unroll
-                        for (int q = 0; q < kCnt; ++q)
-                            if (c + q < own) v[q] += lds_f32(from + q * (kBmLanes * 4));
-                    }
-                    if constexpr (TOK_LANES) {
-                        store_rows<kCnt>(a, buf, lane, l0 + r - lane, c0 + first + c, v);
-                    } else {
+                            for (int q = 0; q < kCnt / 4; ++q) {
+                                const uint4 x = lds128(slot(o, q));
+                                v[4 * q] += __uint_as_float(x.x), v[4 * q + 1] += __uint_as_float(x.y);
+                                v[4 * q + 2] += __uint_as_float(x.z), v[4 * q + 3] += __uint_as_float(x.w);
+                            }
+                        store_rows<kCnt>(a, buf, lane, l0 + r - lane, c0 + part * C::kNC + rank * kCnt, v);
+                    };
+                    if (a.split == 2) join(std::integral_constant<int, C::kNC / 2>());
+                    else if (a.split == 4) join(std::integral_constant<int, C::kNC / 4>());
+                    else join(std::integral_constant<int, C::kNC / 8>());
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int owner = j >> a.red_shift, at = j & ((1 << a.red_shift) - 1);
+                    if (j >= a.red_cols) break;
+                    st_async(map_to_rank(s_red + ((((rank << a.red_shift) + at) * kBmLanes) + r) * 4, owner), acc[j],
+                             map_to_rank(red_bar, owner));
+                }
+                const int first = rank << a.red_shift, own = min(a.red_cols - first, 1 << a.red_shift);
+                if (own > 0 && mbar_wait(red_bar, 0, ctl)) {
+                    constexpr int kCnt = 4;
+                    for (int c = 0; c < own; c += kCnt) {
+                        float v[kCnt];
+#pragma unroll
+                        for (int q = 0; q < kCnt; ++q) v[q] = 0.f;
+                        for (int o = 0; o < a.split; ++o) {
+                            const uint32_t from = s_red + ((((o << a.red_shift) + c) * kBmLanes) + r) * 4;
+#pragma unroll
+                            for (int q = 0; q < kCnt; ++q)
+                                if (c + q < own) v[q] += lds_f32(from + q * (kBmLanes * 4));
+                        }
                         store_cols<kCnt>(a, c0 + first + c, own - c, l0 + r, v);
                     }
                 }
@@ -747,8 +790,8 @@ int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) 
     a.stages = half ? C::kHalfStages : C::fit(red);
     if (a.split > 1 && blocks < a.stages) a.stages = blocks < 4 ? 4 : (blocks + 1) & ~1;
     const int smem = C::kHeadBytes + a.stages * C::kStageBytes + red;
-    a.red_cols = TOK_LANES || a.M > NT ? NT : a.M;
-    while ((a.split << a.red_shift) < a.red_cols) ++a.red_shift;
+    a.red_cols = a.M;
+    while (TOK_LANES ? (1 << a.red_shift) < a.split : (a.split << a.red_shift) < a.red_cols) ++a.red_shift;
     if (rt.trace)
         std::fprintf(stderr, "wq4: block_mm M=%d N=%d K=%d lanes=%s columns=%d pair=%d grid=%d split=%d\n", a.M, a.N, c.K,
                      TOK_LANES ? "tokens" : "weights", NT, PAIR ? 1 : 0, grid, a.split);
