@@ -23,8 +23,8 @@
 // as an unsigned integer of the same order, then the complement of its index, so that equal logits
 // rank by the lower index and no two keys are equal.
 //
-// Bound by memory for many rows (each logit read once). For few rows a cluster of CTAs shares a row
-// and joins its parts through distributed shared memory.
+// Bound by memory and by instructions for many rows (each logit is read once). For few rows a cluster of
+// CTAs shares a row; each sends its statistics and list to the first through distributed shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,6 +47,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFar = 150.f;                 // exp(-150) is below the smallest fp32
 constexpr float kNegInf = -INFINITY;
 
+static_assert(kLpMaxCluster * kLpMaxTop <= kLpThreads / 2, "two threads to a key");
+
 enum : int { kLpBf16 = 0, kLpFp16 = 1, kLpFp32 = 2 };   // the header's dtype codes
 
 struct LpArgs {
@@ -56,6 +58,8 @@ struct LpArgs {
     int* top_ids;
     long long ld;
     int V, k, cluster;
+    unsigned int* status;
+    long long timeout_cycles;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -263,6 +267,17 @@ struct LpAcc {
     }
 };
 
+// To shared memory of a CTA of the cluster; the bytes count on that CTA's barrier.
+__device__ __forceinline__ void st_async(uint32_t addr, unsigned long long v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(addr), "l"(v), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t addr, const LpStat& v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.s)), "r"(0), "r"(bar)
+                 : "memory");
+}
+
 struct LpShared {
     float2 stat[kLpWarps];                           // warps' z and s, with the CTA's m
     LpStat total;
@@ -272,6 +287,11 @@ struct LpShared {
     uint16_t flag[kLpThreads];                       // threads whose best reaches tau
     unsigned long long cand[kLpWarps * kLpMaxTop];
     int rank[kLpMaxCluster * kLpMaxTop];             // of the clusters' lists
+    // what rank 0 is sent by the cluster's CTAs: their statistics and their lists
+    float4 part_stat[kLpMaxCluster];
+    unsigned long long part_top[kLpMaxCluster * kLpMaxTop];
+    unsigned long long part_bar;
+    int abort;
     unsigned long long top[kLpMaxTop];               // this CTA's best, in order, 0 where there are fewer
 };
 
@@ -287,6 +307,16 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     const long long t = C > 1 ? blockIdx.x / C : blockIdx.x;
+    if (C > 1) {
+        if (tid == 0) {
+            mbar_init(smem_u32(&sh.part_bar), 1);
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.part_bar), C * (16 + 8 * a.k));
+            sh.abort = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        cluster_sync();                              // rank 0's barrier is set up before anything is sent to it
+    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const LpRow<DT> row(a.logits, a.ld, t, a.V);
@@ -507,6 +537,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
         if (tid < n) {
             const unsigned long long mine = sh.cand[tid];
             int above = 0;
+#pragma unroll 8
             for (int i = 0; i < n; ++i) above += sh.cand[i] > mine ? 1 : 0;
             if (above < a.k) sh.top[above] = mine;
         }
@@ -515,52 +546,50 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
 
     // ---- the row's, from its CTAs'
     if (C > 1) {
-        cluster_sync();
-        if (rank == 0) {
-            if (warp == 0) {
-                LpStat w{kNegInf, 0.f, 0.f};
-                if (lane < C) {
-                    const uint32_t p = map_to_rank(smem_u32(&sh.total), lane);
-                    w = LpStat{ld_cluster_f32(p), ld_cluster_f32(p + 4), ld_cluster_f32(p + 8)};
-                }
-                float n = w.m;
-#pragma unroll
-                for (int d = kLpMaxCluster / 2; d; d >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
-                w.move(n);
-#pragma unroll
-                for (int d = kLpMaxCluster / 2; d; d >>= 1) {
-                    w.z += __shfl_xor_sync(0xffffffffu, w.z, d);
-                    w.s += __shfl_xor_sync(0xffffffffu, w.s, d);
-                }
-                if (lane == 0) sh.total = LpStat{n, w.z, w.s};
-            }
-            for (int i = tid; i < C * kLpMaxTop; i += kLpThreads) {
-                const uint32_t p = map_to_rank(smem_u32(&sh.top[i % kLpMaxTop]), i / kLpMaxTop);
-                unsigned long long key;
-                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(p) : "memory");
-                sh.cand[i] = key;
-                sh.rank[i] = 0;
-            }
+        // Every CTA sends rank 0 its statistics and its list (its own too) and is done; their bytes count on rank
+        // 0's barrier.
+        if (tid < 32) {
+            const uint32_t bar = map_to_rank(smem_u32(&sh.part_bar), 0);
+            if (tid < a.k) st_async(map_to_rank(smem_u32(&sh.part_top[rank * a.k + tid]), 0), sh.top[tid], bar);
+            if (tid == 0) st_async(map_to_rank(smem_u32(&sh.part_stat[rank]), 0), sh.total, bar);
         }
-        cluster_sync();                              // every part is read: the other CTAs may leave
         if (rank != 0) return;
+        const WaitCtl ctl{&sh.abort, a.status, a.timeout_cycles};
+        if (tid == 0) mbar_wait(smem_u32(&sh.part_bar), 0, ctl);     // (one thread's answer holds for all)
+        __syncthreads();
+        if (sh.abort) {
+            cluster_sync();                          // (not before the others, which may still send, are gone)
+            return;
+        }
+        if (warp == 0) {
+            const float4 x = lane < C ? sh.part_stat[lane] : make_float4(kNegInf, 0.f, 0.f, 0.f);
+            LpStat w{x.x, x.y, x.z};
+            float n = w.m;
+#pragma unroll
+            for (int d = kLpMaxCluster / 2; d; d >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
+            w.move(n);
+#pragma unroll
+            for (int d = kLpMaxCluster / 2; d; d >>= 1) {
+                w.z += __shfl_xor_sync(0xffffffffu, w.z, d);
+                w.s += __shfl_xor_sync(0xffffffffu, w.s, d);
+            }
+            if (lane == 0) sh.total = LpStat{n, w.z, w.s};
+        }
+        for (int i = tid; i < C * kLpMaxTop; i += kLpThreads) sh.rank[i] = 0;
         if (tid < kLpMaxTop) sh.top[tid] = 0;
         __syncthreads();
-        // Each list is in order, so a key's rank is the sum over the lists of how many of each are above it,
-        // found by halving: a thread per key and list.
-        if (a.k > 0) {
-            for (int i = tid; i < C * kLpMaxTop * C; i += kLpThreads) {
-                const unsigned long long mine = sh.cand[i % (C * kLpMaxTop)];
-                const unsigned long long* list = sh.cand + i / (C * kLpMaxTop) * kLpMaxTop;
-                int n = 0;                           // list[0 .. n) are above mine
-#pragma unroll
-                for (int half = kLpMaxTop / 2; half; half >>= 1) n += list[n + half - 1] > mine ? half : 0;
-                n += list[n] > mine ? 1 : 0;
-                if (n) atomicAdd(&sh.rank[i % (C * kLpMaxTop)], n);
+        if (a.k > 0) {                               // ranked by counting, two threads to a key
+            const int keys = C * a.k, i = tid & (kLpThreads / 2 - 1), from = tid < kLpThreads / 2 ? 0 : keys / 2;
+            const int to = tid < kLpThreads / 2 ? keys / 2 : keys;
+            const unsigned long long mine = i < keys ? sh.part_top[i] : 0;
+            if (mine) {
+                int above = 0;
+#pragma unroll 8
+                for (int q = from; q < to; ++q) above += sh.part_top[q] > mine ? 1 : 0;
+                if (above) atomicAdd(&sh.rank[i], above);
             }
             __syncthreads();
-            for (int i = tid; i < C * kLpMaxTop; i += kLpThreads)
-                if (sh.cand[i] && sh.rank[i] < a.k) sh.top[sh.rank[i]] = sh.cand[i];
+            if (tid < keys && mine && sh.rank[tid] < a.k) sh.top[sh.rank[tid]] = mine;
         }
         __syncthreads();
     }
@@ -604,7 +633,7 @@ extern "C" int wq4_token_logprobs(const void* logits, long long ld, const long l
     const int vec = dtype == WQ4_FP32 ? 4 : 8;
     while (C < kLpMaxCluster && 2LL * C * T <= 2LL * rt.sm_count && V / (2 * C) >= kLpThreads * vec) C *= 2;
     if (static_cast<long long>(T) * C > 0x7fffffffLL) return WQ4_ERR_UNSUPPORTED;
-    const LpArgs a{logits, tokens, logprobs, entropy, top_logprobs, top_ids, ld, V, top_k, C};
+    const LpArgs a{logits, tokens, logprobs, entropy, top_logprobs, top_ids, ld, V, top_k, C, rt.status, rt.timeout_cycles};
     const dim3 grid(static_cast<unsigned>(T) * C);
     switch (dtype) {
         case WQ4_BF16: return launch(rt, logprobs_kernel<kLpBf16>, grid, kLpThreads, 0, C, stream, a);
