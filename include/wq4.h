@@ -325,7 +325,8 @@ int wq4_debug_checks(void);
 /* The first violation that the last WQ4_ERR_BOUNDS report read back: record[0] = the check site
  * (1 tile, 2 activation tile copy, 3 activation sums, 4 weight record, 5 epilogue C copy,
  * 6 K-split partial slot, 7 K-split counter, 8 output column, 9 decode weight stage, 10 decode
- * activation piece, 11 problem index), record[1..3] = the offending coordinate or index, then two
+ * activation piece, 11 problem index, 12 block-scaled product operand copy, 13 block-scaled product
+ * output), record[1..3] = the offending coordinate or index, then two
  * values whose meaning depends on the site (listed with the sites in csrc/wq4_check.h). record
  * must hold 4 ints. Returns 1 and clears the saved violation if there was one, 0 (record zeroed)
  * otherwise, WQ4_ERR_INVALID for a null record. */

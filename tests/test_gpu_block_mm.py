@@ -149,3 +149,15 @@ def test_a_layer_in_stream_order(lib, pdl):
     assert np.all(np.abs(gu.double().cpu().numpy() - y1) <= 2.0 ** -16 * m1 + 2.0 ** -8 * np.abs(y1))
     y2, m2 = R.block_mm(codes(q2), sc2.cpu().numpy(), w2q, s2)
     assert np.all(np.abs(out.double().cpu().numpy() - y2) <= 2.0 ** -16 * m2 + 2.0 ** -23 * np.abs(y2))
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 300, 400), (20, 520, 1040), (60, 14336, 128), (200, 300, 2064), (1300, 2100, 272)])
+def test_under_the_bounds_checks(lib, M, N, K):
+    """Every form of the kernel in the bounds-checking build: right, and no check fires."""
+    lib.build(debug=True)
+    old = lib.use_library(lib.DEBUG_LIB_PATH)
+    try:
+        check(lib, M, N, K, torch.bfloat16, seed=9)
+        assert lib.last_violation() is None
+    finally:
+        lib.restore_library(old)

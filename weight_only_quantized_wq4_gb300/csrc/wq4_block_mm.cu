@@ -249,6 +249,7 @@ __device__ __forceinline__ void copy_rows(const BmArgs& a, uint32_t buf, int lan
     constexpr int kPerRow = CNT * SIZE / UNIT, kRows = 32 / kPerRow, kIn = UNIT / SIZE;
     const int c = lane % kPerRow * kIn, r0 = lane / kPerRow;
     const int cols = a.N - n - c, rows = a.M - m0;   // what exists from here on
+    if (!WQ4_CHECK(n >= 0 && m0 >= 0 && m0 < (a.M + 255) / 256 * 256, a.status, nullptr, check::kSiteBlockOut, n, m0, a.N)) return;
     uint8_t* to = static_cast<uint8_t*>(a.y) + ((m0 + r0) * a.ldy + n + c) * SIZE;
     const long long step = a.ldy * (kRows * SIZE);
     const uint32_t from = buf + r0 * 80 + c * SIZE;
@@ -308,6 +309,7 @@ __device__ __forceinline__ void store_rows(const BmArgs& a, uint32_t buf, int la
 template <int CNT>
 __device__ __forceinline__ void store_cols(const BmArgs& a, int m, int rows, int n, const float* v) {
     if (n >= a.N) return;
+    if (!WQ4_CHECK(n >= 0 && m >= 0 && m < a.M + CNT, a.status, nullptr, check::kSiteBlockOut, n, m, a.N)) return;
     const long long at = m * a.ldy + n;
     if (a.dtype == WQ4_FP32) {
         float* y = static_cast<float*>(a.y) + at;
@@ -419,6 +421,8 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
                 const bool lanes = warp == 0, once = lanes ? a.tiles == a.lane_tiles : a.lane_tiles == 1;
                 const uint64_t policy = once ? policy_evict_first() : policy_evict_last();
                 const CUtensorMap* map = lanes ? &a.lane_map : &a.col_map;
+                // rows of this operand's tiles (the last may be partly past its end)
+                [[maybe_unused]] const int row_end = lanes ? a.lane_tiles * kTileLanes : a.tiles / a.lane_tiles * NT;
                 const uint32_t dst = s_ring + (lanes ? 0 : C::kLaneBytes), bytes = lanes ? C::kLaneBytes : C::kColBytes;
                 bool ok = true;
                 int st = 0, i = 0, sc = 0;
@@ -437,7 +441,10 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
                         }
                         if (!mbar_wait(empty_bar(st), phase, ctl)) { ok = false; break; }
                         mbar_arrive_expect_tx(full_bar(st), bytes);
-                        tma_load_2d(dst + st * C::kStageBytes, map, full_bar(st), b * kBmBlock, row, policy);
+                        int x = b * kBmBlock, y = row;       // (a failed check reads the tensor's origin instead)
+                        if (!WQ4_CHECK(check::block_copy_ok(b, a.kb, row, row_end) && check::tma_x_ok(x, 1, 0, x), a.status,
+                                       abort_flag, check::kSiteBlockCopy, b, row, a.kb)) x = y = 0;
+                        tma_load_2d(dst + st * C::kStageBytes, map, full_bar(st), x, y, policy);
                         if (++st == a.stages) { st = 0; phase ^= 1; }
                     }
                 }

@@ -42,6 +42,8 @@ enum Site : int {
     kSiteDecW = 9,        // decode weight stage copy: 16-row block, first group, blocks
     kSiteDecX = 10,       // decode activation piece copy: first 64-wide K panel, piece, K
     kSiteProblem = 11,    // problem index of a scheduled tile: index, problems, 0
+    kSiteBlockCopy = 12,  // block-scaled product, operand or scale copy: block of K, first row, blocks
+    kSiteBlockOut = 13,   // block-scaled product, output: column, token, N
 };
 
 // The words after the status word that hold the first violation: site, then three values.
@@ -66,6 +68,12 @@ WQ4_HD inline bool aligned16(unsigned long long addr) { return (addr & 15ull) ==
 WQ4_HD inline bool tile_ok(int mt, int token_tile, int rows, int nt, int N, int g0, int g1, int k_groups) {
     return mt >= 0 && static_cast<long long>(mt) * token_tile < rows && nt >= 0 &&
            (static_cast<long long>(nt) + 1) * 128 <= N && g0 >= 0 && g0 < g1 && g1 <= k_groups;
+}
+
+// Block b of [0, blocks) and first row `row` of [0, rows) of an operand of the block-scaled product (a copy may
+// run past the last row, where it reads zeros).
+WQ4_HD inline bool block_copy_ok(long long b, long long blocks, long long row, long long rows) {
+    return b >= 0 && b < blocks && row >= 0 && row < rows;
 }
 
 }  // namespace check
