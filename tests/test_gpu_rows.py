@@ -138,6 +138,7 @@ def test_gated_special_values(lib):
     D = 256
     x = make(4, 2 * D, "bf16", 12)
     x[0, :D] = -1000.0                       # silu -> 0
+    x[0, D:] = 3e38                          # (and times the largest u still 0)
     x[1, 3], x[1, D + 3] = 1000.0, 1000.0
     x[2, 130] = float("nan")
     x[3, 7], x[3, D + 7] = inf, 1.0

@@ -32,10 +32,58 @@ __device__ __forceinline__ float to_f32(uint32_t b16) {
     else return __half2float(__ushort_as_half(static_cast<uint16_t>(b16)));
 }
 
+// Two values rounded to the 16-bit type, `lo` in the low half.
 template <bool BF16>
-__device__ __forceinline__ uint32_t from_f32(float v) {
-    if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    else return __half_as_ushort(__float2half_rn(v));
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t u;
+    if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+    return u;
+}
+
+// Two fp32 operations in one instruction each: at the rate of HBM an SM has some 20 instructions for
+// 32 elements, and these kernels' arithmetic is most of what they issue.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ void add8(float (&a)[kVec], const float (&b)[kVec]) {
+#pragma unroll
+    for (int j = 0; j < kVec; j += 2) {
+        uint64_t d;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a[j], a[j + 1])), "l"(pair(b[j], b[j + 1])));
+        unpair(d, a[j], a[j + 1]);
+    }
+}
+__device__ __forceinline__ void mul8(float (&a)[kVec], const float (&b)[kVec]) {
+#pragma unroll
+    for (int j = 0; j < kVec; j += 2) {
+        uint64_t d;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a[j], a[j + 1])), "l"(pair(b[j], b[j + 1])));
+        unpair(d, a[j], a[j + 1]);
+    }
+}
+__device__ __forceinline__ void mul8(float (&a)[kVec], float b) {
+    const float v[kVec] = {b, b, b, b, b, b, b, b};
+    mul8(a, v);
+}
+// sum of the squares, added to the two halves of s
+__device__ __forceinline__ void squares8(const float (&a)[kVec], uint64_t& s) {
+#pragma unroll
+    for (int j = 0; j < kVec; j += 2) {
+        const uint64_t x = pair(a[j], a[j + 1]);
+        asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(s) : "l"(x));
+    }
+}
+// 1 / x to an ulp or so (0 for infinity)
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 template <bool BF16>
@@ -116,7 +164,7 @@ template <bool BF16, bool VEC>
 __device__ __forceinline__ void store8(uint16_t* row, int col, int D, const float (&v)[kVec]) {
     uint32_t u[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = from_f32<BF16>(v[2 * j]) | (from_f32<BF16>(v[2 * j + 1]) << 16);
+    for (int j = 0; j < 4; ++j) u[j] = pack2<BF16>(v[2 * j], v[2 * j + 1]);
     if constexpr (VEC) {
         if (col < D) *reinterpret_cast<uint4*>(row + col) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
@@ -156,19 +204,20 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // The codes of eight values of a row (the thread's 16 lanes hold the block of 128 they are in) and,
 // from the first of those lanes, the block's scale. Every lane of the warp calls it.
 template <bool VEC>
-__device__ __forceinline__ void quantise8(const float (&y)[kVec], int col, int D, uint8_t* q_row, float* scale) {
+__device__ __forceinline__ void quantise8(float (&y)[kVec], int col, int D, uint8_t* q_row, float* scale) {
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) m = fmaxf(m, fabsf(y[j]));      // (fmaxf passes NaN over)
 #pragma unroll
     for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float s = fmaxf(__fdiv_rn(m, kE4m3Max), FLT_MIN);
-    // One reciprocal for the block instead of a division for each element: the quotient can be off
-    // by an fp32 ulp, which moves a code only where it lies that near to a rounding boundary.
-    const float inv = __frcp_rn(s);
+    // A product with 1 / 448 and an approximate reciprocal instead of divisions: the scale and the quotients
+    // can be off by an fp32 ulp or two, which moves a code only where it lies that near to a rounding
+    // boundary. (Exact divisions made a quarter of the kernels' instructions.)
+    const float s = fmaxf(m * (1.f / kE4m3Max), FLT_MIN);
+    mul8(y, rcp(s));
     uint32_t c[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = e4m3x2(y[2 * j] * inv, y[2 * j + 1] * inv);
+    for (int j = 0; j < 4; ++j) c[j] = e4m3x2(y[2 * j], y[2 * j + 1]);
     if (col < D) {                                   // (rows of codes start on 16-byte boundaries)
         if (VEC || col + kVec <= D) {
             *reinterpret_cast<uint2*>(q_row + col) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
@@ -189,7 +238,7 @@ struct NormArgs {
     float* scales;
     long long ldx, ldr, ldro, ldy, ldq, lds;
     int T, D;
-    float eps;
+    float eps, one_over_D;
 };
 
 // A thread holds VPT vectors of a row in registers, so the row is read once although its norm has to be known
@@ -214,7 +263,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormRows : VPT > 1 ? 512 : 1024, 
     if (WARP && t >= a.T) return;
 
     float h[VPT][kVec], w0[kVec];
-    float ss = 0.f;
+    uint64_t ss2 = 0;
     auto col_of = [&](int i) { return (i * n + tid) * kVec; };
     if constexpr (VEC || VPT > 4) {
         if constexpr (VPT == 1) load8<BF16, VEC>(a.w, col_of(0), D, w0);
@@ -224,8 +273,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormRows : VPT > 1 ? 512 : 1024, 
             if (a.r) {
                 float r[kVec];
                 load8<BF16, VEC>(a.r + t * a.ldr, col_of(i), D, r);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) h[i][j] += r[j];
+                add8(h[i], r);
             }
         }
     } else {                                         // (single elements only after every vector is under way)
@@ -242,18 +290,19 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormRows : VPT > 1 ? 512 : 1024, 
             if (a.r) {
                 float v[kVec];
                 end8<BF16, VEC>(r[i], a.r + t * a.ldr, col_of(i), D, v);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) h[i][j] += v[j];
+                add8(h[i], v);
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+        squares8(h[i], ss2);
         // the sum in the 16-bit type is for the next layer; the norm goes by the unrounded one
         if (a.r_out) store8<BF16, VEC>(a.r_out + t * a.ldro, col_of(i), D, h[i]);
     }
+    float ss, odd;
+    unpair(ss2, ss, odd);
+    ss += odd;
 #pragma unroll
     for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
     if constexpr (!WARP) {
@@ -263,14 +312,15 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormRows : VPT > 1 ? 512 : 1024, 
 #pragma unroll
         for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
     }
-    const float rstd = 1.f / sqrtf(ss / static_cast<float>(D) + a.eps);
+    const float rstd = rsqrtf(fmaf(ss, a.one_over_D, a.eps));     // (2 ulp)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int col = col_of(i);
         float w[kVec];
         if constexpr (VPT > 1) load8<BF16, VEC>(a.w, col, D, w);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) h[i][j] = h[i][j] * rstd * (VPT == 1 ? w0[j] : w[j]);
+        mul8(h[i], rstd);
+        if constexpr (VPT == 1) mul8(h[i], w0);
+        else mul8(h[i], w);
         if (a.y) store8<BF16, VEC>(a.y + t * a.ldy, col, D, h[i]);
         if (a.q) quantise8<VEC>(h[i], col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
     }
@@ -334,8 +384,11 @@ __global__ void __launch_bounds__(kGatedVecs / VPT) gated_kernel(const GatedArgs
         end8<BF16, VEC>(rg[i], row, col, D, g);
         end8<BF16, VEC>(ru[i], row + D, col, D, u);
         // silu(g) = g / (1 + exp(-g)); where exp(-g) is infinite the quotient is the limit, 0
+        float e[kVec];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) g[j] = __fdividef(g[j], 1.f + __expf(-g[j])) * u[j];
+        for (int j = 0; j < kVec; ++j) e[j] = rcp(1.f + __expf(-g[j]));
+        mul8(g, e);                                  // (before u: g u may overflow where silu(g) u does not)
+        mul8(g, u);
         quantise8<VEC>(g, col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
     }
 }
@@ -385,7 +438,7 @@ int wq4_add_rmsnorm_quant(const void* X, long long ldx, const void* R, long long
     if (const int rc = runtime(&rt)) return rc;
     const NormArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(R),
                      static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(R_out), static_cast<uint16_t*>(Y),
-                     static_cast<uint8_t*>(Q), scales, ldx, ldr, ldro, ldy, ldq, lds, T, D, eps};
+                     static_cast<uint8_t*>(Q), scales, ldx, ldr, ldro, ldy, ldq, lds, T, D, eps, 1.f / static_cast<float>(D)};
     const bool vec = D % kVec == 0 && vec_ok(X, ldx) && vec_ok(R, ldr) && vec_ok(weight, 0) && vec_ok(R_out, ldro) &&
                      vec_ok(Y, ldy);
     if (dtype == WQ4_BF16) return vec ? go_norm<true, true>(rt, a, stream) : go_norm<true, false>(rt, a, stream);
