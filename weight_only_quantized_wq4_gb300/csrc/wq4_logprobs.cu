@@ -229,22 +229,32 @@ struct LpAcc {
         z = pair(a.z, b.z);
         s = pair(a.s, b.s);
     }
-    __device__ void add(const uint4& v) {            // (m already covers v)
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        if (slow()) {
-            float z0, z1, s0, s1;
-            unpair(z, z0, z1);
-            unpair(s, s0, s1);
+    __device__ void add_slow(const uint4& v) {
+        float z0, z1, s0, s1;
+        unpair(z, z0, z1);
+        unpair(s, s0, s1);
 #pragma unroll
-            for (int j = 0; j < LpVec<DT>::kN; ++j) {
-                const float t = max_nan(LpVec<DT>::at(v, j) - m, -kFar) * kLog2e, e = ex2(t);
-                z0 += e;
-                s0 = fmaf(t, e, s0);
-            }
-            z = pair(z0, z1);
-            s = pair(s0, s1);
-            return;
+        for (int j = 0; j < LpVec<DT>::kN; ++j) {
+            const float t = max_nan(LpVec<DT>::at(v, j) - m, -kFar) * kLog2e, e = ex2(t);
+            z0 += e;
+            s0 = fmaf(t, e, s0);
         }
+        z = pair(z0, z1);
+        s = pair(s0, s1);
+    }
+    // vectors that m already covers
+    template <int U>
+    __device__ void add(const uint4 (&v)[U]) {
+        if (slow()) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) add_slow(v[u]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) add_fast(v[u]);
+        }
+    }
+    __device__ void add_fast(const uint4& v) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
         const uint64_t minus_r = pair(-ref(), -ref()), l2e = pair(kLog2e, kLog2e);
 #pragma unroll
         for (int i = 0; i < LpVec<DT>::kN / 2; ++i) {
@@ -344,13 +354,14 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
             bv = i;
             acc.move(n);
         }
-        acc.add(x);
+        const uint4 one[1] = {x};
+        acc.add(one);
     };
-    if (v == 0 && v < v1) {
+    if (v == 0 && v < v1 && !row.whole(0)) {
         edge(0);
         v += kLpThreads;
     }
-    const int last = min(v1, row.nv - 1);            // whole vectors end here
+    const int last = v1 == row.nv && !row.whole(v1 - 1) ? v1 - 1 : v1;   // whole vectors end here
     uint4 x[kLpUnroll];
     bool more = v + (kLpUnroll - 1) * kLpThreads < last;
     if (more)
@@ -376,8 +387,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
             }
         }
         if (n > acc.m) acc.move(n);
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) acc.add(y[u]);
+        acc.add(y);
     }
     for (; v < v1; v += kLpThreads) edge(v);
     // this thread's best as a bound for elements: its value and its vector's last index
