@@ -75,6 +75,14 @@ def test_gated(lib, T, D, dtype):
     check_quantised(q, s, R.silu_mul(host(x)))
 
 
+@pytest.mark.parametrize("T,D", [(33, 8), (1000, 1), (2501, 99), (1300, 128), (700, 1920), (500, 1921), (300, 4101), (150, 8193)])
+def test_gated_rows_that_share_a_cta(lib, T, D):
+    x = make(T, 2 * D, "bf16", 21, 3.0)
+    q, s = lib.silu_mul_quant(x)
+    assert lib.get_last_error() == 0
+    check_quantised(q, s, R.silu_mul(host(x)))
+
+
 @pytest.mark.parametrize("pad,offset", [(8, 0), (8, 8), (3, 0), (8, 1), (5, 3)])
 @pytest.mark.parametrize("op", ["norm", "gated"])
 def test_strided_rows_and_untouched_padding(lib, op, pad, offset):

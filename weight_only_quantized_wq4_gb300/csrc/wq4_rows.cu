@@ -358,50 +358,73 @@ struct GatedArgs {
     float* scales;
     long long ldx, ldq, lds;
     int D, chunks;                      // chunks: CTAs per row
+    int blocks, groups;                 // short rows: blocks of 128 per row, and in all
 };
 
 constexpr int kGatedVecs = 256;         // vectors of each half that a CTA takes: 2048 columns of one row
 
-// VPT vectors of each half per thread, all loaded before the first is used.
-template <bool BF16, bool VEC, int VPT>
+// VPT vectors of each half per thread, all loaded before the first is used. SHORT: each sixteen lanes take the
+// next block of 128, of whichever row, so that rows shorter than a CTA's columns leave no lanes idle.
+template <bool BF16, bool VEC, int VPT, bool SHORT>
 __global__ void __launch_bounds__(kGatedVecs / VPT) gated_kernel(const GatedArgs a) {
     constexpr int kThreads = kGatedVecs / VPT;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long t = blockIdx.x / a.chunks;
-    const int D = a.D, col0 = ((blockIdx.x % a.chunks) * kGatedVecs + threadIdx.x) * kVec;
-    const uint16_t* row = a.x + t * a.ldx;
+    const int D = a.D;
+    long long t[VPT];
+    int col[VPT];
     Raw8<VEC> rg[VPT], ru[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        rg[i] = begin8<VEC>(row, col0 + i * kThreads * kVec, D);
-        ru[i] = begin8<VEC>(row + D, col0 + i * kThreads * kVec, D);
+        if constexpr (SHORT) {
+            const unsigned g = (blockIdx.x * VPT + i) * (kThreads / 16u) + threadIdx.x / 16u;
+            const unsigned r = g / static_cast<unsigned>(a.blocks);
+            t[i] = r;
+            col[i] = (g - r * a.blocks) * kRowBlock + threadIdx.x % 16 * kVec;
+            if (g >= static_cast<unsigned>(a.groups)) t[i] = 0, col[i] = a.blocks * kRowBlock;   // (past every row's end)
+        } else {
+            t[i] = blockIdx.x / a.chunks;
+            col[i] = ((blockIdx.x % a.chunks) * kGatedVecs + i * kThreads + threadIdx.x) * kVec;
+        }
+        const uint16_t* row = a.x + t[i] * a.ldx;
+        rg[i] = begin8<VEC>(row, col[i], D);
+        ru[i] = begin8<VEC>(row + D, col[i], D);
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int col = col0 + i * kThreads * kVec;
+        const uint16_t* row = a.x + t[i] * a.ldx;
         float g[kVec], u[kVec];
-        end8<BF16, VEC>(rg[i], row, col, D, g);
-        end8<BF16, VEC>(ru[i], row + D, col, D, u);
+        end8<BF16, VEC>(rg[i], row, col[i], D, g);
+        end8<BF16, VEC>(ru[i], row + D, col[i], D, u);
         // silu(g) = g / (1 + exp(-g)); where exp(-g) is infinite the quotient is the limit, 0
         float e[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j) e[j] = rcp(1.f + __expf(-g[j]));
         mul8(g, e);                                  // (before u: g u may overflow where silu(g) u does not)
         mul8(g, u);
-        quantise8<VEC>(g, col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
+        quantise8<VEC>(g, col[i], D, a.q + t[i] * a.ldq, a.scales + (col[i] / kRowBlock) * a.lds + t[i]);
     }
 }
 
-// With more CTAs than the SMs hold at once, 64 threads with four vectors each keep more loads under way
-// (4096 x 14336 bf16: 45.1 us; 128 with two 47.2, 256 with one 52.3); with fewer, one vector each is sooner
-// done (16 x 14336: 1.4 us against 2.0).
+// Rows shorter than a CTA's columns share CTAs (16384 x 128 bf16: 3.2 us, a CTA per row 18.3; 4096 x 1408:
+// 6.6 against 7.8), and so do rows off 16-byte boundaries while a row's last CTA can be a good part of it
+// (2000 x 4101: 11.0 against 14.9; 4096 x 14335: 62.6 against 60.4). Otherwise, with more CTAs than the
+// SMs hold at once, 64 threads with four vectors each keep more loads under way (4096 x 14336 bf16:
+// 45.0 us; 128 with two 47.2, 256 with one 52.3); with fewer, one vector each is sooner done
+// (16 x 14336: 1.4 us against 2.0).
 template <bool BF16, bool VEC>
 int go_gated(const Runtime& rt, const GatedArgs& a, int T, wq4_stream_t st) {
-    const dim3 grid(static_cast<unsigned>(T) * a.chunks);
-    if (static_cast<long long>(T) * a.chunks > 8LL * rt.sm_count)
-        return launch(rt, gated_kernel<BF16, VEC, 4>, grid, kGatedVecs / 4, 0, 1, st, a);
-    return launch(rt, gated_kernel<BF16, VEC, 1>, grid, kGatedVecs, 0, 1, st, a);
+    const long long ctas = static_cast<long long>(T) * a.chunks, groups = static_cast<long long>(T) * a.blocks;
+    constexpr int kPerCta = kGatedVecs * kVec / kRowBlock;
+    if (a.blocks < (VEC ? 1 : 4) * kPerCta && groups < (1LL << 31) - kPerCta) {
+        GatedArgs s = a;
+        s.groups = static_cast<int>(groups);
+        const dim3 grid(static_cast<unsigned>((groups + kPerCta - 1) / kPerCta));
+        return launch(rt, gated_kernel<BF16, VEC, 1, true>, grid, kGatedVecs, 0, 1, st, s);
+    }
+    if (ctas > 8LL * rt.sm_count)
+        return launch(rt, gated_kernel<BF16, VEC, 4, false>, dim3(static_cast<unsigned>(ctas)), kGatedVecs / 4, 0, 1, st, a);
+    return launch(rt, gated_kernel<BF16, VEC, 1, false>, dim3(static_cast<unsigned>(ctas)), kGatedVecs, 0, 1, st, a);
 }
 
 // The quantised rows an operator writes and the product reads: rows of codes on 16-byte boundaries,
@@ -457,7 +480,8 @@ int wq4_silu_mul_quant(const void* X, long long ldx, int T, int D, int dtype, vo
     if (static_cast<long long>(T) * chunks > 0x7fffffffLL) return WQ4_ERR_UNSUPPORTED;
     Runtime rt;
     if (const int rc = runtime(&rt)) return rc;
-    const GatedArgs a{static_cast<const uint16_t*>(X), static_cast<uint8_t*>(Q), scales, ldx, ldq, lds, D, chunks};
+    const GatedArgs a{static_cast<const uint16_t*>(X), static_cast<uint8_t*>(Q), scales, ldx, ldq, lds, D, chunks,
+                      (D + kRowBlock - 1) / kRowBlock, 0};
     const bool vec = D % kVec == 0 && vec_ok(X, ldx);
     if (dtype == WQ4_BF16) return vec ? go_gated<true, true>(rt, a, T, stream) : go_gated<true, false>(rt, a, T, stream);
     return vec ? go_gated<false, true>(rt, a, T, stream) : go_gated<false, false>(rt, a, T, stream);
