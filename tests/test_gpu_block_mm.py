@@ -67,6 +67,14 @@ def test_output_types(lib, M, N, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [1, 7, 16, 50, 95])
+@pytest.mark.parametrize("N,K", [(128, 1024), (2300, 1040), (2440, 900), (3000, 1536), (3700, 656), (5000, 400), (6000, 640), (2560, 1536), (2000, 896)])
+def test_tiles_shared_by_clusters_of_every_size(lib, M, N, K, dtype):
+    """1 to 47 tiles, each cut along K for 8 CTAs down to 2."""
+    check(lib, M, N, K // 16 * 16, dtype, seed=M)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("offset,pad", [(0, 3), (1, 8), (8, 8)])
 @pytest.mark.parametrize("M,N", [(5, 200), (90, 333), (2100, 2300)])
 def test_strided_output_and_untouched_padding(lib, M, N, offset, pad, dtype):

@@ -52,8 +52,8 @@ struct BmArgs {
     int lane_tiles, tiles;                     // tile t: lane tile t % lane_tiles, column tile t / lane_tiles
     int split;                                 // CTAs per cluster, each with a part of K (1: none)
     int stages;                                // of the ring: an even number
-    int red_cols, red_shift;                   // split: weights on the lanes: columns of a tile that are joined, and
-                                               // how many (2^shift) per CTA; tokens on the lanes: split = 2^shift
+    int share;                                 // split: columns that a rank joins (weights on the lanes), or columns of
+                                               // every fold thread (tokens on the lanes, a multiple of 8)
     int dtype;
     int unit;                                  // bytes that a row of Y is stored by: 16, or what its start allows
     unsigned int* status;
@@ -83,9 +83,9 @@ struct BmCfg {
     static constexpr int kScBlocks = 8, kScRing = TOK_LANES ? 3 : 0, kScBytes = kScBlocks * kBmLanes * 4;
     // An even number of stages (fit) and of P buffers: the MMA warps take alternate blocks, so each walks
     // every phase of its own ones (a parity wait is unambiguous one phase ahead only).
-    // Shared memory before the stages, and the parts of a tile that other CTAs of a cluster send (kRedBytes)
+    // Shared memory before the stages, and the most that the parts other CTAs of a cluster send may take
     static constexpr int kHeadBytes = 128 + 1024 + kBarBytes + kScRing * kScBytes + kFW * kWarpBytes;
-    static constexpr int kRedBytes = PAIR ? 0 : NT * kBmLanes * 4;
+    static constexpr int kRedBytes = PAIR ? 0 : TOK_LANES ? NT * kBmLanes * 4 : (NT + 8) * kBmLanes * 4;
     static constexpr int fit(int red) { return ((kBmMaxSmem - kHeadBytes - red) / kStageBytes > 12 ? 12 : (kBmMaxSmem - kHeadBytes - red) / kStageBytes) & ~1; }
     static constexpr int kHalfStages = ((115712 - kHeadBytes) / kStageBytes) & ~1;   // two CTAs of an SM: that many bytes each
     static constexpr int kPBufs = NT <= 128 ? 4 : 2;
@@ -386,9 +386,8 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
         mbar_init(stall_bar, 1);
         if (!PAIR && a.split > 1) {                  // the bytes of the parts of this CTA's columns
             mbar_init(red_bar, 1);
-            const int own = min(max(a.red_cols - (rank << a.red_shift), 0), 1 << a.red_shift);
-            mbar_arrive_expect_tx(red_bar, TOK_LANES ? (a.split - 1) * (NT / a.split) * kBmLanes * 4
-                                                     : own * a.split * kBmLanes * 4);
+            const int own = min(max((TOK_LANES ? C::kNC : a.M) - rank * a.share, 0), a.share);
+            mbar_arrive_expect_tx(red_bar, own * kBmLanes * 4 * (TOK_LANES ? (a.split - 1) * C::kParts : a.split));
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -642,50 +641,57 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
             const BmSched s(a, rank, PAIR);          // (one tile per cluster)
             const int l0 = s.t % a.lane_tiles * kBmLanes, c0 = s.t / a.lane_tiles * NT;
             if constexpr (TOK_LANES) {
-                // Each rank joins a 1 / split of every fold thread's columns, so that the thread that holds a column's
-                // part here joins it there: [rank][fold part][four columns][lane], its own part by a plain store.
-                constexpr int kQuads = C::kNC / 4, kLog = kQuads == 16 ? 4 : 5;
-                static_assert(kQuads == 1 << kLog, "columns of a fold thread");
-                const int lg = kLog - a.red_shift;                           // 2^lg: a rank's share, in fours
-                const int me = s_red + ((part << lg) * kBmLanes + r) * 16, step = (C::kParts << lg) * kBmLanes * 16;
-                auto slot = [&](int src, int q) { return static_cast<uint32_t>(me + src * step + q * (kBmLanes * 16)); };
+                // Each rank joins `share` of every fold thread's columns, so that the thread that holds a column's
+                // part here joins it there: [source][fold part][four columns][lane]. Its own part waits where the
+                // ring's stages were: every MMA that read them has ended.
+                const int quads = a.share / 4, mine = rank * a.share, own = min(C::kNC - mine, a.share);
+                const uint32_t at = (part * quads * kBmLanes + r) * 16, step = C::kParts * quads * kBmLanes * 16;
+                int owner = 0, q = 0;
 #pragma unroll
                 for (int j = 0; j < C::kNC; j += 4) {
-                    const int owner = (j / 4) >> lg, q = (j / 4) & ((1 << lg) - 1);
+                    const uint32_t off = at + q * (kBmLanes * 16);
                     if (owner == rank)
-                        sts128(slot(rank, q), __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
+                        sts128(s_ring + off, __float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
                                __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3]));
                     else
-                        st_async4(map_to_rank(slot(rank, q), owner), acc + j, map_to_rank(red_bar, owner));
+                        st_async4(map_to_rank(s_red + off + (rank - (rank > owner)) * step, owner), acc + j,
+                                  map_to_rank(red_bar, owner));
+                    if (++q == quads) q = 0, ++owner;
                 }
-                if (mbar_wait(red_bar, 0, ctl)) {
+                if (own > 0 && mbar_wait(red_bar, 0, ctl)) {
+                    int done = 0;                    // columns
                     auto join = [&](auto columns) {
                         constexpr int kCnt = decltype(columns)::value;
                         float v[kCnt];
 #pragma unroll
-                        for (int q = 0; q < kCnt; ++q) v[q] = 0.f;
-                        for (int o = 0; o < a.split; ++o)
+                        for (int i = 0; i < kCnt; ++i) v[i] = 0.f;
+                        for (int o = 0; o < a.split; ++o) {
+                            const uint32_t from = (o == rank ? s_ring : s_red + (o - (o > rank)) * step) + at +
+                                                  done / 4 * (kBmLanes * 16);
 #pragma unroll
-                            for (int q = 0; q < kCnt / 4; ++q) {
-                                const uint4 x = lds128(slot(o, q));
-                                v[4 * q] += __uint_as_float(x.x), v[4 * q + 1] += __uint_as_float(x.y);
-                                v[4 * q + 2] += __uint_as_float(x.z), v[4 * q + 3] += __uint_as_float(x.w);
+                            for (int i = 0; i < kCnt / 4; ++i) {
+                                const uint4 x = lds128(from + i * (kBmLanes * 16));
+                                v[4 * i] += __uint_as_float(x.x), v[4 * i + 1] += __uint_as_float(x.y);
+                                v[4 * i + 2] += __uint_as_float(x.z), v[4 * i + 3] += __uint_as_float(x.w);
                             }
-                        store_rows<kCnt>(a, buf, lane, l0 + r - lane, c0 + part * C::kNC + rank * kCnt, v);
+                        }
+                        store_rows<kCnt>(a, buf, lane, l0 + r - lane, c0 + part * C::kNC + mine + done, v);
+                        done += kCnt;
                     };
-                    if (a.split == 2) join(std::integral_constant<int, C::kNC / 2>());
-                    else if (a.split == 4) join(std::integral_constant<int, C::kNC / 4>());
-                    else join(std::integral_constant<int, C::kNC / 8>());
+                    if (own & 32) join(std::integral_constant<int, 32>());
+                    if (own & 16) join(std::integral_constant<int, 16>());
+                    if (own & 8) join(std::integral_constant<int, 8>());
                 }
             } else {
+                int owner = 0, at = 0;
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const int owner = j >> a.red_shift, at = j & ((1 << a.red_shift) - 1);
-                    if (j >= a.red_cols) break;
-                    st_async(map_to_rank(s_red + ((((rank << a.red_shift) + at) * kBmLanes) + r) * 4, owner), acc[j],
+                    if (j >= a.M) break;
+                    st_async(map_to_rank(s_red + ((rank * a.share + at) * kBmLanes + r) * 4, owner), acc[j],
                              map_to_rank(red_bar, owner));
+                    if (++at == a.share) at = 0, ++owner;
                 }
-                const int first = rank << a.red_shift, own = min(a.red_cols - first, 1 << a.red_shift);
+                const int first = rank * a.share, own = min(a.M - first, a.share);
                 if (own > 0 && mbar_wait(red_bar, 0, ctl)) {
                     constexpr int kCnt = 4;
                     for (int c = 0; c < own; c += kCnt) {
@@ -693,7 +699,7 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
 #pragma unroll
                         for (int q = 0; q < kCnt; ++q) v[q] = 0.f;
                         for (int o = 0; o < a.split; ++o) {
-                            const uint32_t from = s_red + ((((o << a.red_shift) + c) * kBmLanes) + r) * 4;
+                            const uint32_t from = s_red + ((o * a.share + c) * kBmLanes + r) * 4;
 #pragma unroll
                             for (int q = 0; q < kCnt; ++q)
                                 if (c + q < own) v[q] += lds_f32(from + q * (kBmLanes * 4));
@@ -784,8 +790,34 @@ int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) 
     const long long tiles = static_cast<long long>(a.lane_tiles) * ((cols + NT - 1) / NT);
     if (tiles > (1 << 30)) return WQ4_ERR_UNSUPPORTED;
     a.tiles = static_cast<int>(tiles);
+    // CTAs per tile: what leaves each the fewest blocks of K, and of those the fewest. Clusters of s lie within
+    // groups of SMs, so that fewer than sm_count / s run at a time: the occupancy calculation says how many
+    // (95 x 2432 x 2176, 19 tiles: 13.9 us with 8 CTAs each, in two waves; 8.1 with 6).
     a.split = 1;
-    while (!PAIR && a.split < 8 && 2 * a.split * tiles <= rt.sm_count && 2 * a.split <= a.kb) a.split *= 2;
+    for (int s = 2; !PAIR && s <= 8 && s <= a.kb && s * tiles <= rt.sm_count; ++s) {
+        if (TOK_LANES && (s == 6 || s == 7)) continue;      // (their parts leave the ring fewer than four stages)
+        if ((a.kb + s - 1) / s >= (a.kb + a.split - 1) / a.split) continue;
+        static int resident[9];                      // (one value per kernel and s, whoever writes it)
+        if (!resident[s]) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(s);
+            cfg.blockDim = dim3(C::kThreads);
+            cfg.dynamicSmemBytes = kBmMaxSmem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = s;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                return WQ4_ERR_CUDA;
+            }
+            resident[s] = n > 0 ? n : -1;
+        }
+        if (tiles <= resident[s]) a.split = s;
+    }
     // More narrow tiles than SMs (and no whole number of waves of them): rings of half the size, two CTAs per SM
     // (4 x 28672 x 4096: 21.1 us; one CTA with the whole ring 23.6).
     constexpr bool kHalf = !TOK_LANES && NT <= 32;
@@ -793,12 +825,12 @@ int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) 
     const int most = PAIR ? rt.sm_count / 2 : half ? 2 * rt.sm_count : rt.sm_count;   // tiles at a time
     const int grid = PAIR ? 2 * (a.tiles < most ? a.tiles : most) : a.split > 1 ? a.tiles * a.split : a.tiles < most ? a.tiles : most;
     // no more stages than a CTA has blocks: with few, the next launch's CTAs fit beside this one's
-    const int red = a.split > 1 ? C::kRedBytes : 0, blocks = (a.kb + a.split - 1) / a.split;
+    a.share = TOK_LANES ? 8 * ((C::kNC / 8 + a.split - 1) / a.split) : (a.M + a.split - 1) / a.split;
+    const int red = a.split == 1 ? 0 : kBmLanes * 4 * a.share * (TOK_LANES ? (a.split - 1) * C::kParts : a.split);
+    const int blocks = (a.kb + a.split - 1) / a.split;
     a.stages = half ? C::kHalfStages : C::fit(red);
     if (a.split > 1 && blocks < a.stages) a.stages = blocks < 4 ? 4 : (blocks + 1) & ~1;
     const int smem = C::kHeadBytes + a.stages * C::kStageBytes + red;
-    a.red_cols = a.M;
-    while (TOK_LANES ? (1 << a.red_shift) < a.split : (a.split << a.red_shift) < a.red_cols) ++a.red_shift;
     if (rt.trace)
         std::fprintf(stderr, "wq4: block_mm M=%d N=%d K=%d lanes=%s columns=%d pair=%d grid=%d split=%d\n", a.M, a.N, c.K,
                      TOK_LANES ? "tokens" : "weights", NT, PAIR ? 1 : 0, grid, a.split);
@@ -849,7 +881,11 @@ extern "C" int wq4_block_mm(const void* X, long long ldx, const float* x_scales,
     if (M <= 16) return go_block_mm<16, false, false>(rt, c, a, stream);
     if (M <= 32) return go_block_mm<32, false, false>(rt, c, a, stream);
     if (M <= 64) return go_block_mm<64, false, false>(rt, c, a, stream);
-    const long long wide = static_cast<long long>((M + 127) / 128) * ((N + 255) / 256);
-    if (2 * wide > rt.sm_count) return go_block_mm<256, true, true>(rt, c, a, stream);
+    // A wave of pair tiles takes 1.5 times as long as one of 128-column tiles, and covers twice as much of Y
+    // (1109 x 3840 x 7168: 26.9 us in one wave of pairs, 34.3 in two of the others; 877 x 10019 x 4736: 55.2
+    // in three of pairs, 49.3 in four of the others).
+    const long long rows = (M + 127) / 128, cols = (N + 127) / 128, one = rt.sm_count, pairs = rt.sm_count / 2;
+    const long long w128 = (rows * cols + one - 1) / one, w256 = ((rows + 1) / 2 * ((cols + 1) / 2) + pairs - 1) / pairs;
+    if (3 * w256 <= 2 * w128) return go_block_mm<256, true, true>(rt, c, a, stream);
     return go_block_mm<128, true, false>(rt, c, a, stream);
 }
