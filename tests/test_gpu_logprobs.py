@@ -120,6 +120,27 @@ def test_nan_and_inf_rows(lib, dtype):
     check(lib, x, 4)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("T,V,k", [(330, 50, 20), (700, 50, 32), (330, 4097, 32), (700, 4096, 20), (330, 20001, 5), (700, 20000, 32),
+                                   (1300, 1003, 7)])
+def test_many_rows_of_every_kind(lib, dtype, T, V, k, pad):
+    """As many rows as are taken by fewer threads each: a thread adds V / 128 terms then, below 2e-5 all the same."""
+    x = make(T, V, dtype, T + V, pad)
+    low = torch.finfo(TYPES[dtype]).min
+    x[0::11] = -float("inf")
+    x[1::11] = low
+    x[2::11, V // 2:] = -float("inf")
+    x[3::11, 3:] = low
+    x[4::11, 7:] = -float("inf")
+    x[5::11] = 0.5
+    x[6::11] = torch.linspace(-9, 9, V, device="cuda").to(TYPES[dtype])
+    x[7::11] = torch.linspace(9, -9, V, device="cuda").to(TYPES[dtype])
+    x[8::11, 16::512] += 40.0
+    x[9::11, V // 3] = float("nan")
+    check(lib, x, k)
+
+
 def test_tokens_outside_the_vocabulary(lib):
     x = make(5, 700, "fp32", 7)
     check(lib, x, 1, torch.tensor([-1, 700, 699, 0, -(1 << 40)], device="cuda"))

@@ -18,7 +18,7 @@
 // The k most likely tokens need no second pass over the row. A thread remembers the largest vector
 // it saw (its maximum and where, the first among equals). 64 groups of 8 threads make 64 such
 // bests; the k-th largest of them, tau, is a bound that at least k elements reach, so only threads
-// whose own best reaches it can hold an answer, about k of 512. Their vectors (V / 512 elements each)
+// whose own best reaches it can hold an answer, about k of them. Their vectors (V / 512 elements each)
 // are read again by whole warps; the elements that reach tau, a few dozen, are ranked by counting. An element's order is one 64-bit key: the float
 // as an unsigned integer of the same order, then the complement of its index, so that equal logits
 // rank by the lower index and no two keys are equal.
@@ -36,10 +36,8 @@
 namespace wq4 {
 namespace {
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpThreads = 512;               // of a CTA (128 or 256 where there are many rows)
 constexpr int kLpGroups = 64;                 // bests that bound the k-th largest
-constexpr int kLpParts = kLpThreads / kLpGroups;
 constexpr int kLpMaxTop = 32;
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpUnroll = 4;                  // vectors of a thread in flight
@@ -288,14 +286,15 @@ __device__ __forceinline__ void st_async(uint32_t addr, const LpStat& v, uint32_
                  : "memory");
 }
 
+template <int THREADS>
 struct LpShared {
-    float2 stat[kLpWarps];                           // warps' z and s, with the CTA's m
+    float2 stat[THREADS / 32];                       // warps' z and s, with the CTA's m
     LpStat total;
     unsigned long long best[kLpGroups];
     int above[kLpGroups];                            // bests above each
     int n, flagged;
-    uint16_t flag[kLpThreads];                       // threads whose best reaches tau
-    unsigned long long cand[kLpWarps * kLpMaxTop];
+    uint16_t flag[THREADS];                          // threads whose best reaches tau
+    unsigned long long cand[THREADS];                // its room is an ordered list of every warp's
     int rank[kLpMaxCluster * kLpMaxTop];             // of the clusters' lists
     // what rank 0 is sent by the cluster's CTAs: their statistics and their lists
     float4 part_stat[kLpMaxCluster];
@@ -310,12 +309,14 @@ __device__ __forceinline__ unsigned long long shfl_xor_max(unsigned long long v,
     return o > v ? o : v;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a) {
+// THREADS: of a CTA, which takes a row or, in a cluster (of kLpThreads only), a part of one.
+template <int DT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const LpArgs a) {
     using Vec = LpVec<DT>;
-    __shared__ LpShared sh;
+    constexpr int kWarps = THREADS / 32, kParts = THREADS / kLpGroups;
+    __shared__ LpShared<THREADS> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int C = THREADS == kLpThreads ? a.cluster : 1, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     const long long t = C > 1 ? blockIdx.x / C : blockIdx.x;
     if (C > 1) {
         if (tid == 0) {
@@ -359,44 +360,44 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
     };
     if (v == 0 && v < v1 && !row.whole(0)) {
         edge(0);
-        v += kLpThreads;
+        v += THREADS;
     }
     const int last = v1 == row.nv && !row.whole(v1 - 1) ? v1 - 1 : v1;   // whole vectors end here
     uint4 x[kLpUnroll];
-    bool more = v + (kLpUnroll - 1) * kLpThreads < last;
+    bool more = v + (kLpUnroll - 1) * THREADS < last;
     if (more)
 #pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) x[u] = row.load(v + u * kLpThreads);
+        for (int u = 0; u < kLpUnroll; ++u) x[u] = row.load(v + u * THREADS);
     while (more) {
         uint4 y[kLpUnroll];
         const int at = v;
-        v += kLpUnroll * kLpThreads;
-        more = v + (kLpUnroll - 1) * kLpThreads < last;
+        v += kLpUnroll * THREADS;
+        more = v + (kLpUnroll - 1) * THREADS < last;
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) y[u] = x[u];
         if (more)                                    // the next batch is on its way while this one is added in
 #pragma unroll
-            for (int u = 0; u < kLpUnroll; ++u) x[u] = row.load(v + u * kLpThreads);
+            for (int u = 0; u < kLpUnroll; ++u) x[u] = row.load(v + u * THREADS);
         float n = acc.m;
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) {
             const float vm = Vec::max(y[u]);
             if (vm > n) {
                 n = vm;
-                bv = at + u * kLpThreads;
+                bv = at + u * THREADS;
             }
         }
         if (n > acc.m) acc.move(n);
         acc.add(y);
     }
-    for (; v < v1; v += kLpThreads) edge(v);
+    for (; v < v1; v += THREADS) edge(v);
     // this thread's best as a bound for elements: its value and its vector's last index
     const unsigned long long best =
         bv < 0 ? 0ull : key_of(acc.m, min(bv * Vec::kN + Vec::kN - 1 - row.head, a.V - 1));
     unsigned long long g = best;
 #pragma unroll
-    for (int d = 1; d < kLpThreads / kLpGroups; d <<= 1) g = shfl_xor_max(g, d);
-    if (tid % (kLpThreads / kLpGroups) == 0) sh.best[tid / (kLpThreads / kLpGroups)] = g;
+    for (int d = 1; d < kParts; d <<= 1) g = shfl_xor_max(g, d);
+    if (tid % kParts == 0) sh.best[tid / kParts] = g;
     if (tid == 0) {
         sh.n = 0;
         sh.flagged = 0;
@@ -421,15 +422,15 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
         const unsigned long long mine = sh.best[tid % kLpGroups];
         int above = 0;
 #pragma unroll
-        for (int i = 0; i < kLpGroups / kLpParts; ++i)
-            above += sh.best[tid / kLpGroups * (kLpGroups / kLpParts) + i] > mine ? 1 : 0;
+        for (int i = 0; i < kLpGroups / kParts; ++i)
+            above += sh.best[tid / kLpGroups * (kLpGroups / kParts) + i] > mine ? 1 : 0;
         if (above) atomicAdd(&sh.above[tid % kLpGroups], above);
     }
     __syncthreads();
-    if (warp == kLpWarps - 1) {
-        float2 w = lane < kLpWarps ? sh.stat[lane] : make_float2(0.f, 0.f);
+    if (warp == kWarps - 1) {
+        float2 w = lane < kWarps ? sh.stat[lane] : make_float2(0.f, 0.f);
 #pragma unroll
-        for (int d = kLpWarps / 2; d; d >>= 1) {
+        for (int d = kWarps / 2; d; d >>= 1) {
             w.x += __shfl_xor_sync(0xffffffffu, w.x, d);
             w.y += __shfl_xor_sync(0xffffffffu, w.y, d);
         }
@@ -456,26 +457,26 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
         const uint32_t tau_order = static_cast<uint32_t>(tau >> 32);
         // The flagged threads' vectors, dealt out over the warps in units of 32: a thread has `per`, and as many
         // threads as fit share a unit. A warp's loads are under way together, kUnits at a time.
-        const int per = (v1 - v0 + kLpThreads - 1) / kLpThreads;
+        const int per = (v1 - v0 + THREADS - 1) / THREADS;
         const int shift = per <= 1 ? 0 : per >= 32 ? 5 : 32 - __clz(per - 1);
         const int rounds = (per + 31) >> 5, flagged = sh.flagged;
         const int units = (flagged << shift) + 31 >> 5;
         constexpr int kUnits = 4;
         auto second_look = [&](auto&& offer) {
             for (int r = 0; r < rounds; ++r) {
-                for (int u0 = warp; u0 < units; u0 += kUnits * kLpWarps) {
+                for (int u0 = warp; u0 < units; u0 += kUnits * kWarps) {
                     uint4 y[kUnits];
                     int w[kUnits];
 #pragma unroll
                     for (int i = 0; i < kUnits; ++i) {
-                        const int slot = (u0 + i * kLpWarps) * 32 + lane;     // of the flagged threads' vectors
+                        const int slot = (u0 + i * kWarps) * 32 + lane;     // of the flagged threads' vectors
                         const int who = slot >> shift;
-                        w[i] = who < flagged ? v0 + sh.flag[who] + (r * 32 + (slot & ((1 << shift) - 1))) * kLpThreads : v1;
+                        w[i] = who < flagged ? v0 + sh.flag[who] + (r * 32 + (slot & ((1 << shift) - 1))) * THREADS : v1;
                         y[i] = w[i] < v1 ? row.load_edge(w[i]) : Vec::none();
                     }
 #pragma unroll
                     for (int i = 0; i < kUnits; ++i)
-                        if (u0 + i * kLpWarps < units) offer(y[i], w[i]);
+                        if (u0 + i * kWarps < units) offer(y[i], w[i]);
                 }
             }
         };
@@ -490,13 +491,13 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
                     const unsigned long long key = f > kNegInf ? key_of(f, w * Vec::kN - row.head + j) : 0ull;
                     if (key > floor0) {
                         const int at = atomicAdd(&sh.n, 1);
-                        if (at < kLpWarps * kLpMaxTop) sh.cand[at] = key;
+                        if (at < THREADS) sh.cand[at] = key;
                     }
                 }
             }
         });
         __syncthreads();
-        if (sh.n > kLpWarps * kLpMaxTop) {           // (the same for every thread)
+        if (sh.n > THREADS) {                        // (the same for every thread)
             __syncthreads();
             if (tid == 0) sh.n = 0;
             __syncthreads();
@@ -585,12 +586,12 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
             }
             if (lane == 0) sh.total = LpStat{n, w.z, w.s};
         }
-        for (int i = tid; i < C * kLpMaxTop; i += kLpThreads) sh.rank[i] = 0;
+        for (int i = tid; i < C * kLpMaxTop; i += THREADS) sh.rank[i] = 0;
         if (tid < kLpMaxTop) sh.top[tid] = 0;
         __syncthreads();
         if (a.k > 0) {                               // ranked by counting, two threads to a key
-            const int keys = C * a.k, i = tid & (kLpThreads / 2 - 1), from = tid < kLpThreads / 2 ? 0 : keys / 2;
-            const int to = tid < kLpThreads / 2 ? keys / 2 : keys;
+            const int keys = C * a.k, i = tid & (THREADS / 2 - 1), from = tid < THREADS / 2 ? 0 : keys / 2;
+            const int to = tid < THREADS / 2 ? keys / 2 : keys;
             const unsigned long long mine = i < keys ? sh.part_top[i] : 0;
             if (mine) {
                 int above = 0;
@@ -615,6 +616,13 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a)
     }
     if (tid == 32 && a.entropy) a.entropy[t] = nothing ? 0.f : logz - kLn2 * (all.s / all.z);
     if (tid == 64 && a.logprobs) a.logprobs[t] = asked == asked ? logp(asked) : asked;
+}
+
+template <int DT>
+int go_logprobs(const Runtime& rt, const LpArgs& a, int threads, dim3 grid, wq4_stream_t st) {
+    if (threads == 128) return launch(rt, logprobs_kernel<DT, 128>, grid, 128, 0, 1, st, a);
+    if (threads == 256) return launch(rt, logprobs_kernel<DT, 256>, grid, 256, 0, 1, st, a);
+    return launch(rt, logprobs_kernel<DT, kLpThreads>, grid, kLpThreads, 0, a.cluster, st, a);
 }
 
 }  // namespace
@@ -645,9 +653,23 @@ extern "C" int wq4_token_logprobs(const void* logits, long long ld, const long l
     if (static_cast<long long>(T) * C > 0x7fffffffLL) return WQ4_ERR_UNSUPPORTED;
     const LpArgs a{logits, tokens, logprobs, entropy, top_logprobs, top_ids, ld, V, top_k, C, rt.status, rt.timeout_cycles};
     const dim3 grid(static_cast<unsigned>(T) * C);
-    switch (dtype) {
-        case WQ4_BF16: return launch(rt, logprobs_kernel<kLpBf16>, grid, kLpThreads, 0, C, stream, a);
-        case WQ4_FP16: return launch(rt, logprobs_kernel<kLpFp16>, grid, kLpThreads, 0, C, stream, a);
-        default: return launch(rt, logprobs_kernel<kLpFp32>, grid, kLpThreads, 0, C, stream, a);
+    // Many rows: fewer threads per row, so that more rows share what the steps after the pass cost each of them
+    // (2048 x 8192 bf16, top 8: 14.7 us with 128 threads, 21.0 with 256, 38.3 with 512), unless the waves or the
+    // length say otherwise (700 x 128256: 45.1 us with 512, 54.0 with 256, 61.2 with 128; 2048 x 131072:
+    // 109, 116, 149). An SM holds 1024 threads; a wave takes as long as a thread needs for its share of
+    // a row, and the steps after the pass are worth some 200 bytes of that. Fewer threads per row also
+    // leave more of the last wave empty, as CTAs do not end together: an eighth, three eighths on top.
+    int threads = kLpThreads;
+    if (C == 1) {
+        const long long bytes = static_cast<long long>(V) * (16 / vec);
+        auto cost = [&](int th) {
+            const long long at_once = static_cast<long long>(rt.sm_count) * (1024 / th);
+            return (T + at_once - 1) / at_once * (200 + bytes * (th == 128 ? 11 : th == 256 ? 9 : 8) / (8 * th));
+        };
+        for (const int th : {256, 128})
+            if (cost(th) < cost(threads)) threads = th;
     }
+    return dtype == WQ4_BF16   ? go_logprobs<kLpBf16>(rt, a, threads, grid, stream)
+           : dtype == WQ4_FP16 ? go_logprobs<kLpFp16>(rt, a, threads, grid, stream)
+                               : go_logprobs<kLpFp32>(rt, a, threads, grid, stream);
 }
