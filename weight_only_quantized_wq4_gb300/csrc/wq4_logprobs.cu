@@ -23,8 +23,10 @@
 // as an unsigned integer of the same order, then the complement of its index, so that equal logits
 // rank by the lower index and no two keys are equal.
 //
-// Bound by memory and by instructions for many rows (each logit is read once). For few rows a cluster of
-// CTAs shares a row; each sends its statistics and list to the first through distributed shared memory.
+// Bound by memory and by instructions for many rows (each logit is read once): 2048 x 131072 bf16 109 us
+// (4.9 TB/s), of which the steps after the pass, some 850 instructions a warp, are a tenth. For few
+// rows a cluster of CTAs shares a row; each sends its statistics and list to the first through
+// distributed shared memory. That is a chain of latencies: 1 x 131072 fp32 6.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
