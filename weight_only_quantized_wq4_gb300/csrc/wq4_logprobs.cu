@@ -349,27 +349,30 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     LpAcc<DT> acc;
     int bv = -1;                                     // the vector of this thread's maximum, acc.m
     int v = v0 + tid;
-    // one vector, which may be the row's first or last and partly outside it
-    auto edge = [&](int i) {
-        const uint4 x = row.load_edge(i);
-        const float n = Vec::max(x);
-        if (n > acc.m) {
-            bv = i;
-            acc.move(n);
-        }
-        const uint4 one[1] = {x};
-        acc.add(one);
-    };
-    if (v == 0 && v < v1 && !row.whole(0)) {
-        edge(0);
-        v += THREADS;
-    }
+    // the row's first and last vector, where they are partly outside it, are taken at the end
+    const bool head = v == 0 && v < v1 && !row.whole(0);
+    if (head) v += THREADS;
     const int last = v1 == row.nv && !row.whole(v1 - 1) ? v1 - 1 : v1;   // whole vectors end here
     uint4 x[kLpUnroll];
     bool more = v + (kLpUnroll - 1) * THREADS < last;
     if (more)
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) x[u] = row.load(v + u * THREADS);
+    // vectors from `at` on; the thread's maximum is its first of equal ones
+    auto take = [&](const auto& y, int at) {
+        constexpr int kY = sizeof(y) / sizeof(uint4);
+        float n = acc.m;
+#pragma unroll
+        for (int u = 0; u < kY; ++u) {
+            const float vm = Vec::max(y[u]);
+            if (vm > n) {
+                n = vm;
+                bv = at + u * THREADS;
+            }
+        }
+        if (n > acc.m) acc.move(n);
+        acc.add(y);
+    };
     while (more) {
         uint4 y[kLpUnroll];
         const int at = v;
@@ -380,19 +383,31 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         if (more)                                    // the next batch is on its way while this one is added in
 #pragma unroll
             for (int u = 0; u < kLpUnroll; ++u) x[u] = row.load(v + u * THREADS);
-        float n = acc.m;
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
-            const float vm = Vec::max(y[u]);
-            if (vm > n) {
-                n = vm;
-                bv = at + u * THREADS;
-            }
-        }
-        if (n > acc.m) acc.move(n);
-        acc.add(y);
+        take(y, at);
     }
-    for (; v < v1; v += THREADS) edge(v);
+    // What is left, fewer whole vectors than a batch and the edges, on its way together as well.
+    const bool tail = last < v1 && tid == (last - v0) % THREADS && !(head && last == 0);
+    if (v < last || head || tail) {
+        uint4 y[kLpUnroll - 1], one[1], e[1];
+        const bool some = v + THREADS < last;        // (most short rows leave one)
+        if (some) {
+#pragma unroll
+            for (int u = 0; u < kLpUnroll - 1; ++u) y[u] = v + u * THREADS < last ? row.load(v + u * THREADS) : Vec::none();
+        } else if (v < last) {
+            one[0] = row.load(v);
+        }
+        if (head || tail) e[0] = row.load_edge(head ? 0 : last);
+        if (some) take(y, v);
+        else if (v < last) take(one, v);
+        if (head) {                                  // (before the others in the row: it wins among equals)
+            const float n = Vec::max(e[0]);
+            if (n >= acc.m && n > kNegInf) bv = 0;
+            if (n > acc.m) acc.move(n);
+            acc.add(e);
+            if (tail) e[0] = row.load_edge(last);
+        }
+        if (tail) take(e, last);
+    }
     // this thread's best as a bound for elements: its value and its vector's last index
     const unsigned long long best =
         bv < 0 ? 0ull : key_of(acc.m, min(bv * Vec::kN + Vec::kN - 1 - row.head, a.V - 1));
