@@ -16,12 +16,13 @@
 // only), a thread subtracts and multiplies instead.
 //
 // The k most likely tokens need no second pass over the row. A thread remembers the largest vector
-// it saw (its maximum and where, the first among equals). 64 groups of 8 threads make 64 such
-// bests; the k-th largest of them, tau, is a bound that at least k elements reach, so only threads
-// whose own best reaches it can hold an answer, about k of them. Their vectors (V / 512 elements each)
-// are read again by whole warps; the elements that reach tau, a few dozen, are ranked by counting. An element's order is one 64-bit key: the float
-// as an unsigned integer of the same order, then the complement of its index, so that equal logits
-// rank by the lower index and no two keys are equal.
+// it saw (its maximum and where, the first among equals). 64 groups of threads make 64 such bests (a
+// group's threads are 64 apart, so that logits next to one another fall to different groups); the
+// k-th largest of them, tau, is a bound that at least k elements reach, so only threads whose own
+// best reaches it can hold an answer, about k of them. Their vectors (V / 512 elements each) are
+// read again by whole warps; the elements that reach tau, a few dozen, are ranked by counting. An
+// element's order is one 64-bit key: the float as an unsigned integer of the same order, then the
+// complement of its index, so that equal logits rank by the lower index and no two keys are equal.
 //
 // Bound by memory and by instructions for many rows (each logit is read once): 2048 x 131072 bf16 109 us
 // (4.9 TB/s), of which the steps after the pass, some 850 instructions a warp, are a tenth. For few
@@ -296,7 +297,8 @@ struct LpShared {
     int above[kLpGroups];                            // bests above each
     int n, flagged;
     uint16_t flag[THREADS];                          // threads whose best reaches tau
-    unsigned long long cand[THREADS];                // its room is an ordered list of every warp's
+    static constexpr int kCand = THREADS < 256 ? 256 : THREADS;
+    unsigned long long cand[kCand];                // its room is an ordered list of every warp's
     int rank[kLpMaxCluster * kLpMaxTop];             // of the clusters' lists
     // what rank 0 is sent by the cluster's CTAs: their statistics and their lists
     float4 part_stat[kLpMaxCluster];
@@ -305,11 +307,6 @@ struct LpShared {
     int abort;
     unsigned long long top[kLpMaxTop];               // this CTA's best, in order, 0 where there are fewer
 };
-
-__device__ __forceinline__ unsigned long long shfl_xor_max(unsigned long long v, int d) {
-    const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, d);
-    return o > v ? o : v;
-}
 
 // THREADS: of a CTA, which takes a row or, in a cluster (of kLpThreads only), a part of one.
 template <int DT, int THREADS>
@@ -411,16 +408,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     // this thread's best as a bound for elements: its value and its vector's last index
     const unsigned long long best =
         bv < 0 ? 0ull : key_of(acc.m, min(bv * Vec::kN + Vec::kN - 1 - row.head, a.V - 1));
-    unsigned long long g = best;
-#pragma unroll
-    for (int d = 1; d < kParts; d <<= 1) g = shfl_xor_max(g, d);
-    if (tid % kParts == 0) sh.best[tid / kParts] = g;
+    sh.cand[tid] = best;
     if (tid == 0) {
         sh.n = 0;
         sh.flagged = 0;
     }
     if (tid < kLpMaxTop) sh.top[tid] = 0;
-    if (tid < kLpGroups) sh.above[tid] = 0;
+    __syncthreads();
+    if (tid < kLpGroups) {                           // a group's threads are kLpGroups apart
+        unsigned long long g = sh.cand[tid];
+#pragma unroll
+        for (int i = 1; i < kParts; ++i) g = max(g, sh.cand[tid + i * kLpGroups]);
+        sh.best[tid] = g;
+        sh.above[tid] = 0;
+    }
     __syncthreads();
 
     // ---- the CTA's m, every thread's sums with it, and tau
@@ -508,13 +509,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
                     const unsigned long long key = f > kNegInf ? key_of(f, w * Vec::kN - row.head + j) : 0ull;
                     if (key > floor0) {
                         const int at = atomicAdd(&sh.n, 1);
-                        if (at < THREADS) sh.cand[at] = key;
+                        if (at < sh.kCand) sh.cand[at] = key;
                     }
                 }
             }
         });
         __syncthreads();
-        if (sh.n > THREADS) {                        // (the same for every thread)
+        if (sh.n > sh.kCand) {                       // (the same for every thread)
             __syncthreads();
             if (tid == 0) sh.n = 0;
             __syncthreads();
@@ -562,8 +563,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             __syncthreads();
         }
         const int n = sh.n;
-        if (tid < n) {
-            const unsigned long long mine = sh.cand[tid];
+        for (int at = tid; at < n; at += THREADS) {
+            const unsigned long long mine = sh.cand[at];
             int above = 0;
 #pragma unroll 8
             for (int i = 0; i < n; ++i) above += sh.cand[i] > mine ? 1 : 0;
