@@ -9,8 +9,9 @@
 // 32 lanes), so two logits share each packed operation:
 //   clamp  a 16-bit maximum with a large negative number: -inf (and the type's lowest value) then
 //          add 0 and not 0 * inf; NaN passes and makes the row NaN
-//   t      one packed fp32 FMA, x log2(e) - R with R = m log2(e) rounded; what the rounding of R leaves
-//          out of z and s is put right once per thread at the end
+//   t      one packed fp32 FMA, x log2(e) - R with R = m log2(e) rounded. Every term is then 2^r too large,
+//          r = m log2(e) - R: z and s are moved from one m to the next with the change of r, and the last r is
+//          taken out once per thread at the end
 //   2^t    one exponential each; then one packed addition and one packed FMA
 // Where m is so large or so low that R or the clamp would not do (a row of the type's lowest value
 // only), a thread subtracts and multiplies instead.
@@ -196,10 +197,10 @@ __device__ __forceinline__ uint64_t clamped_pair(const uint32_t (&u)[4], int i) 
 // Softmax statistics of a set of logits; m = -inf: nothing but -inf (and NaN) so far.
 struct LpStat {
     float m, z, s;
-    // to a reference n >= m
-    __device__ void move(float n) {
+    // to a reference n >= m; dr: how much larger n's r is than m's
+    __device__ void move(float n, float dr = 0.f) {
         if (n > m) {
-            const float d = fmaxf(m - n, -kFar) * kLog2e;      // (m = -inf: z and s are 0, or NaN)
+            const float d = fmaf(fmaxf(m - n, -kFar), kLog2e, dr);     // (m = -inf: z and s are 0, or NaN)
             const float f = ex2(d);
             s = f * fmaf(d, z, s);
             z = f * z;
@@ -219,14 +220,18 @@ struct LpAcc {
         return (m < low && m != kNegInf) || m > 1e38f;
     }
     __device__ float ref() const { return m == kNegInf ? 0.f : m * kLog2e; }
+    // r, by which the exponents of the terms so far are too large
+    __device__ float rest() const { return m == kNegInf || slow() ? 0.f : fmaf(m, kLog2e, -ref()); }
     __device__ void move(float n) {
         float z0, z1, s0, s1;
         unpair(z, z0, z1);
         unpair(s, s0, s1);
         LpStat a{m, z0, s0}, b{m, z1, s1};
-        a.move(n);
-        b.move(n);
+        const float r = rest();
         m = n;
+        const float dr = rest() - r;
+        a.move(n, dr);
+        b.move(n, dr);
         z = pair(a.z, b.z);
         s = pair(a.s, b.s);
     }
@@ -267,13 +272,12 @@ struct LpAcc {
             s = fma2(t, e, s);
         }
     }
-    // The whole, with m itself as the reference: t was off by r, the part of m log2(e) that R leaves out.
+    // The whole, with m itself as the reference: t was r too large.
     __device__ LpStat done() const {
         float z0, z1, s0, s1;
         unpair(z, z0, z1);
         unpair(s, s0, s1);
-        const float r = m == kNegInf || slow() ? 0.f : fmaf(m, kLog2e, -ref());
-        const float f = 1.f - r * kLn2, zz = (z0 + z1) * f;
+        const float r = rest(), f = ex2(-r), zz = (z0 + z1) * f;
         return LpStat{m, zz, fmaf(-r, zz, (s0 + s1) * f)};
     }
 };
