@@ -13,8 +13,8 @@
 //          r = m log2(e) - R: z and s are moved from one m to the next with the change of r, and the last r is
 //          taken out once per thread at the end
 //   2^t    one exponential each; then one packed addition and one packed FMA
-// Where m is so large or so low that R or the clamp would not do (a row of the type's lowest value
-// only), a thread subtracts and multiplies instead.
+// Where |m| is so large that r would be (beyond 2^20; half an ulp of R is below 2^-4 up to there), or m is near
+// the clamp (fp16), a thread subtracts and multiplies instead.
 //
 // The k most likely tokens need no second pass over the row. A thread remembers the largest vector
 // it saw (its maximum and where, the first among equals). 64 groups of threads make 64 such bests (a
@@ -48,6 +48,7 @@ constexpr int kLpUnroll = 4;                  // vectors of a thread in flight
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFar = 150.f;                 // exp(-150) is below the smallest fp32
 constexpr float kNegInf = -INFINITY;
+constexpr float kFine = 1048576.f;            // 2^20: up to here m log2(e) in fp32 is within 2^-4
 
 static_assert(kLpMaxCluster * kLpMaxTop <= kLpThreads / 2, "two threads to a key");
 
@@ -214,10 +215,10 @@ template <int DT>
 struct LpAcc {
     float m = kNegInf;
     uint64_t z = 0, s = 0;
-    // whether R = m log2(e) is no use as a reference, or m is not well above the clamp
+    // whether R = m log2(e) is too coarse for a reference, or (fp16) m is not well above the clamp
     __device__ bool slow() const {
-        constexpr float low = DT == kLpFp16 ? -6e4f : -1e29f;
-        return (m < low && m != kNegInf) || m > 1e38f;
+        if constexpr (DT == kLpFp16) return (m < -6e4f && m != kNegInf) || m == INFINITY;
+        else return fabsf(m) > kFine && m != kNegInf;
     }
     __device__ float ref() const { return m == kNegInf ? 0.f : m * kLog2e; }
     // r, by which the exponents of the terms so far are too large
