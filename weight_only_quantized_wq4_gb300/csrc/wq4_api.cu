@@ -42,7 +42,6 @@ namespace {
 // bounds violation of the debug build (site and three values)
 __device__ unsigned int g_status[1 + check::kRecordWords];
 
-constexpr int kMaxDevices = 64;
 constexpr long long kDefaultTimeoutCycles = 4000000000LL;   // ~2 s at 2 GHz
 constexpr long long kFixupSteps = 10;   // cost of a K-split tile's fixup, in (tile, group) steps
 
@@ -670,6 +669,7 @@ int runtime(Runtime* out) {
     DeviceInfo* dev = nullptr;
     const int rc = device_info(&dev);
     if (rc) return rc;
+    out->device = static_cast<int>(dev - g_dev);
     out->sm_count = dev->sm_count;
     out->status = dev->status;
     out->timeout_cycles = timeout_cycles();

@@ -774,14 +774,18 @@ template <int NT, bool TOK_LANES, bool PAIR>
 int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) {
     using C = BmCfg<NT, TOK_LANES, PAIR>;
     auto kern = block_mm_kernel<NT, TOK_LANES, PAIR>;
-    static int regs = -1;                            // (one value per kernel, whoever writes it)
-    if (regs < 0) {
+    // A kernel's shared memory is granted by device, as its occupancy below is a device's own.
+    static PerDevice ready;
+    const int regs = ready.get(rt.device, [&]() -> int {
         cudaFuncAttributes fa;
         if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBmMaxSmem) != cudaSuccess)
-            return WQ4_ERR_CUDA;
-        regs = fa.numRegs;
-    }
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBmMaxSmem) != cudaSuccess) {
+            cudaGetLastError();
+            return -1;
+        }
+        return fa.numRegs;
+    });
+    if (regs <= 0) return WQ4_ERR_CUDA;
     // the fold warps' share counts on the registers of the launch; with fewer their request would wait
     if (C::kRegSplit && regs != C::kLaunchRegs) return WQ4_ERR_CUDA;
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -805,8 +809,8 @@ int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) 
     for (int s = 2; !PAIR && s <= 8 && s <= a.kb && s * tiles <= rt.sm_count; ++s) {
         if (TOK_LANES && (s == 6 || s == 7)) continue;      // (their parts leave the ring fewer than four stages)
         if ((a.kb + s - 1) / s >= (a.kb + a.split - 1) / a.split) continue;
-        static int resident[9];                      // (one value per kernel and s, whoever writes it)
-        if (!resident[s]) {
+        static PerDevice resident[9];                // of clusters of s, and one more
+        const int room = resident[s].get(rt.device, [&]() -> int {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(s);
             cfg.blockDim = dim3(C::kThreads);
@@ -820,11 +824,12 @@ int go_block_mm(const Runtime& rt, const BmCall& c, BmArgs& a, wq4_stream_t st) 
             int n = 0;
             if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
                 cudaGetLastError();
-                return WQ4_ERR_CUDA;
+                return -1;
             }
-            resident[s] = n > 0 ? n : -1;
-        }
-        if (tiles <= resident[s]) a.split = s;
+            return n + 1;
+        });
+        if (room <= 0) return WQ4_ERR_CUDA;
+        if (tiles < room) a.split = s;
     }
     // More narrow tiles than SMs (and no whole number of waves of them): rings of half the size, two CTAs per SM
     // (4 x 28672 x 4096: 21.1 us; one CTA with the whole ring 23.6).

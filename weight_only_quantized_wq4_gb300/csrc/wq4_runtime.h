@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "wq4.h"
@@ -15,7 +16,10 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+constexpr int kMaxDevices = 64;
+
 struct Runtime {
+    int device;                 // the current device's ordinal, below kMaxDevices
     int sm_count;
     unsigned int* status;       // device status word
     long long timeout_cycles;   // bound of every pipeline wait
@@ -27,6 +31,21 @@ struct Runtime {
 
 // The current device's runtime under the current options (WQ4_ERR_CUDA without a device).
 int runtime(Runtime* out);
+
+// A positive number that belongs to a device (a kernel's attributes once they are set, its occupancy), found out by the first
+// call there. Threads may find it out twice; they find the same. What is not positive, a failure, is not kept.
+class PerDevice {
+public:
+    template <typename F>
+    int get(int device, F find) {
+        int n = v_[device].load(std::memory_order_acquire);
+        if (n == 0 && (n = find()) > 0) v_[device].store(n, std::memory_order_release);
+        return n;
+    }
+
+private:
+    std::atomic<int> v_[kMaxDevices] = {};
+};
 
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
