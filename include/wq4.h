@@ -350,10 +350,14 @@ int wq4_last_violation(int* record);
  *                           call's set-up overlaps the end of the previous kernel on the stream;
  *                           it touches global memory only after that kernel has completed);
  *                           -1 = plain stream order
- *   WQ4_OPT_TEST_STALL      1 = (tests of the failure path) every kernel makes one wait per CTA
- *                           on a barrier that nothing arrives on; it runs out after the
- *                           WQ4_OPT_TIMEOUT_CYCLES bound, the call stops early and
- *                           wq4_get_last_error reports WQ4_ERR_TIMEOUT. 0 = off
+ *   WQ4_OPT_TEST_STALL      1 = (tests of the failure path) the GEMM, decode and block-scaled
+ *                           product kernels make one wait per CTA on a barrier that nothing
+ *                           arrives on, and wq4_token_logprobs one per row that a cluster of
+ *                           CTAs shares; it runs out after the WQ4_OPT_TIMEOUT_CYCLES bound,
+ *                           the call stops early and wq4_get_last_error reports
+ *                           WQ4_ERR_TIMEOUT. Kernels without a bounded wait (norm, gated
+ *                           activation, log probabilities of a row per CTA, prepack) are as
+ *                           ever. 0 = off
  *   WQ4_OPT_CONST_WEIGHTS   1 = the caller promises that no kernel still pending on the stream
  *                           writes a blob that a later call reads: the decode kernel then checks
  *                           the blob header and copies its first weights, and the tensor-core GEMM

@@ -63,6 +63,7 @@ struct LpArgs {
     int V, k, cluster;
     unsigned int* status;
     long long timeout_cycles;
+    int test_stall;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -308,7 +309,7 @@ struct LpShared {
     // what rank 0 is sent by the cluster's CTAs: their statistics and their lists
     float4 part_stat[kLpMaxCluster];
     unsigned long long part_top[kLpMaxCluster * kLpMaxTop];
-    unsigned long long part_bar;
+    unsigned long long part_bar, stall_bar;
     int abort;
     unsigned long long top[kLpMaxTop];               // this CTA's best, in order, 0 where there are fewer
 };
@@ -325,6 +326,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     if (C > 1) {
         if (tid == 0) {
             mbar_init(smem_u32(&sh.part_bar), 1);
+            mbar_init(smem_u32(&sh.stall_bar), 1);
             if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.part_bar), C * (16 + 8 * a.k));
             sh.abort = 0;
             fence_mbar_init();
@@ -589,10 +591,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         }
         if (rank != 0) return;
         const WaitCtl ctl{&sh.abort, a.status, a.timeout_cycles};
-        if (tid == 0) mbar_wait(smem_u32(&sh.part_bar), 0, ctl);     // (one thread's answer holds for all)
+        // one thread's answer holds for all
+        if (tid == 0 && (!a.test_stall || mbar_wait(smem_u32(&sh.stall_bar), 0, ctl))) mbar_wait(smem_u32(&sh.part_bar), 0, ctl);
         __syncthreads();
-        if (sh.abort) {
-            cluster_sync();                          // (not before the others, which may still send, are gone)
+        if (sh.abort) {                              // (not before what the others sent is here, and they are gone)
+            if (tid == 0) mbar_wait_plain(smem_u32(&sh.part_bar), 0, drain_limit(a.timeout_cycles));
+            __syncwarp();
+            cluster_sync();
             return;
         }
         if (warp == 0) {
@@ -674,7 +679,8 @@ extern "C" int wq4_token_logprobs(const void* logits, long long ld, const long l
     const int vec = dtype == WQ4_FP32 ? 4 : 8;
     while (C < kLpMaxCluster && 2LL * C * T <= 2LL * rt.sm_count && V / (2 * C) >= kLpThreads * vec) C *= 2;
     if (static_cast<long long>(T) * C > 0x7fffffffLL) return WQ4_ERR_UNSUPPORTED;
-    const LpArgs a{logits, tokens, logprobs, entropy, top_logprobs, top_ids, ld, V, top_k, C, rt.status, rt.timeout_cycles};
+    const LpArgs a{logits, tokens, logprobs, entropy, top_logprobs, top_ids, ld, V, top_k, C, rt.status, rt.timeout_cycles,
+                   rt.test_stall};
     const dim3 grid(static_cast<unsigned>(T) * C);
     // Many rows: fewer threads per row, so that more rows share what the steps after the pass cost each of them
     // (2048 x 8192 bf16, top 8: 14.7 us with 128 threads, 21.0 with 256, 38.3 with 512), unless the waves or the
