@@ -730,9 +730,10 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
         tc_fence_after();
         bm_tmem_dealloc<PAIR>(tmem, C::kTmemCols);
     }
-    // A CTA whose parts all came is sent nothing more. One that gave up stays until the others, which may still
-    // send to it, have gone or given up too.
+    // A CTA whose parts all came is sent nothing more. One that gave up stays until what the others send (they do
+    // so in any case) is here, and until they, which may still send, have gone or given up too.
     if (!PAIR && a.split > 1 && *abort_flag) {
+        if (threadIdx.x == 0) mbar_wait_plain(red_bar, 0, drain_limit(a.timeout_cycles));
         __syncwarp();
         cluster_sync();
     }
