@@ -433,17 +433,22 @@ __global__ void xsum_kernel(const __grid_constant__ XsumBatch b) {
         if (m < J.M && z < J.K / b.span) {
             const uint4* xp =
                 reinterpret_cast<const uint4*>(J.X + static_cast<size_t>(m) * J.K + static_cast<size_t>(b.span) * z);
-            for (int c = 0; c < b.span / 8; ++c) {
-                const uint4 q = __ldg(xp + c);
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            for (int c0 = 0; c0 < b.span / 8; c0 += 8) {     // (a span is 8 or 16 vectors)
+                uint4 q[8];                                  // on their way together
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (BF16) {
-                        v += __uint_as_float(w[e] << 16);
-                        v += __uint_as_float(w[e] & 0xFFFF0000u);
-                    } else {
-                        v += __half2float(__ushort_as_half(static_cast<unsigned short>(w[e] & 0xFFFFu)));
-                        v += __half2float(__ushort_as_half(static_cast<unsigned short>(w[e] >> 16)));
+                for (int c = 0; c < 8; ++c) q[c] = xp[c0 + c];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (BF16) {
+                            v += __uint_as_float(w[e] << 16);
+                            v += __uint_as_float(w[e] & 0xFFFF0000u);
+                        } else {
+                            v += __half2float(__ushort_as_half(static_cast<unsigned short>(w[e] & 0xFFFFu)));
+                            v += __half2float(__ushort_as_half(static_cast<unsigned short>(w[e] >> 16)));
+                        }
                     }
                 }
             }
@@ -959,9 +964,8 @@ namespace wq4 {
 // or a blob whose header does not match the call, marks the problem invalid (the GEMM skips its
 // tiles) and sets the status word's bad-argument bit.
 template <int C>
-__global__ void ptr_setup_kernel(const __grid_constant__ PtrSetup<C> su, const void* const* __restrict__ X,
-                                 const void* const* __restrict__ W, void* const* __restrict__ Y,
-                                 ProblemDesc* __restrict__ tab, CUtensorMap* __restrict__ maps,
+__global__ void ptr_setup_kernel(const __grid_constant__ PtrSetup<C> su, const void* const* X,
+                                 const void* const* W, void* const* Y, ProblemDesc* tab, CUtensorMap* maps,
                                  unsigned int* status) {
     // Launched with programmatic dependent launch: the GEMM behind it may start its set-up at once
     // (it reads the tables only after this grid has completed); the pointer arrays and the tables

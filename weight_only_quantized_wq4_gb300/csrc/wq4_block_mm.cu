@@ -528,14 +528,14 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
                 // in, the next is read.
                 constexpr int kCols = 16, kPieces = C::kNC / kCols;
                 const int nb = s.kb1 - s.kb0;
-                float w32 = lane < nb ? __ldg(sw + s.kb0 + lane) : 0.f;
+                float w32 = lane < nb ? sw[s.kb0 + lane] : 0.f;
 #pragma unroll
                 for (int j = 0; j < C::kNC; ++j) acc[j] = 0.f;
                 uint32_t v[2][kCols];
 #pragma unroll 1
                 for (int b = 0; b < nb; ++b) {
                     if (b % C::kScBlocks == 0) {
-                        if (b % 32 == 0 && b) w32 = b + lane < nb ? __ldg(sw + s.kb0 + b + lane) : 0.f;
+                        if (b % 32 == 0 && b) w32 = b + lane < nb ? sw[s.kb0 + b + lane] : 0.f;
                         if (!mbar_wait(scfull_bar(sc), sc_phase, ctl)) { ok = false; break; }
                     }
                     const float f = lds_f32(s_sc + sc * C::kScBytes + (b % C::kScBlocks) * (kBmLanes * 4) + 4 * r) *
@@ -581,10 +581,10 @@ __global__ void __launch_bounds__(BmCfg<NT, TOK_LANES, PAIR>::kThreads, !TOK_LAN
 #pragma unroll
                     for (int j = 0; j < kAhead; ++j, px += a.ldsx) {
                         if (j >= n) break;
-                        nsw[j] = __ldg(pw + j);
-                        if (loads) nsx[j * kPer] = __ldg(px);
+                        nsw[j] = pw[j];
+                        if (loads) nsx[j * kPer] = *px;
                         if constexpr (kPer > 1)
-                            if (loads2) nsx[j * kPer + 1] = __ldg(px + 32);
+                            if (loads2) nsx[j * kPer + 1] = px[32];
                     }
                     pw += kAhead;
                 };

@@ -140,7 +140,7 @@ struct LpRow {
         nv = (V + head + LpVec<DT>::kN - 1) / LpVec<DT>::kN;
     }
     __device__ bool whole(int v) const { return v * LpVec<DT>::kN >= head && (v + 1) * LpVec<DT>::kN <= V + head; }
-    __device__ uint4 load(int v) const { return __ldg(reinterpret_cast<const uint4*>(base) + v); }
+    __device__ uint4 load(int v) const { return reinterpret_cast<const uint4*>(base)[v]; }
     __device__ uint4 load_edge(int v) const {
         if (whole(v)) return load(v);
         uint4 r = LpVec<DT>::none();

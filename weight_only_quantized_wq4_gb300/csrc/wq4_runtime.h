@@ -51,7 +51,8 @@ inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<ui
 
 // Launches `kern` on `st`, in clusters of `cluster` CTAs, with programmatic dependent launch when
 // the options ask for it: every kernel launched so waits (griddepcontrol.wait) before it touches
-// global memory.
+// global memory, and reads it by ordinary loads and copies: a read-only load (ld.global.nc) is for data that
+// nothing writes while the kernel is there, and it is there while the kernels ahead may still write.
 template <typename... P, typename... A>
 int launch(const Runtime& rt, void (*kern)(P...), dim3 grid, int threads, int smem, int cluster, wq4_stream_t st,
            A&&... args) {
