@@ -378,7 +378,8 @@ def _bind():
     if _binding is None:
         path = os.path.join(PKG, "_wq4_binding.so")
         if not os.path.exists(path):
-            raise RuntimeError("_wq4_binding.so is not built: run `python -m weight_only_quantized_wq4_gb300.builder`")
+            raise RuntimeError("_wq4_binding.so is not built: run `python -m weight_only_quantized_wq4_gb300.builder` "
+                               "(needs torch with CUDA and Python's headers)")
         import importlib.util
         spec = importlib.util.spec_from_file_location(__name__ + "._wq4_binding", path)
         module = importlib.util.module_from_spec(spec)

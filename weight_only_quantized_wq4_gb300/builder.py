@@ -1,5 +1,5 @@
 """Builds libwq4.so in-tree with nvcc for sm_103a (one object per .cu, compiled in parallel) and, where
-torch is installed, _wq4_binding.so, which marshals some of its Python calls.
+torch with CUDA and Python's headers are installed, _wq4_binding.so, which marshals some of its Python calls.
 
 With --debug it builds libwq4_debug.so instead: the same sources with -DWQ4_DEBUG=1, whose kernels
 check every copy coordinate, weight record range, scheduled tile and output column before use
@@ -57,15 +57,19 @@ def _stamp(flags) -> str:
 
 
 def _binding_command():
-    """The compiler call that makes _wq4_binding.so, or None without torch (found, not imported)."""
+    """The compiler call that makes _wq4_binding.so, or None without what it is made against: torch (found,
+    not imported) with CUDA, and Python's headers."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
         return None
     root = spec.submodule_search_locations[0]
     lib = os.path.join(root, "lib")
+    python = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(lib, "libc10_cuda.so")) or not os.path.exists(os.path.join(python, "Python.h")):
+        return None
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-I", INCLUDE,
-            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+            "-I", python, "-isystem", os.path.join(root, "include"),
             "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
             os.path.join(CSRC, "wq4_binding.cpp"), "-o", BINDING + ".tmp", "-L" + lib, "-Wl,-rpath," + lib,
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
