@@ -99,7 +99,9 @@ const at::Tensor* leading(PyObject* o, const char* name, bool fp32, int* dtype, 
     return &t;
 }
 
-bool fits(const char* name, int64_t n) { return n <= 0x7fffffff || refuse(name, "smaller than 2^31 in each dimension"); }
+bool fits(const char* name, int64_t n) {
+    return (n >= -0x7fffffff && n <= 0x7fffffff) || refuse(name, "smaller than 2^31 in each dimension");
+}
 
 wq4_stream_t stream(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 
@@ -183,7 +185,7 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (PyErr_Occurred()) return nullptr;
     Rows rx, ri, rl;
     void *tok = nullptr, *lp = nullptr, *ent = nullptr;
-    if (!fits("logits", T) || !fits("logits", V) || !rows_of(*x, "logits", &rx) ||
+    if (!fits("logits", T) || !fits("logits", V) || !fits("top_k", k) || !rows_of(*x, "logits", &rx) ||
         !vector(a[1], "tokens", T, at::kLong, dev, &tok) || !vector(a[3], "logprobs", T, at::kFloat, dev, &lp) ||
         !vector(a[4], "entropy", T, at::kFloat, dev, &ent) ||
         (a[5] != Py_None && !rows(a[5], "top_ids", T, k, at::kInt, dev, &ri)) ||
