@@ -236,8 +236,8 @@ int wq4_grouped_mm_dev_ptrs(int P, const int* M, const int* N, const int* K,
  * columns has a scale of its own. Both pointers are 16-byte aligned. Padding (codes past D, scales
  * past T) is neither read nor written.
  *
- * A block's scale is max(max |y| / 448, 2^-126) and its codes are y / scale rounded to nearest even
- * (448 is the largest e4m3 value). A NaN becomes a NaN code and does not touch the scale; a block
+ * A block's scale is max(max |y| / 448, 2^-126) and its codes are y / scale, the quotients in fp32 rounded
+ * to nearest, the codes to nearest even (448 is the largest e4m3 value). A NaN becomes a NaN code and does not touch the scale; a block
  * with an infinity gets an infinite scale, and all its values read back as NaN.
  * ------------------------------------------------------------------------------------------ */
 

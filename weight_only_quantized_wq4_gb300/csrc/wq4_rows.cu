@@ -2,7 +2,7 @@
 // addition, and the gated activation. Both end alike. A row's values y, in fp32, are cut into
 // blocks of 128; block b of token t gets the scale
 //     s[b][t] = max(max |y| / 448, 2^-126)
-// and the codes q = e4m3(y / s), rounded to nearest even; 448 is e4m3's largest value, and the
+// and the codes q = e4m3(y / s), every quotient rounded to fp32 and the code to nearest even; 448 is e4m3's largest value, and the
 // lower bound keeps the quotient defined for a block of zeros. A NaN stays one in its own code and
 // does not touch its block's scale; a block with an infinity has an infinite scale, so that every
 // value read back from it (q s) is NaN.
@@ -10,8 +10,8 @@
 // Both are bound by memory: each element is read and written once, in 16-byte vectors of 8 elements
 // (across boundaries where rows do not start on one), and everything in between stays in registers. 16
 // neighbouring lanes hold one block of 128, so a block's maximum takes four shuffles and no shared
-// memory. Passes back to back: norm with residual, 4096 x 4096 bf16, 20.3 us (5.8 TB/s); gated,
-// 4096 x 14336 bf16, 45.0 us (6.6 TB/s); 1 x 4096 and 16 x 14336 take 1.6 and 1.4 us, a launch and one
+// memory. Passes back to back: norm with residual, 4096 x 4096 bf16, 20.6 us (5.7 TB/s); gated,
+// 4096 x 14336 bf16, 44.8 us (6.6 TB/s); 1 x 4096 and 16 x 14336 take 1.6 and 1.4 us, a launch and one
 // trip to memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -82,11 +82,26 @@ __device__ __forceinline__ void squares8(const float (&a)[kVec], uint64_t& s) {
         asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(s) : "l"(x));
     }
 }
-// 1 / x to an ulp or so (0 for infinity)
+// 1 / x to an ulp or so (0 for infinity and for x > 2^126)
 __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// -a / b of each, rounded to nearest, from r, the reciprocal of b rounded to nearest: q = -a r is within an ulp or so of it, and
+// q - r (q b + a), two fused operations more, then is it (P. Markstein, Computation of elementary functions on the IBM
+// RISC System/6000 processor, 1990), as long as nothing underflows. (So and not with a / b, a zero keeps its sign.)
+__device__ __forceinline__ void minus_div8(float (&a)[kVec], float b, float r) {
+    const uint64_t bb = pair(b, b), minus_r = pair(-r, -r);
+#pragma unroll
+    for (int j = 0; j < kVec; j += 2) {
+        const uint64_t x = pair(a[j], a[j + 1]);
+        uint64_t q, rest;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(minus_r));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rest) : "l"(q), "l"(bb), "l"(x));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(q) : "l"(rest), "l"(minus_r));
+        unpair(q, a[j], a[j + 1]);
+    }
 }
 
 template <bool BF16>
@@ -204,8 +219,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return d;
 }
 
-// The codes of eight values of a row (the thread's 16 lanes hold the block of 128 they are in) and,
-// from the first of those lanes, the block's scale. Every lane of the warp calls it.
+// The codes of -y, eight values of a row (the thread's 16 lanes hold the block of 128 they are in), and, from the
+// first of those lanes, the block's scale. Every lane of the warp calls it.
 template <bool VEC>
 __device__ __forceinline__ void quantise8(float (&y)[kVec], int col, int D, uint8_t* q_row, float* scale) {
     float m = 0.f;
@@ -213,11 +228,18 @@ __device__ __forceinline__ void quantise8(float (&y)[kVec], int col, int D, uint
     for (int j = 0; j < kVec; ++j) m = fmaxf(m, fabsf(y[j]));      // (fmaxf passes NaN over)
 #pragma unroll
     for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    // A product with 1 / 448 and an approximate reciprocal instead of divisions: the scale and the quotients
-    // can be off by an fp32 ulp or two, which moves a code only where it lies that near to a rounding
-    // boundary. (Exact divisions made a quarter of the kernels' instructions.)
-    const float s = fmaxf(m * (1.f / kE4m3Max), FLT_MIN);
-    mul8(y, rcp(s));
+    // m / 448 and the quotients rounded to nearest, by reciprocals and remainders: divisions one by one took
+    // longer (4096 x 4096 norm 21.4 us), products with the reciprocals alone less (20.3), but their codes can be a
+    // step off at a rounding boundary.
+    float s = m;
+    if (m <= FLT_MAX) {
+        const float s0 = m * (1.f / kE4m3Max);
+        s = fmaxf(fmaf(fmaf(-kE4m3Max, s0, m), 1.f / kE4m3Max, s0), FLT_MIN);
+        const float r = rcp(s);
+        minus_div8(y, s, fmaf(r, fmaf(-s, r, 1.f), r));
+    } else {
+        mul8(y, -0.f);                               // (y / s is 0, or NaN; branches: 4096 x 14336 46.8 us with selects)
+    }
     uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = e4m3x2(y[2 * j], y[2 * j + 1]);
@@ -321,10 +343,15 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormRows : VPT > 1 ? 512 : 1024, 
         const int col = col_of(i);
         float w[kVec];
         if constexpr (VPT > 1) load8<BF16, VEC>(a.w, col, D, w);
-        mul8(h[i], rstd);
+        mul8(h[i], -rstd);                           // (-y from here on)
         if constexpr (VPT == 1) mul8(h[i], w0);
         else mul8(h[i], w);
-        if (a.y) store8<BF16, VEC>(a.y + t * a.ldy, col, D, h[i]);
+        if (a.y) {
+            float y[kVec];
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) y[j] = -h[i][j];
+            store8<BF16, VEC>(a.y + t * a.ldy, col, D, y);
+        }
         if (a.q) quantise8<VEC>(h[i], col, D, a.q + t * a.ldq, a.scales + (col / kRowBlock) * a.lds + t);
     }
 }
@@ -399,11 +426,11 @@ __global__ void __launch_bounds__(kGatedVecs / VPT) gated_kernel(const GatedArgs
         float g[kVec], u[kVec];
         end8<BF16, VEC>(rg[i], row, col[i], D, g);
         end8<BF16, VEC>(ru[i], row + D, col[i], D, u);
-        // silu(g) = g / (1 + exp(-g)); where exp(-g) is infinite the quotient is the limit, 0
+        // silu(g) = g / (1 + exp(-g)); where exp(-g) is beyond 2^126 (g < -87.3) the quotient is taken for its limit, 0
         float e[kVec];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) e[j] = rcp(1.f + __expf(-g[j]));
-        mul8(g, e);                                  // (before u: g u may overflow where silu(g) u does not)
+        for (int j = 0; j < kVec; ++j) e[j] = rcp(-1.f - __expf(-g[j]));
+        mul8(g, e);                                  // (-silu(g); before u: g u may overflow where silu(g) u does not)
         mul8(g, u);
         quantise8<VEC>(g, col[i], D, a.q + t[i] * a.ldq, a.scales + (col[i] / kRowBlock) * a.lds + t[i]);
     }
