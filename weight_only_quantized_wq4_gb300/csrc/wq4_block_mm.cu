@@ -24,13 +24,14 @@
 // With fewer tiles than SMs, a cluster of CTAs shares each tile, cut along K; the parts are sent
 // through distributed shared memory to the CTA that joins them, which adds them in rank order.
 //
-// What bounds it, and measured device times (passes back to back, weights not in L2):
+// What bounds it, and measured device times (passes back to back, replayed from a graph, weights not in L2):
 //   few tokens    the weights' bytes, and some 4 us of launch, first copies and last stores: 16 x 14336 x 4096 bf16
 //                 13.4 us (4.4 TB/s; a kernel that only copies as many bytes takes 12.1), 1 x 4096 x 4096 6.4 us
 //   middle sizes  the same 4 us, then 480 to 600 cycles a block: 333 x 4100 x 2064 fp16 10.3 us
 //   large sizes   the fold: 650 to 810 cycles per block of 256 columns for tcgen05.ld and 128 FMAs a thread,
-//                 against the MMAs' 515: 4096 x 4096 x 14336 bf16 183 us (2.6 PFLOP/s; the MMAs alone are 72% of
-//                 it). A third buffer of tensor memory would hide its latency; two of 256 columns fill it.
+//                 against the MMAs' 515: 4096 x 4096 x 14336 bf16 184 us (2.6 PFLOP/s; the MMAs alone are 72% of
+//                 it), 199 in calls from Python, where the board's power limit tells. A third buffer of tensor memory would
+//                 hide the fold's latency; two of 256 columns fill it.
 //
 // Every wait is bounded, as in wq4_gemm.cuh: one that runs out is recorded in the status word and the
 // CTA drains its copies and MMAs, frees its tensor memory and returns.

@@ -20,13 +20,14 @@
 // it saw (its maximum and where, the first among equals). 64 groups of threads make 64 such bests (a
 // group's threads are 64 apart, so that logits next to one another fall to different groups); the
 // k-th largest of them, tau, is a bound that at least k elements reach, so only threads whose own
-// best reaches it can hold an answer, about k of them. Their vectors (V / 512 elements each) are
-// read again by whole warps; the elements that reach tau, a few dozen, are ranked by counting. An
+// best reaches it can hold an answer, about k of them. Their vectors (a 512th, 256th or 128th of the row each,
+// by the CTA's threads) are read again by whole warps; the elements that reach tau, a few dozen, are ranked by counting. An
 // element's order is one 64-bit key: the float as an unsigned integer of the same order, then the
 // complement of its index, so that equal logits rank by the lower index and no two keys are equal.
 //
-// Bound by memory and by instructions for many rows (each logit is read once): 2048 x 131072 bf16 109 us
-// (4.9 TB/s), of which the steps after the pass, some 850 instructions a warp, are a tenth. For few
+// Bound by the latency of loads for many rows (each logit is read once; an SM holds 1024 threads, half of what it
+// could, issues in 54 % of its cycles and waits for loads most): 2048 x 131072 bf16 109 us (4.9 TB/s), of which the
+// steps after the pass, some 850 instructions a warp, are a tenth: a CTA loads nothing meanwhile. For few
 // rows a cluster of CTAs shares a row; each sends its statistics and list to the first through
 // distributed shared memory. That is a chain of latencies: 1 x 131072 fp32 6.5 us.
 #include <cuda_bf16.h>
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         st.s += __shfl_xor_sync(0xffffffffu, st.s, d);
     }
     if (lane == 0) sh.stat[warp] = make_float2(st.z, st.s);
-    if (a.k > 0) {                                   // how many bests are above each: an eighth of them per thread
+    if (a.k > 0) {                                   // how many bests are above each: a kParts-th of them per thread
         const unsigned long long mine = sh.best[tid % kLpGroups];
         int above = 0;
 #pragma unroll

@@ -360,15 +360,15 @@ template <bool BF16, bool VEC>
 int go_norm(const Runtime& rt, const NormArgs& a, wq4_stream_t st) {
     const int nv = (a.D + kVec - 1) / kVec;
     const bool many = a.T > 4 * rt.sm_count;
-    // Many short rows: a warp each (8192 x 256 bf16: 4.1 us against 8.6 with a CTA each).
+    // Many short rows: a warp each (8192 x 256 bf16: 4.2 us against 8.6 with a CTA each).
     if (many && nv <= 64) {
         const dim3 grid((static_cast<unsigned>(a.T) + kNormRows - 1) / kNormRows);
         if (nv <= 32) return launch(rt, norm_kernel<BF16, VEC, 1, true>, grid, 32 * kNormRows, 0, 1, st, a);
         return launch(rt, norm_kernel<BF16, VEC, 2, true>, grid, 32 * kNormRows, 0, 1, st, a);
     }
-    // Vectors per thread: one, two or four. Measured with the residual, bf16: 4096 x 4096, 23.4 / 20.5 / 21.6 us;
-    // 2000 x 8192, 25.5 / 20.5 / 21.5; 1 x 4096, 1.6 / 1.8 / 2.4; 4096 x 1024, 6.9 / 8.1 / 9.2; 517 x 2064
-    // without it, 2.1 / 2.7 / 3.0. (Two: at most 40 registers, three CTAs of 512.)
+    // Vectors per thread: one, two or four. Measured with the residual, bf16: 4096 x 4096, 24.2 / 21.0 / 22.1 us;
+    // 2000 x 8192, 26.7 / 21.1 / 22.1; 1 x 4096, 1.7 / 2.0 / 2.7; 4096 x 1024, 7.2 / 8.7 / 9.5; 517 x 2064
+    // without it, 2.2 / 3.1 / 3.4. (Two: at most 40 registers, three CTAs of 512.)
     const int vpt = nv > 2048 ? 8 : nv > 1024 ? 4 : many && nv > 256 ? 2 : 1;
     const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
     switch (vpt) {
@@ -436,12 +436,12 @@ __global__ void __launch_bounds__(kGatedVecs / VPT) gated_kernel(const GatedArgs
     }
 }
 
-// Rows shorter than a CTA's columns share CTAs (16384 x 128 bf16: 3.2 us, a CTA per row 18.3; 4096 x 1408:
-// 6.6 against 7.8), and so do rows off 16-byte boundaries while a row's last CTA can be a good part of it
-// (2000 x 4101: 11.0 against 14.9; 4096 x 14335: 62.6 against 60.4). Otherwise, with more CTAs than the
+// Rows shorter than a CTA's columns share CTAs (16384 x 128 bf16: 3.3 us, a CTA per row 21.9; 4096 x 1408:
+// 7.0 against 8.1), and so do rows off 16-byte boundaries while a row's last CTA can be a good part of it
+// (2000 x 4101: 11.5 against 13.7; 4096 x 14335: 66.7 against 63.7). Otherwise, with more CTAs than the
 // SMs hold at once, 64 threads with four vectors each keep more loads under way (4096 x 14336 bf16:
-// 45.0 us; 128 with two 47.2, 256 with one 52.3); with fewer, one vector each is sooner done
-// (16 x 14336: 1.4 us against 2.0).
+// 44.8 us; 128 with two 50.3, 256 with one 52.4); with fewer, one vector each is sooner done
+// (16 x 14336: 1.4 us against 1.6 with two).
 template <bool BF16, bool VEC>
 int go_gated(const Runtime& rt, const GatedArgs& a, int T, wq4_stream_t st) {
     const long long ctas = static_cast<long long>(T) * a.chunks, groups = static_cast<long long>(T) * a.blocks;
