@@ -297,12 +297,115 @@ int wq4_token_logprobs(const void* logits, long long ld, const long long* tokens
                        float* logprobs, float* entropy, int* top_ids, float* top_logprobs, wq4_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ *
+ * Attention over a paged cache, for decoding with drafted tokens: what lies between a layer's projection to
+ * queries, keys and values and its output projection, and what decides on the drafts.
+ *
+ * Sequences are ragged: sequence b's tokens of this step are rows starts[b] .. starts[b + 1] - 1 of every
+ * per-token array. With drafts they form a tree: the first is the last token that is certain, every other one has
+ * a parent among the ones before it. context[b] tokens of the sequence came before; the cache holds them
+ * at places 0 .. context[b] - 1 of the sequence, and token i of this step at place context[b] + i.
+ * ------------------------------------------------------------------------------------------ */
+
+/* A paged cache of one layer: element (page, token of the page, head, feature) of the keys lies at
+ * k + page k_page + token k_token + head k_head + feature, and so for the values; strides in elements of the
+ * call's dtype. A slot is page * page_size + token of the page; pages * page_size < 2^31. */
+typedef struct wq4_kv_cache {
+    void *k, *v;
+    long long k_page, k_token, k_head;
+    long long v_page, v_token, v_head;
+    int pages, page_size;
+} wq4_kv_cache;
+
+/* Queries, keys and values of T tokens, with a norm and a rotation on the way; keys and values go to their slots:
+ *     x' = x / sqrt(mean(x^2) + eps) * weight                  (each head of q and k; fp32 throughout)
+ *     (a, b) -> (a cos w - b sin w, b cos w + a sin w),  w = positions[t] inv_freq[i]
+ * for the pairs i < rot_dim / 2 of features (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved = 1. The
+ * angle is the exact product of position and frequency, however far the position is.
+ *   Q, K, V   [T][q_heads or kv_heads][D] dtype (WQ4_BF16 or WQ4_FP16): element (t, h, d) at t ts + h hs + d; so
+ *             views of one projection's rows will do. Rows do not overlap.
+ *   q_weight, k_weight   [D] dtype; both NULL: no norm. With q_heads == 0 (keys and values only) q_weight is NULL.
+ *   positions   [T] any 64-bit number, read with rot_dim > 0; inv_freq [rot_dim / 2] radians per position.
+ *   Q_out     [T][q_heads][D] with strides of its own; may be Q itself (same strides).
+ *   slots     [T]; a negative one: the token's key and value are not written (padding; its query is). One beyond
+ *             the cache is not written either, and wq4_get_last_error reports WQ4_ERR_INVALID. Slots are
+ *             distinct: of two tokens with the same slot either's elements may stay.
+ * The rest of the cache is left as it is. D <= 1024, any D; multiples of 16 with 16-byte rows are fastest.
+ * T == 0 is a no-op. */
+int wq4_rope_append(const void* Q, long long q_ts, long long q_hs, const void* K, long long k_ts, long long k_hs,
+                    const void* V, long long v_ts, long long v_hs, int T, int q_heads, int kv_heads, int D, int dtype,
+                    const void* q_weight, const void* k_weight, float eps, const long long* positions,
+                    const float* inv_freq, int rot_dim, int interleaved, void* Q_out, long long qo_ts, long long qo_hs,
+                    const wq4_kv_cache* cache, const long long* slots, wq4_stream_t stream);
+
+/* Attention of B sequences' tokens over their paged caches:
+ *     out[t][h] = sum_j p_j V[j][h / (q_heads / kv_heads)],   p = softmax over j of scale q[t][h] . K[j][...]
+ * over the places j of the sequence that the token sees: every place of its context and, among this
+ * step's tokens, those its mask names, or without masks those before it and itself.
+ *   Q, out    [T][q_heads][D] dtype, 16-byte aligned, strides multiples of 8 elements. q_heads is a multiple of
+ *             kv_heads. out must not overlap Q.
+ *   cache     this step's keys and values are in it (wq4_rope_append). k and v 16-byte aligned, strides multiples
+ *             of 8; page_size a multiple of 16.
+ *   page_table   [B][table_width] int, row stride ld_table: page i of sequence b holds its places from i page_size.
+ *             Entries past a sequence's last place are not read.
+ *   starts    [B + 1] int, in DEVICE memory as page_table and context [B] int; 0 <= starts[b] <= starts[b + 1] <= T.
+ *   max_tokens   the most tokens that one sequence has in this step.
+ *   mask      [T][mask_words] 64-bit words: token i of a sequence sees token j of the same where bit j % 64 of
+ *             word j / 64 is set (bits past its sequence's tokens count for nothing). mask_words >=
+ *             ceil(max_tokens / 64). NULL: it sees tokens j <= i.
+ *   lse       [T][q_heads] log of the sum of exp over the places seen, or NULL.
+ * A token that sees nothing gets zeros and an lse of -inf. What lies in places that a token does not see, NaN and
+ * infinities among it, does not reach its output. Rows of out and lse past starts[B] are left as they are.
+ * Probabilities are rounded to dtype before they multiply the values (their sum is not); all sums are fp32.
+ * A page outside the cache, a table too narrow for a sequence, or starts that do not ascend within T and by at most
+ * max_tokens give outputs that mean nothing, and wq4_get_last_error reports WQ4_ERR_INVALID; nothing
+ * is read or written out of bounds.
+ *   workspace   wq4_tree_attention_workspace_bytes(...) bytes on the current device, 16-byte aligned, zero-filled once
+ *             when allocated; every completed call leaves it fit for the next. Calls that may overlap
+ *             on the GPU need separate workspaces (two graphs captured with the same one as well).
+ * D a multiple of 8, at most 256 (WQ4_ERR_UNSUPPORTED otherwise). Results are identical from run to run for
+ * the same lengths. B == 0 or T == 0 is a no-op. */
+int wq4_tree_attention_workspace_bytes(int B, int max_tokens, int q_heads, int kv_heads, int D, size_t* bytes);
+int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_kv_cache* cache, const int* page_table,
+                       int ld_table, int table_width, const int* starts, const int* context, int B, int T,
+                       int max_tokens, int q_heads, int kv_heads, int D, int dtype, float scale,
+                       const unsigned long long* mask, int mask_words, void* out, long long o_ts, long long o_hs,
+                       float* lse, void* workspace, size_t workspace_bytes, wq4_stream_t stream);
+
+/* Verification of drafted tokens: which of them the target model keeps, and the token that follows them, such that
+ * what comes out is distributed as the target's own tokens are.
+ * Row t of the logits answers token t. The walk through sequence b begins at its first token with p =
+ * softmax(logits / temperature) of its row, and goes through the others j in order. Where j's parent is the node the
+ * walk is at, j is tried: it is kept if uniforms[j] q(token_j) < p(token_j), and the walk goes on from j
+ * with the p of its row; otherwise what the draft accounts for is taken from the target,
+ * p = max(p - q, 0) / its sum (p stays where nothing is left). q is the node's row of draft_probs, the distribution that
+ * its children were drawn from; without draft_probs a draft is certain: q = 1 at the token tried, 0 elsewhere. At the
+ * end the next token is drawn from p: the first one at which the sum of p exceeds final_uniforms[b].
+ *   logits    [T][V] dtype (WQ4_BF16, WQ4_FP16 or WQ4_FP32), row stride ld. -inf: a token that cannot occur.
+ *   tokens    [T]; parents [T] int, the parent's place within the sequence (the first token's is not read); starts
+ *             [B + 1] int as in wq4_tree_attention, all in DEVICE memory. A draft outside the vocabulary is
+ *             not kept and takes nothing from p.
+ *   draft_probs   [T][V] fp32, row stride ldp, or NULL.
+ *   temperature   [B] fp32, 0: greedy (the whole of p at the row's first largest logit), or NULL: 1 everywhere.
+ *   uniforms [T], final_uniforms [B]   random numbers of [0, 1).
+ *   accepted  [B] int, the drafts kept; path [B][max(1, max_tokens - 1)] int, row stride ld_path: their places
+ *             within the sequence in order, then -1; next_tokens [B].
+ * The walk ends with next token -1 at a row that holds a NaN or +inf, or nothing but -inf, for a temperature that is
+ * negative, NaN, infinite or so small that the scaled logits overflow, and for a sequence without tokens.
+ * Probabilities are fp32, sums over the vocabulary hold 44 bits and more. starts that do not ascend within
+ * T and by at most max_tokens: as in wq4_tree_attention. V <= 400000. B == 0 is a no-op. */
+int wq4_verify_drafts(const void* logits, long long ld, const long long* tokens, const int* parents, const int* starts,
+                      int B, int T, int max_tokens, int V, int dtype, const float* draft_probs, long long ldp,
+                      const float* temperature, const float* uniforms, const float* final_uniforms, int* accepted,
+                      int* path, int ld_path, long long* next_tokens, wq4_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ *
  * Errors and options.
  * ------------------------------------------------------------------------------------------ */
 
 /* Synchronises the stream, then reports (and clears) what any wq4 kernel on the current device
  * recorded in the device status word: a failed bounds check of the debug build (WQ4_ERR_BOUNDS),
- * else a blob header that did not match its call (WQ4_ERR_INVALID), else a pipeline timeout
+ * else a blob header that did not match its call or an index in device memory outside what it
+ * indexes (WQ4_ERR_INVALID), else a pipeline timeout
  * (WQ4_ERR_TIMEOUT); with nothing recorded, a pending CUDA error (WQ4_ERR_CUDA), else WQ4_OK. A
  * call whose waits ran out stops early and leaves its outputs undefined; the context stays
  * usable, but a workspace it used must be zero-filled again before the next call (its split

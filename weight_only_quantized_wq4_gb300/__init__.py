@@ -28,6 +28,13 @@ GROUP = 128
 _lib = None
 
 
+class KvCache(ctypes.Structure):
+    """wq4_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_longlong) for n in ("k_page", "k_token", "k_head", "v_page", "v_token", "v_head")] + [
+        ("pages", ctypes.c_int), ("page_size", ctypes.c_int)]
+
+
 class Wq4Error(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -77,6 +84,13 @@ def load_library(path: str = LIB_PATH):
         "wq4_silu_mul_quant": (c_int, [vp, ll, c_int, c_int, c_int, vp, ll, vp, ll, vp]),
         "wq4_block_mm": (c_int, [vp, ll, vp, ll, vp, ll, vp, ll, vp, ll, c_int, c_int, c_int, c_int, vp]),
         "wq4_token_logprobs": (c_int, [vp, ll, vp, c_int, c_int, c_int, c_int, vp, vp, vp, vp, vp]),
+        "wq4_rope_append": (c_int, [vp, ll, ll, vp, ll, ll, vp, ll, ll, c_int, c_int, c_int, c_int, c_int, vp, vp, ctypes.c_float,
+                                    vp, vp, c_int, c_int, vp, ll, ll, ctypes.POINTER(KvCache), vp, vp]),
+        "wq4_tree_attention_workspace_bytes": (c_int, [c_int, c_int, c_int, c_int, c_int, ctypes.POINTER(c_size)]),
+        "wq4_tree_attention": (c_int, [vp, ll, ll, ctypes.POINTER(KvCache), vp, c_int, c_int, vp, vp, c_int, c_int, c_int,
+                                       c_int, c_int, c_int, c_int, ctypes.c_float, vp, c_int, vp, ll, ll, vp, vp, c_size, vp]),
+        "wq4_verify_drafts": (c_int, [vp, ll, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, vp, ll, vp, vp, vp, vp, vp, c_int,
+                                      vp, vp]),
         "wq4_get_last_error": (c_int, [vp]),
         "wq4_debug_checks": (c_int, []),
         "wq4_last_violation": (c_int, [ip]),
@@ -386,7 +400,8 @@ def _bind():
         spec.loader.exec_module(module)
         _binding = module
     _binding.bind(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in (
-        lib.wq4_add_rmsnorm_quant, lib.wq4_silu_mul_quant, lib.wq4_block_mm, lib.wq4_token_logprobs)])
+        lib.wq4_add_rmsnorm_quant, lib.wq4_silu_mul_quant, lib.wq4_block_mm, lib.wq4_token_logprobs,
+        lib.wq4_rope_append, lib.wq4_tree_attention, lib.wq4_verify_drafts)])
     _bound = lib
 
 
@@ -485,3 +500,86 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entropy=N
     if rc:
         raise Wq4Error(rc, "wq4_token_logprobs")
     return logprobs, entropy, top_ids, top_logprobs
+
+
+# ------------------------------------------------------------------------------------ attention over a paged cache
+def rope_append(q, k, v, k_cache, v_cache, slots, positions=None, inv_freq=None, q_weight=None, k_weight=None,
+                eps: float = 1e-6, interleaved: bool = False, q_out=None):
+    """Norm and rotation of each query and key head; keys and values to their slots of a paged cache (wq4_rope_append).
+
+    q, k, v: bf16/fp16 [T][heads][D], with any strides along tokens and heads (views of one projection's rows will
+    do); q may be None. k_cache, v_cache: [pages][page_size][kv heads][D]. slots: int64 [T], page * page_size + place
+    in the page; a negative one: the token's key and value are not written. positions: int64 [T] with inv_freq,
+    fp32 [R/2] radians per position: the first R features of each head are rotated, in pairs (i, i + R/2) or, with
+    interleaved, (2i, 2i + 1). q_weight, k_weight: [D], RMS norm of each head ahead of that. Returns q_out (allocated if
+    not given; may be q itself; None without q)."""
+    if _bound is not _lib or _lib is None:
+        _bind()
+    if q is not None and q_out is None:
+        q_out = _torch().empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+    rc = _binding.rope_append(q, k, v, k_cache, v_cache, slots, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out)
+    if rc:
+        raise Wq4Error(rc, "wq4_rope_append")
+    return q_out
+
+
+def tree_attention_workspace_bytes(B: int, max_tokens: int, q_heads: int, kv_heads: int, D: int) -> int:
+    """Workspace of tree_attention for B sequences of up to max_tokens tokens each, on the current device."""
+    out = ctypes.c_size_t(0)
+    _check(load_library().wq4_tree_attention_workspace_bytes(B, max_tokens, q_heads, kv_heads, D, ctypes.byref(out)),
+           "wq4_tree_attention_workspace_bytes")
+    return int(out.value)
+
+
+def tree_attention(q, k_cache, v_cache, page_table, starts, context, max_tokens: int = 1, mask=None, scale=None, out=None,
+                   lse=None, workspace=None):
+    """Attention of each sequence's tokens over its paged cache (wq4_tree_attention).
+
+    q: bf16/fp16 [T][heads][D]; k_cache, v_cache: [pages][page_size][kv heads][D], this step's keys and values in them
+    (rope_append); page_table int32 [B][width]; starts int32 [B + 1]: sequence b's tokens are rows starts[b] ..
+    starts[b + 1] - 1, at most max_tokens; context int32 [B]: the places of the cache ahead of them, which every token
+    sees. mask int64 [T][ceil(max_tokens / 64)]: bit j % 64 of word j / 64 where a token sees token j of its sequence;
+    None: j up to itself. scale: 1 / sqrt(D) by default. lse: fp32 [T][heads], filled if given. workspace:
+    alloc_workspace(tree_attention_workspace_bytes(...)), allocated if not given. Returns out."""
+    if _bound is not _lib or _lib is None:
+        _bind()
+    if out is None:
+        out = _torch().empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if workspace is None:
+        torch = _torch()
+        with torch.cuda.device(q.device):
+            nbytes = tree_attention_workspace_bytes(page_table.shape[0], max_tokens, q.shape[-2], k_cache.shape[-2], q.shape[-1])
+        workspace = alloc_workspace(nbytes, q.device)
+    rc = _binding.tree_attention(q, k_cache, v_cache, page_table, starts, context, max_tokens, mask, scale, out, lse, workspace)
+    if rc:
+        raise Wq4Error(rc, "wq4_tree_attention")
+    return out
+
+
+def verify_drafts(logits, tokens, parents, starts, uniforms, final_uniforms, max_tokens: int, draft_probs=None, temperature=None,
+                  accepted=None, path=None, next_tokens=None):
+    """Which drafted tokens the target keeps, and the token that follows them (wq4_verify_drafts).
+
+    logits: bf16, fp16 or fp32 [T][V], row t answering token t; tokens int64 [T]; parents int32 [T], places within the
+    sequence; starts int32 [B + 1]; the first token of each sequence is certain, the others are drafts. uniforms fp32
+    [T] and final_uniforms fp32 [B]: random numbers of [0, 1). draft_probs fp32 [T][V]: row t is what t's children were
+    drawn from; None: drafts are certain. temperature fp32 [B], 0 for greedy. Returns (accepted int32 [B], path int32
+    [B][max(1, max_tokens - 1)]: the kept drafts' places, then -1; next_tokens int64 [B]); allocated if not given."""
+    if _bound is not _lib or _lib is None:
+        _bind()
+    if accepted is None or path is None or next_tokens is None:
+        torch = _torch()
+        B, dev = starts.shape[0] - 1, logits.device
+        if accepted is None:
+            accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        if path is None:
+            path = torch.empty((B, max(1, max_tokens - 1)), dtype=torch.int32, device=dev)
+        if next_tokens is None:
+            next_tokens = torch.empty(B, dtype=torch.int64, device=dev)
+    rc = _binding.verify_drafts(logits, tokens, parents, starts, uniforms, final_uniforms, max_tokens, draft_probs, temperature,
+                                accepted, path, next_tokens)
+    if rc:
+        raise Wq4Error(rc, "wq4_verify_drafts")
+    return accepted, path, next_tokens
