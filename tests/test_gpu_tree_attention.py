@@ -143,6 +143,36 @@ def test_long_and_ragged(lib, dtype, D):
     Case(counts, context, 8, 2, D, 16, dtype, True, seed=1, extra_rows=3).check(lib)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("counts,context,Hq,Hk", [([32, 1], [40000, 3000], 4, 1), ([50], [30000], 8, 1), ([16, 3], [300, 20000], 4, 2)])
+def test_trees_over_long_contexts(lib, dtype, D, counts, context, Hq, Hk):
+    """So many tiles for each CTA that every buffer is used many times over; every sixth token is compared."""
+    c = Case(counts, context, Hq, Hk, D, 64, dtype, True, seed=2)
+    out, lse = c.run(lib)
+    keep = range(0, sum(counts), 6)
+    q, K, V, page = c.q, c.k.double().cpu().numpy(), c.v.double().cpu().numpy(), 64
+    parts = [np.zeros(x, dtype=np.float64) for x in (q.shape, q.shape[:2], q.shape, q.shape[:2])]
+    for t in keep:
+        b = int(np.searchsorted(c.starts_list, t, side="right")) - 1
+        places = np.concatenate([np.arange(context[b]), context[b] + np.flatnonzero(c.seen[t])])
+        pages = c.table[b].cpu().numpy()[places // page]
+        x = q[t].double().cpu().numpy()
+        for h in range(Hq):
+            k, v = K[pages, places % page, h * Hk // Hq], V[pages, places % page, h * Hk // Hq]
+            s = D ** -0.5 * (k @ x[h])
+            p = np.exp(s - s.max())
+            parts[1][t, h] = s.max() + np.log(p.sum())
+            p /= p.sum()
+            parts[0][t, h], parts[2][t, h] = p @ v, p @ np.abs(v)
+            parts[3][t, h] = D ** -0.5 * (np.abs(k) @ np.abs(x[h])).max()
+    drop = np.setdiff1d(np.arange(sum(counts)), list(keep))
+    out, lse = out.clone(), lse.clone()
+    for t in drop:                                   # (not compared)
+        out[t], lse[t] = 0, 0
+    c.compare(out, lse, *parts)
+
+
 def test_many_sequences(lib):
     rng = np.random.default_rng(0)
     counts, context = rng.integers(0, 4, 400).tolist(), rng.integers(0, 90, 400).tolist()

@@ -230,4 +230,9 @@ inline bool encode_cache(EncodeTiledFn fn, CUtensorMap* map, int dtype, void* p,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The kernel for many rows per kv head (wq4_attention_tiles.cu): D <= 128, scale above 0.
+int tiles_rows();                       // rows of a unit
+int tiles_places();                     // places of a tile
+int launch_attention_tiles(const Runtime& rt, const AttnArgs& a, int dtype, wq4_stream_t st);
+
 }  // namespace wq4

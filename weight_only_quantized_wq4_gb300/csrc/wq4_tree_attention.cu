@@ -427,14 +427,17 @@ int go_attention(const Runtime& rt, AttnArgs& a, wq4_stream_t st) {
 struct Space {
     size_t stats, parts, bytes;
 };
-Space space_of(int grid, int D) {
+Space space_of(int grid, int D, int rows) {
     const size_t parts = 2 * static_cast<size_t>(grid), dp = (D + 63) / 64 * 64;
     Space s;
     s.stats = (4 * static_cast<size_t>(grid) + 255) / 256 * 256;
-    s.parts = s.stats + parts * kRows * 8;
-    s.bytes = s.parts + parts * kRows * dp * 4;
+    s.parts = s.stats + parts * rows * 8;
+    s.bytes = s.parts + parts * rows * dp * 4;
     return s;
 }
+
+// The kernel with tiles of 128 rows, where the rows of a kv head fill more than one of 16.
+bool use_tiles(int max_tokens, int group, int D) { return static_cast<long long>(max_tokens) * group > kRows && D <= 128; }
 
 int check_heads(int B, int max_tokens, int q_heads, int kv_heads, int D) {
     if (B < 0 || max_tokens < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads || D < 1) return WQ4_ERR_INVALID;
@@ -454,7 +457,7 @@ int wq4_tree_attention_workspace_bytes(int B, int max_tokens, int q_heads, int k
     if (const int rc = check_heads(B, max_tokens, q_heads, kv_heads, D)) return rc;
     Runtime rt;
     if (const int rc = runtime(&rt)) return rc;
-    *bytes = space_of(rt.sm_count, D).bytes;
+    *bytes = space_of(rt.sm_count, D, use_tiles(max_tokens, q_heads / kv_heads, D) ? tiles_rows() : kRows).bytes;
     return WQ4_OK;
 }
 
@@ -487,7 +490,9 @@ int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_
     if (const int rc = runtime(&rt)) return rc;
     AttnArgs a{};
     a.grid = rt.sm_count;
-    const Space sp = space_of(a.grid, D);
+    // (the tiles' softmax takes maxima ahead of the scale; the other kernel, whose parts are smaller, after it)
+    const bool tiles = use_tiles(max_tokens, q_heads / kv_heads, D) && scale > 1e-30f;
+    const Space sp = space_of(a.grid, D, tiles ? tiles_rows() : kRows);
     if (!workspace || workspace_bytes < sp.bytes) return WQ4_ERR_WORKSPACE;
     a.q = static_cast<const uint16_t*>(Q);
     a.out = static_cast<uint16_t*>(out);
@@ -509,15 +514,16 @@ int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_
     a.status = rt.status;
     a.timeout_cycles = rt.timeout_cycles;
     a.box = 16;                                      // the places of one copy: they lie in one page
-    while (a.box < kTile && cache.page_size % (2 * a.box) == 0) a.box *= 2;
+    while (a.box < (tiles ? tiles_places() : kTile) && cache.page_size % (2 * a.box) == 0) a.box *= 2;
     const int panels = (D + 63) / 64;
-    const bool whole = D % 64 == 0;                  // all panels in one copy, or (D cuts one) a copy each
+    const bool whole = D % 64 == 0 && !tiles;        // all panels in one copy, or (D cuts one, or they lie apart) a copy each
     a.copies = whole ? 1 : panels;
     if (!encode_cache(rt.encode, &a.k_map, dtype, cache.k, D, cache.k_token, cache.k_head, cache.k_page, cache, kv_heads, a.box, whole ? panels : 1) ||
         !encode_cache(rt.encode, &a.v_map, dtype, cache.v, D, cache.v_token, cache.v_head, cache.v_page, cache, kv_heads, a.box, whole ? panels : 1))
         return WQ4_ERR_CUDA;
     if (rt.trace)
-        std::fprintf(stderr, "wq4: tree_attention B=%d tokens=%d heads=%d/%d D=%d box=%d grid=%d\n", B, max_tokens, q_heads, kv_heads, D, a.box, a.grid);
+        std::fprintf(stderr, "wq4: tree_attention B=%d tokens=%d heads=%d/%d D=%d box=%d grid=%d rows=%d\n", B, max_tokens, q_heads, kv_heads, D, a.box, a.grid, tiles ? tiles_rows() : kRows);
+    if (tiles) return launch_attention_tiles(rt, a, dtype, stream);
     if (dtype == WQ4_BF16) {
         switch (panels) {
             case 1: return go_attention<true, 1>(rt, a, stream);
