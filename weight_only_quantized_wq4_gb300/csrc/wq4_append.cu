@@ -66,12 +66,113 @@ constexpr int kAppendMaxD = 1024;
 // ROTATE: 0 none, 1 pairs (i, i + R / 2), 2 pairs (2 i, 2 i + 1).
 template <bool BF16, int ROTATE, bool NORM>
 __global__ void __launch_bounds__(1024) append_kernel(const AppendArgs a) {
-    extern __shared__ float2 turn[];                 // [tokens][R / 2]
+    extern __shared__ float4 turns[];                // [tokens][R / 2] (cos, sin)
+    float2* const turn = reinterpret_cast<float2*>(turns);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int heads = a.Hq + 2 * a.Hk, D = a.D, P = a.per_head;
     const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
     const int tokens = static_cast<int>(min(static_cast<long long>(a.tokens), a.T - t0));
+    const int lane = threadIdx.x % P, groups = blockDim.x / P;
+    // this thread's two vectors of a head
+    int c0 = lane * 16, c1 = c0 + 8;
+    bool rot = ROTATE == 2 ? c0 < a.R : false, rot1 = ROTATE == 2 ? c1 < a.R : false;
+    if (ROTATE == 1) {
+        if (lane < a.R / 16) c0 = lane * 8, c1 = c0 + a.R / 2, rot = true;
+    }
+    const bool in = c0 < D;
+    const int all = tokens * heads;
+    // One head of one token: where it lies, what is read of it.
+    struct Item {
+        long long t, slot;
+        int tok, head, hk;
+        bool live, is_q, is_v;
+        uint4 x0, x1;
+    };
+    auto load = [&](int item) {
+        Item m;
+        m.tok = item / heads, m.head = item - m.tok * heads;
+        m.live = in && item < all;
+        m.t = t0 + m.tok;
+        m.is_q = m.head < a.Hq, m.is_v = m.head >= a.Hq + a.Hk;
+        m.hk = m.is_v ? m.head - a.Hq - a.Hk : m.head - a.Hq;
+        m.x0 = m.x1 = make_uint4(0, 0, 0, 0);
+        m.slot = -1;
+        if (m.live) {
+            const uint16_t* p = m.is_q ? a.q + m.t * a.q_ts + m.head * a.q_hs : m.is_v ? a.v + m.t * a.v_ts + m.hk * a.v_hs
+                                                                                   : a.k + m.t * a.k_ts + m.hk * a.k_hs;
+            m.x0 = *reinterpret_cast<const uint4*>(p + c0);
+            m.x1 = *reinterpret_cast<const uint4*>(p + c1);
+            if (!m.is_q) m.slot = a.slots[m.t];
+        }
+        return m;
+    };
+    auto finish = [&](Item& m) {
+        float v0[8], v1[8];
+        unpack8<BF16>(m.x0, v0);
+        unpack8<BF16>(m.x1, v1);
+        float ss = 0.f;
+        if constexpr (NORM) {                        // (every lane of the warp, whatever its head is)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(v0[j], v0[j], fmaf(v1[j], v1[j], ss));
+            for (int d = P / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        }
+        if (!m.live) return;
+        if (!m.is_v) {
+            if constexpr (NORM) {
+                const float r = rsqrtf(fmaf(ss, a.one_over_D, a.eps));
+                float w0[8], w1[8];
+                const uint16_t* w = m.is_q ? a.q_weight : a.k_weight;
+                unpack8<BF16>(*reinterpret_cast<const uint4*>(w + c0), w0);
+                unpack8<BF16>(*reinterpret_cast<const uint4*>(w + c1), w1);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v0[j] *= r * w0[j], v1[j] *= r * w1[j];
+            }
+            if (ROTATE == 1 && rot) {
+                const float4* cs = reinterpret_cast<const float4*>(turn + m.tok * (a.R / 2) + c0);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float4 c = cs[j / 2];
+                    const float x = v0[j], y = v1[j], x2 = v0[j + 1], y2 = v1[j + 1];
+                    v0[j] = x * c.x - y * c.y;
+                    v1[j] = y * c.x + x * c.y;
+                    v0[j + 1] = x2 * c.z - y2 * c.w;
+                    v1[j + 1] = y2 * c.z + x2 * c.w;
+                }
+            }
+            if (ROTATE == 2) {
+                auto rotate = [&](float(&v)[8], const float2* cs) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = v[2 * j], y = v[2 * j + 1];
+                        v[2 * j] = x * cs[j].x - y * cs[j].y;
+                        v[2 * j + 1] = y * cs[j].x + x * cs[j].y;
+                    }
+                };
+                const float2* cs = turn + m.tok * (a.R / 2) + c0 / 2;
+                if (rot) rotate(v0, cs);
+                if (rot1) rotate(v1, cs + 4);
+            }
+            m.x0 = pack8<BF16>(v0);
+            m.x1 = pack8<BF16>(v1);
+        }
+        uint16_t* out = nullptr;
+        if (m.is_q) {
+            out = a.q_out + m.t * a.qo_ts + m.head * a.qo_hs;
+        } else if (m.slot >= 0) {                    // (a negative one is a padded token)
+            if (m.slot < static_cast<long long>(a.cache.pages) * a.cache.page_size) {
+                out = m.is_v ? a.cache.v_at(static_cast<unsigned>(m.slot), m.hk) : a.cache.k_at(static_cast<unsigned>(m.slot), m.hk);
+            } else {
+                atomicOr(a.status, kStatusBadIndex);
+            }
+        }
+        if (out) {
+            *reinterpret_cast<uint4*>(out + c0) = m.x0;
+            *reinterpret_cast<uint4*>(out + c1) = m.x1;
+        }
+    };
+    int item = threadIdx.x / P;
+    Item next = load(item);                          // (under way while the angles are found)
     if constexpr (ROTATE != 0) {
         const int half = a.R / 2;
         for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
@@ -81,92 +182,11 @@ __global__ void __launch_bounds__(1024) append_kernel(const AppendArgs a) {
         }
         __syncthreads();
     }
-    const int lane = threadIdx.x % P, groups = blockDim.x / P;
-    // this thread's two vectors of a head
-    int c0 = lane * 16, c1 = c0 + 8;
-    bool rot = ROTATE == 2 ? c0 < a.R : false, rot1 = ROTATE == 2 ? c1 < a.R : false;
-    if (ROTATE == 1) {
-        if (lane < a.R / 16) c0 = lane * 8, c1 = c0 + a.R / 2, rot = true;
-    }
-    const bool in = c0 < D;
-    for (int item = threadIdx.x / P; item < (tokens * heads + groups - 1) / groups * groups; item += groups) {
-        const int tok = item / heads, head = item - tok * heads;
-        const bool live = in && item < tokens * heads;
-        const long long t = t0 + tok;
-        const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hk;
-        const int hk = is_v ? head - a.Hq - a.Hk : head - a.Hq;
-        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-        if (live) {
-            const uint16_t* p = is_q ? a.q + t * a.q_ts + head * a.q_hs : is_v ? a.v + t * a.v_ts + hk * a.v_hs
-                                                                                : a.k + t * a.k_ts + hk * a.k_hs;
-            x0 = *reinterpret_cast<const uint4*>(p + c0);
-            x1 = *reinterpret_cast<const uint4*>(p + c1);
-        }
-        float v0[8], v1[8];
-        unpack8<BF16>(x0, v0);
-        unpack8<BF16>(x1, v1);
-        float ss = 0.f;
-        if constexpr (NORM) {                        // (every lane of the warp, whatever its head is)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(v0[j], v0[j], fmaf(v1[j], v1[j], ss));
-            for (int d = P / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        }
-        if (!is_v) {
-            if constexpr (NORM) {
-                const float r = rsqrtf(fmaf(ss, a.one_over_D, a.eps));
-                float w0[8], w1[8];
-                const uint16_t* w = is_q ? a.q_weight : a.k_weight;
-                if (live) {
-                    unpack8<BF16>(*reinterpret_cast<const uint4*>(w + c0), w0);
-                    unpack8<BF16>(*reinterpret_cast<const uint4*>(w + c1), w1);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v0[j] *= r * w0[j], v1[j] *= r * w1[j];
-                }
-            }
-            if (ROTATE == 1 && live && rot) {
-                const float2* cs = turn + tok * (a.R / 2) + c0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float x = v0[j], y = v1[j];
-                    v0[j] = x * cs[j].x - y * cs[j].y;
-                    v1[j] = y * cs[j].x + x * cs[j].y;
-                }
-            }
-            if (ROTATE == 2 && live) {
-                const float2* cs = turn + tok * (a.R / 2) + c0 / 2;
-                auto rotate = [&](float(&v)[8], const float2* cs) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = v[2 * j], y = v[2 * j + 1];
-                        v[2 * j] = x * cs[j].x - y * cs[j].y;
-                        v[2 * j + 1] = y * cs[j].x + x * cs[j].y;
-                    }
-                };
-                if (rot) rotate(v0, cs);
-                if (rot1) rotate(v1, cs + 4);
-            }
-            x0 = pack8<BF16>(v0);
-            x1 = pack8<BF16>(v1);
-        }
-        if (live) {
-            uint16_t* out = nullptr;
-            if (is_q) {
-                out = a.q_out + t * a.qo_ts + head * a.qo_hs;
-            } else {
-                const long long slot = a.slots[t];
-                if (slot >= 0) {                     // (a negative one is a padded token)
-                    if (slot < static_cast<long long>(a.cache.pages) * a.cache.page_size) {
-                        out = is_v ? a.cache.v_at(static_cast<unsigned>(slot), hk) : a.cache.k_at(static_cast<unsigned>(slot), hk);
-                    } else {
-                        atomicOr(a.status, kStatusBadIndex);
-                    }
-                }
-            }
-            if (out) {
-                *reinterpret_cast<uint4*>(out + c0) = x0;
-                *reinterpret_cast<uint4*>(out + c1) = x1;
-            }
-        }
+    for (const int rounds = (all + groups - 1) / groups * groups; item < rounds;) {
+        Item now = next;
+        item += groups;
+        if (item < rounds) next = load(item);
+        finish(now);
     }
 }
 

@@ -6,9 +6,9 @@
 // w exceeds u z.
 //
 // A cluster of CTAs walks a sequence, each with its share of the vocabulary's weights in shared memory as fp32, so that a
-// row of logits is read once however many children are tried. Each step over the weights ends with one exchange: every
-// CTA tells the others its part of the sum and, if it has it, the weight of the draft that is tried next; all of them then
-// come to the same decision. Which token is drawn hangs on sums over the whole vocabulary next to a random border, so sums
+// row of logits is read once however many children are tried. Each step over them ends with one exchange: every CTA tells
+// the others its part of the sum and, if it has it, the weight of the draft that is tried next; all of them then come
+// to the same decision. Which token is drawn hangs on sums over the whole vocabulary next to a random border, so sums
 // are kept as a pair of floats (the rounding of each addition is carried along), 44 bits and more; the weights
 // themselves are rounded as fp32 operations round them, one by one.
 #include <cuda_bf16.h>
@@ -64,50 +64,103 @@ __device__ __forceinline__ Sum warp_sum(Sum x) {
         o.c = __shfl_xor_sync(0xffffffffu, x.c, d);
         x.add(o);
     }
-    return x;                                        // (lanes may differ in the last bits; lane 0's counts)
+    x.s = __shfl_sync(0xffffffffu, x.s, 0);          // (lanes may differ in the last bits, and all decide alike)
+    x.c = __shfl_sync(0xffffffffu, x.c, 0);
+    return x;
+}
+// 1 / x, rounded to nearest (but for ties within 2^-24 of a step): one step of Newton's method from the reciprocal of x.s.
+__device__ __forceinline__ float reciprocal(const Sum& x) {
+    const float hi = __fadd_rn(x.s, x.c), lo = __fadd_rn(__fsub_rn(x.s, hi), x.c), r = __frcp_rn(hi);
+    return __fmaf_rn(r, __fmaf_rn(-lo, r, __fmaf_rn(-hi, r, 1.f)), r);
 }
 
-// What a CTA tells the others at the end of a step.
+// What a CTA tells the others at the end of a step. Of a row's logits: its largest, the sum of exp against that (greedy: the
+// largest one's place) and the logit of the draft that is tried, -inf where it is another CTA's. Of weights: their sum, as
+// a pair, and the weight of the draft that is tried next, -1 where it is another CTA's, by the new weights and by the old.
 struct Part {
-    float s, c;                         // its sum; or, of a row's first step, its largest logit and (greedy) that one's place
-    float w;                            // the weight of the draft that is tried next, -1 where it is another CTA's
-    int pad;
+    float a, b, c, d;
 };
+
+constexpr int kHeld = 128;              // drafts of a sequence whose parents, tokens and numbers are kept at hand
 
 struct Shared {
     Part part[2][kMaxCluster];          // [turn][CTA]: written by the others
-    Sum sum[kWarps];
-    float top[kWarps];
+    float top[kWarps], sum[kWarps];
     int top_at[kWarps];
-    double block[kMaxShare / kBlock];
-    int found;
+    Sum block[kMaxShare / kBlock];
+    long long tokens[kHeld];
+    int parents[kHeld];
+    float uniforms[kHeld];
 };
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, const Part& p) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(__float_as_uint(p.s)),
-                 "r"(__float_as_uint(p.c)), "r"(__float_as_uint(p.w)), "r"(p.pad)
-                 : "memory");
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(p.a), "f"(p.b), "f"(p.c), "f"(p.d) : "memory");
 }
 
+// Eight values of a row from column i on, where the row's columns are 16-byte aligned in eights, and one.
 template <int DT>
-__device__ __forceinline__ float logit(const void* p, long long i) {
+__device__ __forceinline__ void load8(const void* p, long long i, uint4& lo, uint4& hi) {
+    if constexpr (DT == WQ4_FP32) {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+        lo = q[0], hi = q[1];
+    } else {
+        lo = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    }
+}
+template <int DT>
+__device__ __forceinline__ void values8(const uint4& lo, const uint4& hi, float (&v)[8]) {
+    if constexpr (DT == WQ4_FP32) {
+        const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(u[j]);
+    } else {
+        unpack8<DT == WQ4_BF16>(lo, v);
+    }
+}
+template <int DT>
+__device__ __forceinline__ float value1(const void* p, long long i) {
     if constexpr (DT == WQ4_FP32) return static_cast<const float*>(p)[i];
     else return to_f32<DT == WQ4_BF16>(static_cast<const uint16_t*>(p)[i]);
 }
 
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
-    extern __shared__ float w[];                     // this CTA's weights
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
+    extern __shared__ float4 w4[];                   // this CTA's logits, scaled, then weights
+    float* const w = reinterpret_cast<float*>(w4);
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0, b = blockIdx.x / C;
     const int v0 = rank * a.share, mine = max(0, min(a.share, a.V - v0));   // vocabulary [v0, v0 + mine)
+    const int blocks = (mine + kBlock - 1) / kBlock;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (C > 1) cluster_sync();                       // (every CTA is there before anything is sent to it)
+    const int s0 = a.starts[b], s1 = a.starts[b + 1];
+    int n = static_cast<int>(static_cast<unsigned>(s1) - static_cast<unsigned>(s0));
+    if (s0 < 0 || s1 < s0 || s1 > a.T || n > a.max_tokens) {
+        if (tid == 0) atomicOr(a.status, kStatusBadIndex);
+        n = 0;
+    }
+    if (tid < kHeld && tid < n) {
+        sh.parents[tid] = a.parents[s0 + tid];
+        sh.tokens[tid] = a.tokens[s0 + tid];
+        sh.uniforms[tid] = a.uniforms[s0 + tid];
+    }
+    const float heat = a.temperature ? a.temperature[b] : 1.f;
+    const bool greedy = heat == 0.f;
+    const float inv_heat = greedy ? 1.f : __frcp_rn(heat);
+    bool fine = n > 0 && heat >= 0.f && !isinf(heat);
+    // (every CTA is there before anything is sent to it)
+    if (C > 1) cluster_sync();
+    else __syncthreads();
     int turn = 0;
     // Sends this CTA's part to all, waits for theirs.
-    auto exchange = [&](Part p) {
+    auto exchange = [&](const Part& p) {
         if (tid < C) {
             if (C > 1) st_cluster(map_to_rank(smem_u32(&sh.part[turn][rank]), tid), p);
             else sh.part[turn][0] = p;
@@ -118,155 +171,256 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
         turn ^= 1;                                   // (a CTA may send its next part while another reads these)
         return turn ^ 1;
     };
-    // The CTA's sum from every thread's, in all threads.
-    auto cta_sum = [&](Sum x) {
-        x = warp_sum(x);
-        if (lane == 0) sh.sum[warp] = x;
-        __syncthreads();
-        Sum t{0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) t.add(sh.sum[i]);
-        __syncthreads();
-        return t;
-    };
-    const int s0 = a.starts[b], s1 = a.starts[b + 1];
-    int n = static_cast<int>(static_cast<unsigned>(s1) - static_cast<unsigned>(s0));
-    if (s0 < 0 || s1 < s0 || s1 > a.T || n > a.max_tokens) {
-        if (tid == 0) atomicOr(a.status, kStatusBadIndex);
-        n = 0;
-    }
-    const float heat = a.temperature ? a.temperature[b] : 1.f;
-    const bool greedy = heat == 0.f;
-    const float inv_heat = greedy ? 1.f : __frcp_rn(heat);
-    bool fine = n > 0 && heat >= 0.f && !isinf(heat);
-    int node = 0, kept = 0, j = 0;                   // j: the last draft tried
-    double z = 0;
     int* path = a.path + static_cast<long long>(b) * a.ld_path;
-
+    int node = 0, kept = 0, j = 0;                   // j: the last draft tried
     // The next draft to try after j: a child of the node whose token exists.
-    long long draft = 0;
+    long long draft = -1;
+    float draft_q = 1.f;
     auto next_draft = [&] {
         while (++j < n) {
-            if (a.parents[s0 + j] != node) continue;
-            draft = a.tokens[s0 + j];
-            if (draft >= 0 && draft < a.V) return;
+            if ((j < kHeld ? sh.parents[j] : a.parents[s0 + j]) != node) continue;
+            draft = j < kHeld ? sh.tokens[j] : a.tokens[s0 + j];
+            if (draft >= 0 && draft < a.V) {
+                if (a.draft_probs) draft_q = a.draft_probs[(s0 + node) * a.ldp + draft];
+                return;
+            }
         }
+        draft = -1;
     };
-    // Adds up what the CTAs told: z, and the draft's weight.
-    float draft_w = 0.f;
-    auto take = [&](int was) {
-        double s = 0;
-        draft_w = -1.f;
-        for (int i = 0; i < C; ++i) {
-            const Part& p = sh.part[was][i];
-            s += static_cast<double>(p.s) + static_cast<double>(p.c);
-            draft_w = fmaxf(draft_w, p.w);
+    // Whether the draft is kept, its weight and the weights' sum given. (In fp32: a random number lies as near to the border as these
+    // three roundings reach once in some millions.)
+    auto keeps = [&](float weight, float z) { return __fmul_rn(__fmul_rn(j < kHeld ? sh.uniforms[j] : a.uniforms[s0 + j], draft_q), z) < weight; };
+    auto here = [&](long long t) { return t >= v0 && t < v0 + mine; };
+    // f of each of the CTA's weights and of the same place of another row (null: 0): the sums of blocks of 1024 go to sh.block, f
+    // itself, if it is to, into the weights' place. Returns the sum of all, in warp 0.
+    auto weigh = [&](const float* other, bool write, auto f) {
+        const bool vec = (reinterpret_cast<uintptr_t>(other) & 15u) == 0;
+        for (int k = warp; k < blocks; k += kWarps) {
+            Sum s{0.f, 0.f};
+            const int from = k * kBlock + lane * 4;
+            if (vec && k * kBlock + kBlock <= mine) {
+                float4 o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = other ? *reinterpret_cast<const float4*>(other + from + 128 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = from + 128 * i;
+                    float4 x = w4[at / 4];
+                    x.x = f(at, x.x, o[i].x), x.y = f(at + 1, x.y, o[i].y), x.z = f(at + 2, x.z, o[i].z), x.w = f(at + 3, x.w, o[i].w);
+                    if (write) w4[at / 4] = x;
+                    s.add(x.x), s.add(x.y), s.add(x.z), s.add(x.w);
+                }
+            } else {
+                for (int i0 = 0; i0 < kBlock; i0 += 256) {
+                    float o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = k * kBlock + i0 + 32 * i + lane;
+                        o[i] = other && at < mine ? other[at] : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = k * kBlock + i0 + 32 * i + lane;
+                        if (at < mine) {
+                            const float x = f(at, w[at], o[i]);
+                            if (write) w[at] = x;
+                            s.add(x);
+                        }
+                    }
+                }
+            }
+            s = warp_sum(s);
+            if (lane == 0) sh.block[k] = s;
         }
-        return s;
+        __syncthreads();
+        Sum all{0.f, 0.f};
+        if (warp == 0) {
+            for (int k = lane; k < blocks; k += 32) all.add(sh.block[k]);
+            all = warp_sum(all);
+        }
+        return all;
     };
-    auto draft_here = [&] {                          // (after the CTA's weights are written)
-        const long long at = draft - v0;
-        return j < n && at >= 0 && at < mine ? w[at] : -1.f;
+    // The sum that the CTAs told, in every thread of the cluster to the same bits.
+    auto sum_of = [&](int was) {
+        Sum t{0.f, 0.f};
+        if (lane < C) t = Sum{sh.part[was][lane].a, sh.part[was][lane].b};
+        return warp_sum(t);
     };
 
+    // The largest of the lanes' values, and the lowest place of it.
+    auto largest = [&](float& x, int& at, int from) {
+        for (int d = from; d; d >>= 1) {
+            const float o = __shfl_xor_sync(0xffffffffu, x, d);
+            const int o_at = __shfl_xor_sync(0xffffffffu, at, d);
+            if (o > x || (o == x && o_at < at)) at = o_at;
+            x = fmaxf(x, o);
+        }
+    };
+    float top = 0.f;
+    int top_at = 0, was = 0;
+    // a draft that was not kept: its row, 1 / sum of the weights it is taken from, its place among the CTA's
+    const float* q_row = nullptr;
+    float inv = 0.f;
+    long long tried = -1;
+    bool pending = false;                            // whether it is still to be taken
+    auto left = [&](int i, float x, float q) {
+        if (a.draft_probs) return fmaxf(__fsub_rn(__fmul_rn(x, inv), q), 0.f);
+        return i == tried ? 0.f : x;
+    };
     while (fine) {
-        // ---- the node's row
-        const long long row = (s0 + node) * a.ld;
-        const long long r0 = row + v0;
-        float top = -INFINITY;
-        int top_at = 0x7fffffff;
+        // ---- the node's row: its logits, scaled, in shared memory; their maximum
+        const long long r0 = (s0 + node) * a.ld + v0;
+        float m = -INFINITY;
+        int m_at = 0x7fffffff;
         bool odd = false;                            // NaN
-        for (int i = tid; i < mine; i += kThreads) {
-            float x = logit<DT>(a.logits, r0 + i);
-            odd |= x != x;
-            if (greedy && x > top) top_at = v0 + i;
-            x = __fmul_rn(x, inv_heat);
-            w[i] = x;
-            top = fmaxf(top, x);
-        }
-        if (odd) top = INFINITY;
+        constexpr int kSize = DT == WQ4_FP32 ? 4 : 2;
+        const bool vec = (reinterpret_cast<uintptr_t>(a.logits) + r0 * kSize) % 16 == 0;
+        int done = 0;
+        if (vec) {
+            constexpr int kBatch = DT == WQ4_FP32 ? 2 : 4;
+            for (int i0 = 0; i0 + 8 <= mine; i0 += kThreads * 8 * kBatch) {
+                uint4 lo[kBatch], hi[kBatch];
 #pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const float o = __shfl_xor_sync(0xffffffffu, top, d);
-            const int at = __shfl_xor_sync(0xffffffffu, top_at, d);
-            if (o > top || (o == top && at < top_at)) top_at = at;
-            top = fmaxf(top, o);
+                for (int k = 0; k < kBatch; ++k) {
+                    const int i = i0 + (k * kThreads + tid) * 8;
+                    if (i + 8 <= mine) load8<DT>(a.logits, r0 + i, lo[k], hi[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int i = i0 + (k * kThreads + tid) * 8;
+                    if (i + 8 > mine) break;
+                    float x[8];
+                    values8<DT>(lo[k], hi[k], x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        odd |= x[e] != x[e];
+                        if (greedy && x[e] > m) m_at = v0 + i + e;
+                        x[e] = __fmul_rn(x[e], inv_heat);
+                        m = fmaxf(m, x[e]);
+                    }
+                    w4[i / 4] = make_float4(x[0], x[1], x[2], x[3]);
+                    w4[i / 4 + 1] = make_float4(x[4], x[5], x[6], x[7]);
+                }
+            }
+            done = mine & ~7;
         }
-        if (lane == 0) sh.top[warp] = top, sh.top_at[warp] = top_at;
+        constexpr int kSingles = 8;
+        for (int i0 = done; i0 < mine; i0 += kThreads * kSingles) {
+            float x[kSingles];
+#pragma unroll
+            for (int k = 0; k < kSingles; ++k) {
+                const int i = i0 + k * kThreads + tid;
+                x[k] = i < mine ? value1<DT>(a.logits, r0 + i) : -INFINITY;
+            }
+#pragma unroll
+            for (int k = 0; k < kSingles; ++k) {
+                const int i = i0 + k * kThreads + tid;
+                odd |= x[k] != x[k];
+                if (greedy && x[k] > m) m_at = v0 + i;
+                x[k] = __fmul_rn(x[k], inv_heat);
+                m = fmaxf(m, x[k]);
+                if (i < mine) w[i] = x[k];
+            }
+        }
+        if (odd) m = INFINITY;
+        next_draft();
+        largest(m, m_at, 16);
+        if (lane == 0) sh.top[warp] = m, sh.top_at[warp] = m_at;
         __syncthreads();
-        top = sh.top[0], top_at = sh.top_at[0];
-        for (int i = 1; i < kWarps; ++i) {
-            if (sh.top[i] > top || (sh.top[i] == top && sh.top_at[i] < top_at)) top_at = sh.top_at[i];
-            top = fmaxf(top, sh.top[i]);
+        m = sh.top[lane % kWarps], m_at = sh.top_at[lane % kWarps];
+        largest(m, m_at, kWarps / 2);
+        // ---- their sum, against the CTA's maximum. It decides on the first draft alone, whose random number is as near to the border
+        // as this sum is off (2^-22) once in millions.
+        float s = 0.f;
+        if (!greedy && j < n && !isinf(m)) {
+            const float to2 = 1.44269504f, by = -m * to2;
+            float s2 = 0.f;
+            for (int i = tid; i < mine / 4; i += kThreads) {
+                const float4 x = w4[i];
+                s += exp2_fast(fmaf(x.x, to2, by)) + exp2_fast(fmaf(x.y, to2, by));
+                s2 += exp2_fast(fmaf(x.z, to2, by)) + exp2_fast(fmaf(x.w, to2, by));
+            }
+            const int i = (mine & ~3) + tid;
+            if (i < mine) s += exp2_fast(fmaf(w[i], to2, by));
+            s += s2;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (lane == 0) sh.sum[warp] = s;
+            __syncthreads();
+            s = sh.sum[lane % kWarps];
+#pragma unroll
+            for (int d = kWarps / 2; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
         }
-        int was = exchange(Part{top, __int_as_float(top_at), 0.f, 0});
-        top = -INFINITY, top_at = 0x7fffffff;
-        for (int i = 0; i < C; ++i) {
-            const Part& p = sh.part[was][i];
-            if (p.s > top || (p.s == top && __float_as_int(p.c) < top_at)) top_at = __float_as_int(p.c);
-            top = fmaxf(top, p.s);
-        }
+        was = exchange(Part{m, greedy ? __int_as_float(m_at) : s, j < n && here(draft) ? w[draft - v0] : -INFINITY, 0.f});
+        const Part told = sh.part[was][lane & (C - 1)];
+        float draft_x = told.c;
+        top = told.a, top_at = __float_as_int(told.b);
+        largest(top, top_at, kMaxCluster / 2);
+#pragma unroll
+        for (int d = kMaxCluster / 2; d; d >>= 1) draft_x = fmaxf(draft_x, __shfl_xor_sync(0xffffffffu, draft_x, d));
         if (isinf(top)) {                            // (either way; NaN as +inf)
             fine = false;
             break;
         }
-        Sum part{0.f, 0.f};
-        for (int i = tid; i < mine; i += kThreads) {
-            const float e = greedy ? (v0 + i == top_at ? 1.f : 0.f) : expf(__fsub_rn(w[i], top));
-            w[i] = e;
-            part.add(e);
+        // ---- the first draft
+        if (j < n) {
+            float draft_w = draft == top_at ? 1.f : 0.f, z = 1.f;
+            if (!greedy) {
+                draft_w = expf(__fsub_rn(draft_x, top));
+                z = lane < C ? told.b * expf(__fsub_rn(told.a, top)) : 0.f;
+#pragma unroll
+                for (int d = kMaxCluster / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+                z = __shfl_sync(0xffffffffu, z, 0);
+            }
+            if (keeps(draft_w, z)) {
+                if (rank == 0 && tid == 0) path[kept] = j;
+                ++kept;
+                node = j;
+                __syncthreads();                     // (the logits, and sh.top, are written again)
+                continue;
+            }
         }
-        next_draft();
-        part = cta_sum(part);
-        was = exchange(Part{part.s, part.c, draft_here(), 0});
-        z = take(was);
-        // ---- its children
+        // ---- the weights themselves, and their sum
+        Sum all = weigh(nullptr, true, [&](int i, float x, float) { return greedy ? (v0 + i == top_at ? 1.f : 0.f) : expf(__fsub_rn(x, top)); });
+        was = exchange(Part{all.s, all.c, -1.f, 0.f});
+        if (j >= n) break;
+        // ---- what each draft that is not kept leaves of them
         bool moved = false;
-        while (j < n) {
-            const float q = a.draft_probs ? a.draft_probs[(s0 + node) * a.ldp + draft] : 1.f;
-            if (static_cast<double>(a.uniforms[s0 + j]) * static_cast<double>(q) * z < static_cast<double>(draft_w)) {
+        for (;;) {
+            inv = reciprocal(sum_of(was));
+            q_row = a.draft_probs ? a.draft_probs + (s0 + node) * a.ldp + v0 : nullptr;
+            tried = draft - v0;
+            all = weigh(q_row, false, left);
+            next_draft();
+            const int at = j < n && here(draft) ? static_cast<int>(draft - v0) : -1;
+            was = exchange(Part{all.s, all.c, at < 0 ? -1.f : left(at, w[at], q_row ? q_row[at] : 0.f), 0.f});
+            const bool some = sum_of(was).s > 0.f;
+            if (!some) {                             // nothing is left: the weights stay
+                all = weigh(nullptr, false, [](int, float x, float) { return x; });
+                was = exchange(Part{all.s, all.c, at < 0 ? -1.f : w[at], 0.f});
+            }
+            if (j >= n) {
+                pending = some;                      // (the search below takes what is left from the weights)
+                break;
+            }
+            if (some) {
+                weigh(q_row, true, left);
+                __syncthreads();
+            }
+            float draft_w = -1.f;
+            for (int i = 0; i < C; ++i) draft_w = fmaxf(draft_w, sh.part[was][i].c);
+            const Sum z = sum_of(was);
+            if (keeps(draft_w, __fadd_rn(z.s, z.c))) {
                 if (rank == 0 && tid == 0) path[kept] = j;
                 ++kept;
                 node = j;
                 moved = true;
+                __syncthreads();
                 break;
             }
-            // what the draft leaves of the target
-            const float inv = static_cast<float>(1.0 / z);
-            const float* q_row = a.draft_probs + (s0 + node) * a.ldp + v0;
-            Sum left{0.f, 0.f};
-            if (a.draft_probs) {
-                for (int i = tid; i < mine; i += kThreads) left.add(fmaxf(__fsub_rn(__fmul_rn(w[i], inv), q_row[i]), 0.f));
-            } else {
-                for (int i = tid; i < mine; i += kThreads) left.add(v0 + i == draft ? 0.f : w[i]);
-            }
-            left = cta_sum(left);
-            const long long tried = draft;
-            next_draft();
-            // the next draft's weight, should this step's count
-            float next_w = -1.f;
-            const long long at = draft - v0;
-            if (j < n && at >= 0 && at < mine)
-                next_w = a.draft_probs ? fmaxf(__fsub_rn(__fmul_rn(w[at], inv), q_row[at]), 0.f) : draft == tried ? 0.f : w[at];
-            const float kept_w = draft_here();
-            __syncthreads();
-            was = exchange(Part{left.s, left.c, next_w, __float_as_int(kept_w)});
-            const double z_left = take(was);
-            if (z_left > 0) {
-                if (a.draft_probs) {
-                    for (int i = tid; i < mine; i += kThreads) w[i] = fmaxf(__fsub_rn(__fmul_rn(w[i], inv), q_row[i]), 0.f);
-                } else if (tid == 0 && tried >= v0 && tried < v0 + mine) {
-                    w[tried - v0] = 0.f;
-                }
-                z = z_left;
-            } else {                                 // nothing is left: the weights stay
-                draft_w = -1.f;
-                for (int i = 0; i < C; ++i) draft_w = fmaxf(draft_w, __int_as_float(sh.part[was][i].pad));
-            }
-            __syncthreads();
         }
         if (!moved) break;
-        __syncthreads();                             // (the weights are overwritten)
     }
     if (rank == 0) {
         for (int i = kept + tid; i < max(1, a.max_tokens - 1); i += kThreads) path[i] = -1;
@@ -276,67 +430,72 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
         if (rank == 0 && tid == 0) a.next_tokens[b] = -1;
         return;
     }
-    // ---- the next token: sums of blocks of 1024 weights, in pieces of 32, each lane's read askew so that the lanes lie in
-    // different banks
-    auto piece_sum = [&](int block) {
-        Sum s{0.f, 0.f};
-        const int from = block * kBlock + lane * 32;
-        for (int i = 0; i < 32; ++i) {
-            const int at = from + ((i + lane) & 31);
-            s.add(at < mine ? w[at] : 0.f);
-        }
-        return s;
-    };
-    const int blocks = (mine + kBlock - 1) / kBlock;
-    for (int k = warp; k < blocks; k += kWarps) {
-        const Sum s = warp_sum(piece_sum(k));
-        if (lane == 0) sh.block[k] = s.value();
-    }
-    __syncthreads();
-    double here = 0;
-    for (int k = 0; k < blocks; ++k) here += sh.block[k];
-    const int was = exchange(Part{static_cast<float>(here), static_cast<float>(here - static_cast<double>(static_cast<float>(here))), 0.f, 0});
-    double all = 0;
-    for (int i = 0; i < C; ++i) all += static_cast<double>(sh.part[was][i].s) + static_cast<double>(sh.part[was][i].c);
-    const double aim = static_cast<double>(a.final_uniforms[b]) * all;
-    double upto = 0;
-    int owner = -1, last = 0;
-    for (int i = 0; i < C; ++i) {
-        const double s = static_cast<double>(sh.part[was][i].s) + static_cast<double>(sh.part[was][i].c);
-        if (s > 0) last = i;
-        if (owner < 0 && upto + s > aim) owner = i;
-        if (owner < 0) upto += s;
-    }
-    const bool past = owner < 0;                     // (u z rounded up to all of z): the last token with a weight
-    if (past) owner = last;
-    if (owner != rank || warp != 0) return;
-    int k = -1, last_k = 0;
-    for (int i = 0; i < blocks; ++i) {
-        const double s = sh.block[i];
-        if (s > 0) last_k = i;
-        if (k < 0 && !past && upto + s > aim) k = i;
-        if (k < 0) upto += s;
-    }
-    // (where the blocks' sums and the CTA's do not agree to the last bit, the last one with a weight)
-    const bool end = k < 0;
-    if (end) k = last_k;
-    // of the block's 32 pieces, then of the piece's 32 weights, the first whose running sum exceeds the aim
-    const double mine_of_32 = piece_sum(k).value();
-    auto pick = [&](double x) {                      // the lane
+    // ---- the next token: the CTA, its block of 1024, of the block's 32 pieces and of the piece's 32 weights the first at which the
+    // running sum exceeds the aim
+    if (warp != 0) return;
+    auto first_over = [&](double x, double aim, double& upto, bool any) {    // the lane; upto: the sum ahead of it (any: the last with a weight)
         double run = x;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const double y = __shfl_up_sync(0xffffffffu, run, d);
             if (lane >= d) run += y;
         }
-        const unsigned over = __ballot_sync(0xffffffffu, upto + run > aim), some = __ballot_sync(0xffffffffu, x > 0);
-        const int at = !end && over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
-        if (at > 0) upto += __shfl_sync(0xffffffffu, run, at - 1);
+        const unsigned over = any ? 0u : __ballot_sync(0xffffffffu, upto + run > aim), some = __ballot_sync(0xffffffffu, x > 0);
+        const int at = over ? __ffs(over) - 1 : any && some ? 31 - __clz(some) : -1;
+        if (at != 0) upto += __shfl_sync(0xffffffffu, run, at < 0 ? 31 : at - 1);
         return at;
     };
-    const int piece = pick(mine_of_32);
+    const double part = lane < C ? Sum{sh.part[was][lane].a, sh.part[was][lane].b}.value() : 0.0;
+    double z = part, upto = 0;
+#pragma unroll
+    for (int d = kMaxCluster / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+    const double aim = static_cast<double>(a.final_uniforms[b]) * __shfl_sync(0xffffffffu, z, 0);
+    int owner = first_over(part, aim, upto, false);
+    bool end = owner < 0;                            // (u z rounded up to all of z): the last token with a weight
+    if (end) owner = first_over(part, aim, upto, true);
+    if (owner != rank) return;
+    int k = -1;
+    for (int at = 0; at < blocks && k < 0 && !end; at += 32) {
+        const double x = at + lane < blocks ? sh.block[at + lane].value() : 0.0;
+        const int f = first_over(x, aim, upto, false);
+        if (f >= 0) k = at + f;
+    }
+    // (where the blocks' sums and the CTA's do not agree to the last bit, the last one with a weight)
+    if (k < 0) {
+        end = true;
+        for (int at = 0; at < blocks; at += 32) {
+            const unsigned some = __ballot_sync(0xffffffffu, at + lane < blocks && sh.block[at + lane].s > 0.f);
+            if (some) k = at + 31 - __clz(some);
+        }
+        k = max(k, 0);
+    }
+    auto weight = [&](int at) { return at >= mine ? 0.f : pending ? left(at, w[at], q_row ? q_row[at] : 0.f) : w[at]; };
+    auto pick = [&](double x) {                      // the lane
+        double before = upto;
+        int at = end ? -1 : first_over(x, aim, before, false);
+        if (at < 0) {
+            end = true;
+            at = max(0, first_over(x, aim, before, true));
+        }
+        upto = before;
+        return at;
+    };
+    Sum mine_of_32{0.f, 0.f};
+    if (pending && q_row) {                          // (a row in global memory: read along it, a piece at a time)
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = weight(k * kBlock + 32 * i + lane);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const Sum s = warp_sum(Sum{x[i], 0.f});
+            if (lane == i) mine_of_32 = s;
+        }
+    } else {                                         // each lane's reads askew, so that the lanes lie in different banks
+        for (int i = 0; i < 32; ++i) mine_of_32.add(weight(k * kBlock + lane * 32 + ((i + lane) & 31)));
+    }
+    const int piece = pick(mine_of_32.value());
     const int from = k * kBlock + piece * 32;
-    const int at = pick(from + lane < mine ? static_cast<double>(w[from + lane]) : 0.0);
+    const int at = pick(static_cast<double>(weight(from + lane)));
     if (lane == 0) a.next_tokens[b] = v0 + from + at;
 }
 
@@ -378,7 +537,8 @@ extern "C" int wq4_verify_drafts(const void* logits, long long ld, const long lo
     if (const int rc = runtime(&rt)) return rc;
     VerifyArgs a{logits, tokens, parents, starts, draft_probs, temperature, uniforms, final_uniforms, accepted, path, next_tokens,
                  ld, ldp, B, T, max_tokens, V, ld_path, 1, 0, rt.status};
-    while (a.cluster < kMaxCluster && V > 16 * kBlock * a.cluster) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && (V > 16 * kBlock * a.cluster || (2LL * a.cluster * B <= rt.sm_count && V > 2 * kBlock * a.cluster)))
+        a.cluster *= 2;
     a.share = ((V + a.cluster - 1) / a.cluster + kBlock - 1) / kBlock * kBlock;
     if (rt.trace) std::fprintf(stderr, "wq4: verify_drafts B=%d tokens=%d V=%d cluster=%d\n", B, max_tokens, V, a.cluster);
     if (dtype == WQ4_BF16) return go_verify<WQ4_BF16>(rt, a, stream);
