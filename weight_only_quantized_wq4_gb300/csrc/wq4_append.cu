@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "wq4_cache.cuh"
@@ -29,7 +30,7 @@ struct AppendArgs {
     long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs;
     int T, Hq, Hk, D, R;
     int per_head;                       // threads of a head, a power of two
-    int tokens;                         // of a CTA
+    int beside, steps;                  // tokens of a CTA: beside each other, one after the other
     float eps, one_over_D;
     unsigned int* status;
 };
@@ -61,132 +62,176 @@ __device__ __forceinline__ float2 turned(long long p, unsigned long long F, floa
     return cs;
 }
 
-constexpr int kAppendMaxD = 1024;
+constexpr int kAppendMaxD = 1024, kAppendThreads = 384;
 
+// Two fp32 to an instruction.
+__device__ __forceinline__ uint64_t both(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& x, uint64_t (&v)[4]) {
+    float f[8];
+    wq4::unpack8<BF16>(x, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = both(f[2 * j], f[2 * j + 1]);
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm("mov.b64 {%0, %1}, %2;" : "=f"(f[2 * j]), "=f"(f[2 * j + 1]) : "l"(v[j]));
+    return wq4::pack8<BF16>(f);
+}
+
+// A thread has two vectors of one head and goes through `steps` tokens with it, so that the head's place, its weights' loads and what
+// depends on them are found once; the angles of all the CTA's tokens and their places in the cache are found first, by
+// all its threads, while the first token's loads are under way.
 // ROTATE: 0 none, 1 pairs (i, i + R / 2), 2 pairs (2 i, 2 i + 1).
 template <bool BF16, int ROTATE, bool NORM>
-__global__ void __launch_bounds__(1024) append_kernel(const AppendArgs a) {
-    extern __shared__ float4 turns[];                // [tokens][R / 2] (cos, sin)
-    float2* const turn = reinterpret_cast<float2*>(turns);
+__global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const AppendArgs a) {
+    // [token] a slot, -1 where there is none to write; then [token][4][lane] cos and sin, each lane's 16 bytes beside the next one's:
+    // two of a lane's pairs (cos, cos, sin, sin) with ROTATE 1, (cos, sin) of each with 2
+    extern __shared__ float4 shared4[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int heads = a.Hq + 2 * a.Hk, D = a.D, P = a.per_head;
-    const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
-    const int tokens = static_cast<int>(min(static_cast<long long>(a.tokens), a.T - t0));
-    const int lane = threadIdx.x % P, groups = blockDim.x / P;
+    const int lane = threadIdx.x % P, group = threadIdx.x / P, groups = blockDim.x / P;
+    const int beside = a.beside, tok0 = beside > 1 ? group / heads : 0;          // tokens beside each other, this thread's first
+    const long long t0 = static_cast<long long>(blockIdx.x) * (beside * a.steps);
+    const int most = beside * a.steps, tokens = static_cast<int>(min(static_cast<long long>(most), a.T - t0));
+    int* const slots = reinterpret_cast<int*>(shared4);
+    float4* const turns = shared4 + (most + 3) / 4;
+    const int r16 = a.R / 16;                        // lanes whose features are all rotated
     // this thread's two vectors of a head
     int c0 = lane * 16, c1 = c0 + 8;
-    bool rot = ROTATE == 2 ? c0 < a.R : false, rot1 = ROTATE == 2 ? c1 < a.R : false;
-    if (ROTATE == 1) {
-        if (lane < a.R / 16) c0 = lane * 8, c1 = c0 + a.R / 2, rot = true;
-    }
-    const bool in = c0 < D;
-    const int all = tokens * heads;
-    // One head of one token: where it lies, what is read of it.
-    struct Item {
-        long long t, slot;
-        int tok, head, hk;
-        bool live, is_q, is_v;
-        uint4 x0, x1;
-    };
-    auto load = [&](int item) {
-        Item m;
-        m.tok = item / heads, m.head = item - m.tok * heads;
-        m.live = in && item < all;
-        m.t = t0 + m.tok;
-        m.is_q = m.head < a.Hq, m.is_v = m.head >= a.Hq + a.Hk;
-        m.hk = m.is_v ? m.head - a.Hq - a.Hk : m.head - a.Hq;
-        m.x0 = m.x1 = make_uint4(0, 0, 0, 0);
-        m.slot = -1;
-        if (m.live) {
-            const uint16_t* p = m.is_q ? a.q + m.t * a.q_ts + m.head * a.q_hs : m.is_v ? a.v + m.t * a.v_ts + m.hk * a.v_hs
-                                                                                   : a.k + m.t * a.k_ts + m.hk * a.k_hs;
-            m.x0 = *reinterpret_cast<const uint4*>(p + c0);
-            m.x1 = *reinterpret_cast<const uint4*>(p + c1);
-            if (!m.is_q) m.slot = a.slots[m.t];
+    const bool rot = ROTATE != 0 && lane < r16;
+    if (ROTATE == 1 && rot) c0 = lane * 8, c1 = c0 + a.R / 2;
+    int head = group - tok0 * heads;
+    const int last = beside > 1 ? head + 1 : (heads + groups - 1) / groups * groups;   // (all of a warp's lanes take as many rounds)
+    bool found = false;
+    for (; head < last; head += groups) {
+        const bool in = c0 < D && head < heads && tok0 < beside;
+        const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hk;
+        const int hk = is_v ? head - a.Hq - a.Hk : head - a.Hq;
+        const long long ts = is_q ? a.q_ts : is_v ? a.v_ts : a.k_ts;
+        const uint16_t* p = (is_q ? a.q + head * a.q_hs : is_v ? a.v + hk * a.v_hs : a.k + hk * a.k_hs) + (t0 + tok0) * ts;
+        const long long step_in = beside * ts;
+        int left = in ? tokens - tok0 : 0;           // of this thread's tokens, counted in the CTA's
+        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+        if (left > 0) {
+            x0 = *reinterpret_cast<const uint4*>(p + c0);
+            x1 = *reinterpret_cast<const uint4*>(p + c1);
         }
-        return m;
-    };
-    auto finish = [&](Item& m) {
-        float v0[8], v1[8];
-        unpack8<BF16>(m.x0, v0);
-        unpack8<BF16>(m.x1, v1);
-        float ss = 0.f;
-        if constexpr (NORM) {                        // (every lane of the warp, whatever its head is)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(v0[j], v0[j], fmaf(v1[j], v1[j], ss));
-            for (int d = P / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        }
-        if (!m.live) return;
-        if (!m.is_v) {
-            if constexpr (NORM) {
-                const float r = rsqrtf(fmaf(ss, a.one_over_D, a.eps));
-                float w0[8], w1[8];
-                const uint16_t* w = m.is_q ? a.q_weight : a.k_weight;
-                unpack8<BF16>(*reinterpret_cast<const uint4*>(w + c0), w0);
-                unpack8<BF16>(*reinterpret_cast<const uint4*>(w + c1), w1);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v0[j] *= r * w0[j], v1[j] *= r * w1[j];
-            }
-            if (ROTATE == 1 && rot) {
-                const float4* cs = reinterpret_cast<const float4*>(turn + m.tok * (a.R / 2) + c0);
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float4 c = cs[j / 2];
-                    const float x = v0[j], y = v1[j], x2 = v0[j + 1], y2 = v1[j + 1];
-                    v0[j] = x * c.x - y * c.y;
-                    v1[j] = y * c.x + x * c.y;
-                    v0[j + 1] = x2 * c.z - y2 * c.w;
-                    v1[j + 1] = y2 * c.z + x2 * c.w;
+        if (!found) {
+            found = true;
+            if constexpr (ROTATE != 0) {
+                const int half = a.R / 2;
+                float* const t = reinterpret_cast<float*>(turns);
+                for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
+                    const int tok = i / half, pair = i - tok * half;
+                    const float f = a.inv_freq[pair];
+                    const float2 cs = turned(a.positions[t0 + tok], turns_of(f), f);
+                    float* at = t + (((tok * 4 + (pair >> 1 & 3)) * r16 + (pair >> 3)) << 2);
+                    at[ROTATE == 1 ? pair & 1 : 2 * (pair & 1)] = cs.x;
+                    at[ROTATE == 1 ? 2 + (pair & 1) : 2 * (pair & 1) + 1] = cs.y;
                 }
             }
-            if (ROTATE == 2) {
-                auto rotate = [&](float(&v)[8], const float2* cs) {
+            for (int i = threadIdx.x; i < tokens; i += blockDim.x) {
+                const long long slot = a.slots[t0 + i];
+                const bool past = slot >= static_cast<long long>(a.cache.pages) * a.cache.page_size;
+                if (past) atomicOr(a.status, kStatusBadIndex);
+                slots[i] = slot < 0 || past ? -1 : static_cast<int>(slot);       // (a negative one is a padded token)
+            }
+            __syncthreads();
+        }
+        uint16_t* q_out = a.q_out + (t0 + tok0) * a.qo_ts + head * a.qo_hs;      // (of a query head)
+        for (int tok = tok0; tok < most; tok += beside, left -= beside) {
+            if (tok != tok0 && left > 0) {
+                p += step_in;
+                x0 = *reinterpret_cast<const uint4*>(p + c0);
+                x1 = *reinterpret_cast<const uint4*>(p + c1);
+            }
+            if (!is_v || NORM) {                     // (with a norm: every lane of the warp, whatever its head is)
+                uint64_t v0[4], v1[4];
+                unpack8<BF16>(x0, v0);
+                unpack8<BF16>(x1, v1);
+                if constexpr (NORM) {
+                    uint64_t s2 = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = v[2 * j], y = v[2 * j + 1];
-                        v[2 * j] = x * cs[j].x - y * cs[j].y;
-                        v[2 * j + 1] = y * cs[j].x + x * cs[j].y;
+                    for (int j = 0; j < 4; ++j) s2 = fma2(v0[j], v0[j], fma2(v1[j], v1[j], s2));
+                    float ss, odd;
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(ss), "=f"(odd) : "l"(s2));
+                    ss += odd;
+                    for (int d = P / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+                    const float r = rsqrtf(fmaf(ss, a.one_over_D, a.eps));
+                    const uint64_t rr = both(r, r);
+                    if (left > 0 && !is_v) {
+                        const uint16_t* weight = is_q ? a.q_weight : a.k_weight;     // (in L1 after the first token)
+                        uint64_t w[4];
+                        unpack8<BF16>(*reinterpret_cast<const uint4*>(weight + c0), w);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v0[j] = mul2(mul2(v0[j], rr), w[j]);
+                        unpack8<BF16>(*reinterpret_cast<const uint4*>(weight + c1), w);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v1[j] = mul2(mul2(v1[j], rr), w[j]);
                     }
-                };
-                const float2* cs = turn + m.tok * (a.R / 2) + c0 / 2;
-                if (rot) rotate(v0, cs);
-                if (rot1) rotate(v1, cs + 4);
+                }
+                if (ROTATE != 0 && rot && left > 0) {
+                    const float4* cs = turns + tok * 4 * r16 + lane;
+                    if constexpr (ROTATE == 1) {
+                        const uint64_t minus = both(-1.f, -1.f);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 t = cs[j * r16];
+                            const uint64_t c = both(t.x, t.y), s = both(t.z, t.w), x = v0[j], y = v1[j];
+                            v0[j] = fma2(mul2(y, minus), s, mul2(x, c));
+                            v1[j] = fma2(x, s, mul2(y, c));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 t = cs[j * r16];                 // of pairs 2 j and 2 j + 1 of the lane's eight
+                            const float c[2] = {t.x, t.z}, s[2] = {t.y, t.w};
+                            uint64_t(&v)[4] = j < 2 ? v0 : v1;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float x, y;
+                                asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v[2 * (j & 1) + e]));
+                                v[2 * (j & 1) + e] = both(x * c[e] - y * s[e], y * c[e] + x * s[e]);
+                            }
+                        }
+                    }
+                }
+                if (!is_v) {
+                    x0 = pack8<BF16>(v0);
+                    x1 = pack8<BF16>(v1);
+                }
             }
-            m.x0 = pack8<BF16>(v0);
-            m.x1 = pack8<BF16>(v1);
-        }
-        uint16_t* out = nullptr;
-        if (m.is_q) {
-            out = a.q_out + m.t * a.qo_ts + m.head * a.qo_hs;
-        } else if (m.slot >= 0) {                    // (a negative one is a padded token)
-            if (m.slot < static_cast<long long>(a.cache.pages) * a.cache.page_size) {
-                out = m.is_v ? a.cache.v_at(static_cast<unsigned>(m.slot), m.hk) : a.cache.k_at(static_cast<unsigned>(m.slot), m.hk);
-            } else {
-                atomicOr(a.status, kStatusBadIndex);
+            if (left > 0) {
+                uint16_t* out = q_out;
+                if (!is_q) {
+                    const int slot = slots[tok];
+                    out = slot < 0 ? nullptr : is_v ? a.cache.v_at(slot, hk) : a.cache.k_at(slot, hk);
+                }
+                if (out) {
+                    *reinterpret_cast<uint4*>(out + c0) = x0;
+                    *reinterpret_cast<uint4*>(out + c1) = x1;
+                }
             }
+            q_out += beside * a.qo_ts;
         }
-        if (out) {
-            *reinterpret_cast<uint4*>(out + c0) = m.x0;
-            *reinterpret_cast<uint4*>(out + c1) = m.x1;
-        }
-    };
-    int item = threadIdx.x / P;
-    Item next = load(item);                          // (under way while the angles are found)
-    if constexpr (ROTATE != 0) {
-        const int half = a.R / 2;
-        for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
-            const int tok = i / half, pair = i - tok * half;
-            const float f = a.inv_freq[pair];
-            turn[i] = turned(a.positions[t0 + tok], turns_of(f), f);
-        }
-        __syncthreads();
-    }
-    for (const int rounds = (all + groups - 1) / groups * groups; item < rounds;) {
-        Item now = next;
-        item += groups;
-        if (item < rounds) next = load(item);
-        finish(now);
     }
 }
 
@@ -261,11 +306,16 @@ int go_append(const Runtime& rt, AppendArgs& a, bool vec, wq4_stream_t st) {
     }
     a.per_head = 1;
     while (a.per_head < a.D / 16) a.per_head *= 2;
+    // A CTA takes one token's heads side by side, as many tokens as its threads hold where the heads are few; and, with more than
+    // a few waves of CTAs, up to four tokens one after the other.
     const int all = heads * a.per_head;              // threads of a token
-    a.tokens = 1;
-    const int threads = all > 512 ? 512 : (all + 31) / 32 * 32;
-    const unsigned grid = static_cast<unsigned>((a.T + a.tokens - 1) / a.tokens);
-    return launch(rt, append_kernel<BF16, ROTATE, NORM>, dim3(grid), threads, ROTATE ? a.tokens * (a.R / 2) * 8 : 0, 1, st, a);
+    a.beside = all >= kAppendThreads ? 1 : std::max(1, std::min(256 / all, a.T));
+    const int threads = all >= kAppendThreads ? kAppendThreads : (all * a.beside + 31) / 32 * 32;
+    const int waves = static_cast<int>(a.T / (static_cast<long long>(a.beside) * rt.sm_count * 4));
+    a.steps = std::max(1, std::min(4, waves));
+    const int tokens = a.beside * a.steps;
+    const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.T) + tokens - 1) / tokens);
+    return launch(rt, append_kernel<BF16, ROTATE, NORM>, dim3(grid), threads, (tokens + 3) / 4 * 16 + (ROTATE ? tokens * a.R * 4 : 0), 1, st, a);
 }
 
 template <bool BF16>

@@ -18,8 +18,9 @@ struct AttnArgs {
     long long q_ts, q_hs, o_ts, o_hs;
     int ld_table, table_width, mask_words;
     int B, T, max_tokens, Hq, Hk, G, D;
+    int max_rows;                       // max_tokens G, or as many as matter
     int box, copies;                    // places of one copy; copies of a box's panels
-    int grid, least;                    // CTAs; the fewest tiles worth a CTA
+    int grid;                           // CTAs
     float scale_log2;
     int* counters;                      // [grid] parts that have come, of the unit whose first part is the CTA's
     float2* stats;                      // [2 grid][rows] (maximum, sum)
@@ -76,45 +77,60 @@ struct Walk {
     __device__ bool begin(Scan& sc, int tid, int threads) {
         const int lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
         int n, c;
-        unsigned long long mine = 0, own = 0;
+        auto scan = [&](unsigned long long x) {      // up to and with this lane's
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            return x;
+        };
+        // the sum of what each thread loads of all sequences; with no more of those than threads, their running sum too
+        unsigned long long own = 0, mine = 0;
         for (int i = tid; i < a.B; i += threads) {
             own = load(i, n, c);
             mine += own;
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-        if (lane == 0) sc.sum[warp] = mine;
+        const unsigned long long upto = scan(mine);
+        if (lane == 31) sc.sum[warp] = upto;
         __syncthreads();
-        unsigned long long total = 0;
-        for (int i = 0; i < warps; ++i) total += sc.sum[i];
+        unsigned long long total = 0, ahead = 0;
+        for (int i = 0; i < warps; ++i) {
+            if (i == warp) ahead = total;
+            total += sc.sum[i];
+        }
         if (total > 0x7fffffffull) {
             if (tid == 0) atomicOr(a.status, kStatusBadIndex);
             return false;
         }
         cta = blockIdx.x;
-        chunk = max(static_cast<unsigned>((total + a.grid - 1) / a.grid), static_cast<unsigned>(a.least));
+        chunk = max((static_cast<unsigned>(total) + a.grid - 1) / a.grid, 1u);
         const unsigned long long lo = static_cast<unsigned long long>(cta) * chunk;
         if (lo >= total) return false;
-        unsigned long long carry = 0;
-        for (int at = 0; at < a.B && carry <= lo; at += threads) {
-            const unsigned long long x = a.B <= threads ? own : at + tid < a.B ? load(at + tid, n, c) : 0;
-            unsigned long long up = x;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned long long y = __shfl_up_sync(0xffffffffu, up, d);
-                if (lane >= d) up += y;
+        if (a.B <= threads) {
+            if (ahead + upto - own <= lo && lo < ahead + upto) {
+                sc.b = tid;
+                sc.before = ahead + upto - own;
             }
-            if (lane == 31) sc.part[warp] = up;
-            __syncthreads();
-            unsigned long long ahead = carry;
-            for (int i = 0; i < warp; ++i) ahead += sc.part[i];
-            if (ahead + up - x <= lo && lo < ahead + up) {
-                sc.b = at + tid;
-                sc.before = ahead + up - x;
+        } else {
+            unsigned long long carry = 0;
+            for (int at = 0; at < a.B && carry <= lo; at += threads) {
+                const unsigned long long x = at + tid < a.B ? load(at + tid, n, c) : 0, up = scan(x);
+                if (lane == 31) sc.part[warp] = up;
+                __syncthreads();
+                unsigned long long before = carry;
+                for (int i = 0; i < warps; ++i) {
+                    if (i < warp) before += sc.part[i];
+                    carry += sc.part[i];
+                }
+                if (before + up - x <= lo && lo < before + up) {
+                    sc.b = at + tid;
+                    sc.before = before + up - x;
+                }
+                __syncthreads();
             }
-            for (int i = 0; i < warps; ++i) carry += sc.part[i];
-            __syncthreads();
         }
+        __syncthreads();
         pos = static_cast<unsigned>(lo);
         end = static_cast<unsigned>(min(total, lo + chunk));
         base = static_cast<unsigned>(sc.before);

@@ -10,6 +10,8 @@
 // long as nothing overflows), so that O is rarely scaled.
 //
 // Work is cut as in wq4_tree_attention.cu: equal shares of all the units' tiles, and the CTA that finishes last joins a unit.
+#include <new>
+
 #include "wq4_attention.cuh"
 
 namespace wq4 {
@@ -18,8 +20,9 @@ namespace {
 constexpr int kTile = 128;              // places of a tile
 constexpr int kLanes = 128;             // rows of a stream's tile
 constexpr int kUnitRows = 2 * kLanes;
-constexpr int kSoftmaxWarp = 4;         // the first of eight; before them: copies, MMAs, two that look at drafted values
-constexpr int kThreads = 32 * (kSoftmaxWarp + 8);
+constexpr int kSoftmaxWarp = 4;         // the first of sixteen; before them: copies, MMAs, two that look at drafted values
+constexpr int kSoftmax = 512;           // their threads
+constexpr int kThreads = 32 * kSoftmaxWarp + kSoftmax;
 constexpr int kMaxSlots = 16;
 constexpr float kSlack = 8.f;           // log2 of what a probability may exceed 1 by
 
@@ -28,20 +31,35 @@ struct Cfg {
     static constexpr int kDp = 64 * NC;
     static constexpr int kSlot = kTile * kDp * 2;            // a tile's keys, or values
     static constexpr int kQ = kLanes * kDp * 2;
-    static constexpr int kHead = 4096;                       // barriers, statistics
+    static constexpr int kHead = 3072;                       // barriers, maxima
     static constexpr int kMaxSmem = 232448;                  // 227 KB
-    static constexpr int kSlots = (kMaxSmem - 1024 - kHead - 2 * kQ) / kSlot < kMaxSlots ? (kMaxSmem - 1024 - kHead - 2 * kQ) / kSlot : kMaxSlots;
-    static constexpr int kSmem = 1024 + kHead + 2 * kQ + kSlots * kSlot;
+    // Ring slots beside one or two streams' Q.
+    __host__ __device__ static constexpr int slots(int q) {
+        const int n = (kMaxSmem - kHead - q * kQ) / kSlot;
+        return n < kMaxSlots ? n : kMaxSlots;
+    }
+    __host__ __device__ static constexpr int smem(int q) { return kHead + q * kQ + slots(q) * kSlot; }
     static constexpr int kO = 2 * kTile;                     // tensor memory: S of both streams, then O of both
-    static constexpr uint32_t kTmemCols = 2 * kTile + 2 * kDp > 256 ? 512 : 256;
+    static constexpr uint32_t kTmemCols = 512;
 };
 
-// Registers: 128 x 88 + 256 x 208 are those of the launch, 384 x 168.
+// Registers: 128 x 64 + 512 x 104 are those of the launch, 640 x 96.
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+__device__ __forceinline__ uint64_t both(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+// Scores of places that are not seen.
+__device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t seen) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        if (!(seen >> c & 1u)) x[c] = 0xff800000u;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -89,38 +107,55 @@ __device__ __forceinline__ uint32_t seen32(const AttnArgs& a, int t, int i, int 
     return ctx | static_cast<uint32_t>(bits << shift);
 }
 
+// A unit as the softmax warps see it: in shared memory, as their registers hold S.
+struct Unit {
+    int more;                                                // whether there is one
+    int b, h, row0, rows, context, count, t0, n, first;      // n: tiles; first: the sequence's first row
+    int pieces, first_cta, part;
+    __device__ __forceinline__ bool two() const volatile { return rows - row0 > kLanes; }
+    __device__ __forceinline__ int part_of(int i) const volatile { return 2 * (first_cta + i) + (i == 0 ? 1 : 0); }
+};
+
 template <bool BF16, int NC>
 __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __grid_constant__ AttnArgs a) {
     using C = Cfg<NC>;
     constexpr int kDp = C::kDp, kPanel = kTile * 128;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t s_base = (smem_u32(smem_raw) + 1023) & ~1023u;
-    uint8_t* base = smem_raw + (s_base - smem_u32(smem_raw));
+    // (nothing else is in shared memory, so that it starts on a swizzle's boundary: checked below)
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t s_base = smem_u32(smem_raw);
+    const int queries = a.max_rows > kLanes ? 2 : 1, slots = C::slots(queries);
+    // the ring and Q first, on 1024-byte boundaries
+    const uint32_t s_q = s_base, s_ring = s_base + queries * C::kQ;
+    uint8_t* const head = smem_raw + queries * C::kQ + slots * C::kSlot;
+    const uint32_t s_head = smem_u32(head);
     // barriers
-    const uint32_t s_full = s_base, s_empty = s_base + 8 * kMaxSlots, s_vok = s_base + 16 * kMaxSlots;
-    const uint32_t s_sfull = s_base + 24 * kMaxSlots, s_pfull = s_sfull + 16, s_ofull = s_sfull + 32, s_qfull = s_sfull + 40,
+    const uint32_t s_full = s_head, s_empty = s_head + 8 * kMaxSlots, s_vok = s_head + 16 * kMaxSlots;
+    const uint32_t s_sfull = s_head + 24 * kMaxSlots, s_pfull = s_sfull + 16, s_ofull = s_sfull + 32, s_qfull = s_sfull + 40,
                    s_drain = s_sfull + 48, s_stall = s_sfull + 56;
-    int* ctl_i = reinterpret_cast<int*>(base + 512);         // [0] abort, [1] last to finish, [2] gave up, [3] tensor memory, [4] values not finite
+    int* ctl_i = reinterpret_cast<int*>(head + 512);         // [0] abort, [1] last to finish, [2] gave up, [3] tensor memory, [4] values not finite
     volatile int* abort_flag = ctl_i;
     volatile int* bad_slot = ctl_i + 8;                      // [slots] a drafted value that is not finite was taken out
-    float2* s_stat = reinterpret_cast<float2*>(base + 1024); // [2][lanes] (maximum, sum)
-    const uint32_t s_q = s_base + C::kHead, s_ring = s_q + 2 * C::kQ;
-    __shared__ Scan scan;
+    Walk* const walk = reinterpret_cast<Walk*>(head + 640);  // (the softmax warps' own)
+    Unit* const units = reinterpret_cast<Unit*>(head + 832); // [2] the unit at hand and the next
+    static_assert(sizeof(Walk) <= 192 && 2 * sizeof(Unit) <= 192, "fit ahead of the maxima");
+    float* s_max = reinterpret_cast<float*>(head + 1024);    // [stream][half of the places][lane]
+    // at times when Q is not there: the schedule's sums, and at a unit's end [stream][half][lane] (maximum, sum)
+    Scan& scan = *reinterpret_cast<Scan*>(smem_raw);
+    float2* s_stat = reinterpret_cast<float2*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < 16; ++i) ctl_i[i] = 0;
-        for (int i = 0; i < C::kSlots; ++i) {
+        for (int i = 0; i < 32; ++i) ctl_i[i] = 0;
+        for (int i = 0; i < slots; ++i) {
             mbar_init(s_full + 8 * i, 1);
             mbar_init(s_empty + 8 * i, 3);           // the MMAs that read it, and the two warps that look at drafted values
             mbar_init(s_vok + 8 * i, 2);
-            bad_slot[i] = 0;
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_sfull + 8 * s, 1);
-            mbar_init(s_pfull + 8 * s, 4);
+            mbar_init(s_pfull + 8 * s, 8);
         }
         mbar_init(s_ofull, 2);
-        mbar_init(s_qfull, 8);
+        mbar_init(s_qfull, 16);
         mbar_init(s_drain, 1);
         mbar_init(s_stall, 1);
         fence_mbar_init();
@@ -138,37 +173,44 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     const uint32_t tmem = static_cast<uint32_t>(ctl_i[3]);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     Walk w(a, kTile, kUnitRows);
-    const bool work = w.begin(scan, tid, kThreads);          // (all threads of the CTA alike)
+    bool work = w.begin(scan, tid, kThreads);                // (all threads of the CTA alike)
+    if (s_base & 1023u) {
+        if (tid == 0) atomicOr(a.status, kStatusTimeout);
+        work = false;
+    }
+    __syncthreads();                                         // (Q comes where the schedule's sums were)
     const WaitCtl ctl{abort_flag, a.status, a.timeout_cycles};
-    Ring ring(C::kSlots);
+    Ring ring(slots);
     // A unit's tiles: lag of the values behind the keys, and whether both streams have rows of their own.
     auto two = [&] { return w.rows - w.row0 > kLanes; };
 
     if (warp < kSoftmaxWarp) {
-        fewer_registers<88>();
+        fewer_registers<64>();
         if (warp == 0) {
             // ------------------------------------------------------------ copies
             const uint64_t pol = policy_evict_first();
-            const int per_box = NC, panel = lane % NC, box = lane / NC;
-            const bool mine = lane < kTile / a.box * per_box;
+            const int panel = lane % NC, box = lane / NC;
+            const bool mine = lane < kTile / a.box * NC;
             bool ok = work;
             while (ok && w.next()) {
                 const int n = w.t1 - w.t0, lag = two() ? 1 : 2;
+                // The page of this lane's places of a tile: looked up a tile ahead of its keys and kept for its values.
+                auto place_of = [&](int tile) { return (w.t0 + tile) * kTile + box * a.box; };
+                auto find = [&](int tile) {
+                    const int place = place_of(tile);
+                    return mine && tile < n && place < w.len ? a.table[static_cast<long long>(w.b) * a.ld_table + place / a.cache.page_size]
+                                                             : a.cache.pages;    // past the last place: outside the tensor, zeros
+                };
+                int ahead = find(0), page[3] = {};           // of tile j + 1; of j, j - 1, j - 2
                 for (int j = 0; j < n + lag && ok; ++j) {
-                    for (int kind = 0; kind < 2 && ok; ++kind) {         // 0: values of j - lag, 1: keys of j
-                        const int tile = kind ? j : j - lag;
-                        if (tile < 0 || tile >= n) continue;
-                        const int place = (w.t0 + tile) * kTile + box * a.box;
-                        int page = a.cache.pages, at = 0;                // past the last place: outside the tensor, zeros
-                        if (mine && place < w.len) {
-                            const int i = place / a.cache.page_size;
-                            page = a.table[static_cast<long long>(w.b) * a.ld_table + i];
-                            at = place - i * a.cache.page_size;
-                            if (page < 0 || page >= a.cache.pages) {
-                                atomicOr(a.status, kStatusBadIndex);
-                                page = a.cache.pages;
-                            }
-                        }
+                    page[2] = page[1], page[1] = page[0], page[0] = ahead;
+                    ahead = find(j + 1);
+                    if (page[0] < 0 || page[0] > a.cache.pages) {
+                        atomicOr(a.status, kStatusBadIndex);
+                        page[0] = a.cache.pages;
+                    }
+                    for (int kind = 0; kind < 2; ++kind) {               // 0: values of j - lag, 1: keys of j
+                        if (kind ? j >= n : j < lag) continue;
                         if (lane == 0) ok = mbar_wait(s_empty + 8 * ring.slot, ring.phase ^ 1, ctl);
                         ok = __shfl_sync(0xffffffffu, ok, 0);
                         if (!ok) break;
@@ -177,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                         __syncwarp();
                         if (mine)
                             tma_load_5d(s_ring + ring.slot * C::kSlot + panel * kPanel + box * a.box * 128, kind ? &a.k_map : &a.v_map, bar,
-                                        64 * panel, at, 0, w.h, page, pol);
+                                        64 * panel, place_of(kind ? j : j - lag) % a.cache.page_size, 0, w.h,
+                                        kind ? page[0] : lag == 1 ? page[1] : page[2], pol);
                         ring.step();
                     }
                 }
@@ -188,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 constexpr uint32_t kIdescS = make_idesc(BF16, kLanes, kTile);
                 constexpr uint32_t kIdescO = make_idesc(BF16, kLanes, kDp) | (1u << 16);    // values: features lead
                 const int ksteps = (a.D + 15) / 16;
-                uint32_t vok_phase = 0, p_phase[2] = {0, 0}, q_phase = 0;
+                uint32_t vok_phase = 0, p_phase = 0, q_phase = 0;   // p_phase: bit s
                 bool ok = work, any = false;
                 while (ok && w.next()) {
                     const bool pair = two();
@@ -218,13 +261,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                         }
                         for (int s = 0; s < 2; ++s) {
                             if (v >= 0 && (pair || (v & 1) == s)) {
-                                if (!(ok = mbar_wait(s_pfull + 8 * s, p_phase[s], ctl))) break;
-                                p_phase[s] ^= 1;
+                                if (!(ok = mbar_wait(s_pfull + 8 * s, p_phase >> s & 1u, ctl))) break;
+                                p_phase ^= 1u << s;
                                 tc_fence_after();
                                 const uint32_t from = s_ring + v_slot * C::kSlot;
 #pragma unroll
                                 for (int k = 0; k < kTile / 16; ++k)
-                                    mma_ts(tmem + C::kO + s * kDp, tmem + s * kTile + k * 8, values_desc(from + k * 2048, kPanel), kIdescO,
+                                    mma_ts(tmem + C::kO + s * kDp, tmem + s * kTile + (k >> 2) * 64 + (k & 3) * 8, values_desc(from + k * 2048, kPanel), kIdescO,
                                            (begun >> s & 1u) | (k > 0));
                                 begun |= 1u << s;
                             }
@@ -269,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                         const int place0 = (w.t0 + tile) * kTile;
                         if (kind == 0 && place0 + kTile > w.context) {
                             const int first = max(0, w.context - place0), last = w.len - place0;    // drafted rows
-                            uint8_t* slot = base + (s_ring - s_base) + ring.slot * C::kSlot;
+                            uint8_t* slot = smem_raw + (s_ring - s_base) + ring.slot * C::kSlot;
                             constexpr int kChunks = NC * 8;              // 16 bytes each, of a row
                             for (int i = first * kChunks + (warp - 2) * 32 + lane; i < kTile * kChunks; i += 64) {
                                 const int row = i / kChunks, c = i % kChunks;
@@ -304,27 +347,53 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             }
         }
     } else {
-        more_registers<208>();
+        more_registers<104>();
         // ---------------------------------------------------------------- softmax
-        const int s = (warp - kSoftmaxWarp) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-        const uint32_t t_lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const uint32_t t_s = t_lanes + s * kTile;
+        // Two threads to a row of S, each with 64 places; they tell each other their maxima.
+        const int s = (warp - kSoftmaxWarp) >> 3, half = warp >> 2 & 1, row = (warp & 3) * 32 + lane;
+        const uint32_t t_lanes = tmem + (static_cast<uint32_t>(row & ~31) << 16);
+        const uint32_t max_at = smem_u32(s_max) + ((s * 2 + half) * kLanes + row) * 4;       // (the other's: 4 kLanes bytes across)
         uint32_t s_phase = 0, o_phase = 0;
         bool dead = false;
         if (a.test_stall && work && tid == 32 * kSoftmaxWarp) mbar_wait(s_stall, 0, ctl);   // (tests: nothing arrives there)
-        while (work && w.next()) {
-            const bool pair = two();
-            const int n = w.t1 - w.t0, first = a.starts[w.b];
-            const int r = w.row0 + (pair ? s * kLanes : 0) + row;        // of the problem
-            const bool live = r < w.rows;
-            const bool idle = __all_sync(0xffffffffu, !live);
-            const int token = live ? r / a.G : 0, head = w.h * a.G + (live ? r - token * a.G : 0);
-            // ---- this stream's rows of Q (each stream half of them where they are shared)
+        // This thread's row of a unit's problem (past its rows: the last one's token and head, for loads alone), found anew where it is
+        // needed: the registers are S's.
+        auto row_of = [&](const volatile Unit* u) {
+            int at = row;
+            asm volatile("" : "+r"(at));
+            return u->row0 + (u->two() ? s * kLanes : 0) + at;
+        };
+        auto token_of = [&](const volatile Unit* u) { return min(row_of(u), u->rows - 1) / a.G; };
+        auto head_of = [&](const volatile Unit* u, int token) { return u->h * a.G + min(row_of(u), u->rows - 1) - token * a.G; };
+        const bool leads = tid == 32 * kSoftmaxWarp;
+        auto describe = [&](Unit& u) {                       // (the leading thread)
+            Walk& v = *walk;
+            u.more = v.next();
+            if (!u.more) return;
+            u.b = v.b, u.h = v.h, u.row0 = v.row0, u.rows = v.rows, u.context = v.context, u.count = v.count;
+            u.t0 = v.t0, u.n = v.t1 - v.t0, u.first = a.starts[v.b];
+            u.pieces = v.pieces, u.first_cta = v.first_cta, u.part = v.part;
+        };
+        if (leads) {
+            units[0].more = 0;
+            if (work) {
+                new (walk) Walk(w);
+                describe(units[0]);
+            }
+        }
+        bar_sync(1, kSoftmax);
+        for (const volatile Unit* u = units; u->more; u = u == units ? units + 1 : units) {
+            const bool pair = u->two();
+            const bool idle = u->row0 + (pair ? s * kLanes : 0) + (row & ~31) >= u->rows;
+            // ---- this thread's part of its row of Q: a half, a quarter where the streams share rows
             {
-                const uint16_t* from = a.q + static_cast<long long>(first + token) * a.q_ts + head * a.q_hs;
+                const bool live = row_of(u) < u->rows;
+                const int token = token_of(u), head = head_of(u, token);
+                const uint16_t* from = a.q + static_cast<long long>(u->first + token) * a.q_ts + head * a.q_hs;
                 const uint32_t to = s_q + (pair ? s * C::kQ : 0) + row * 128;
-                const int c0 = pair ? 0 : s * (NC * 4), c1 = pair ? NC * 8 : c0 + NC * 4;
-#pragma unroll 8
+                constexpr int kAll = NC * 8;                 // 16-byte pieces of a row
+                const int c0 = pair ? half * (kAll / 2) : (2 * s + half) * (kAll / 4), c1 = c0 + (pair ? kAll / 2 : kAll / 4);
+#pragma unroll 4
                 for (int c = c0; c < c1; ++c) {
                     uint4 x = make_uint4(0, 0, 0, 0);
                     if (live && c * 8 < a.D) x = *reinterpret_cast<const uint4*>(from + c * 8);
@@ -335,40 +404,48 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_qfull);
             }
+            if (leads) describe(units[u == units]);          // (the next one, seen by all after the barriers below)
             float ref = -INFINITY, l = 0.f;
             bool begun = false;
-            for (int j = pair ? 0 : s; j < n; j += pair ? 1 : 2) {
+            for (int j = pair ? 0 : s; j < u->n; j += pair ? 1 : 2) {
                 if (!dead) {
                     const bool ok = mbar_wait(s_sfull + 8 * s, s_phase, ctl);
                     dead = !__all_sync(0xffffffffu, ok);
                 }
-                if (dead) break;
                 s_phase ^= 1;
-                tc_fence_after();
-                if (!idle) {
-                    uint32_t x[4][32];
+                if (!idle) {                                 // (a warp that gave up goes on, as the one it meets may)
+                    tc_fence_after();
+                    // S is read twice, 32 places at a time: for the maxima and for the probabilities. (Held in registers in between, it pushes
+                    // others out to local memory, whose loads miss the small L1 beside 227 KB of shared memory: 7000 cycles a tile.)
+                    const uint32_t t_s = t_lanes + s * kTile + 64 * half;
+                    const int place0 = (u->t0 + j) * kTile + 64 * half;
+                    const bool tail = place0 + 64 > u->context;
+                    uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+                    if (tail) {
+                        const int tok = token_of(u);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_ld32(t_s + 32 * k, x[k]);
-                    tmem_ld_wait();
-                    const int place0 = (w.t0 + j) * kTile;
-                    if (place0 + kTile > w.context) {
+                        for (int k = 0; k < 2; ++k) seen[k] = seen32(a, u->first + tok, tok, place0 + 32 * k - u->context, u->count);
+                    }
+                    float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t seen = seen32(a, first + token, token, place0 + 32 * k - w.context, w.count);
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t x[32];
+                        tmem_ld32(t_s + 32 * k, x);
+                        tmem_ld_wait();
+                        if (tail) hide(x, seen[k]);
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!(seen >> c & 1u)) x[k][c] = 0xff800000u;
+                        for (int c = 0; c < 32; c += 8) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) top4[e] = max3(top4[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
                         }
                     }
-                    float top = -INFINITY, top2 = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            top = max3(top, __uint_as_float(x[k][c]), __uint_as_float(x[k][c + 1]));
-                            top2 = max3(top2, __uint_as_float(x[k][c + 2]), __uint_as_float(x[k][c + 3]));
-                        }
-                    top = fmaxf(top, top2) * a.scale_log2;
+                    float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * a.scale_log2;
+                    // (read by the other warp before this stream's next S is there)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(max_at), "f"(top) : "memory");
+                    bar_sync(2 + s * 4 + (warp & 3), 64);
+                    float other;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(max_at ^ (4 * kLanes)) : "memory");
+                    top = fmaxf(top, other);
                     const bool grows = top > ref + kSlack || (ref == -INFINITY && top > ref);
                     if (__any_sync(0xffffffffu, grows)) {
                         const float now = grows ? top : ref;
@@ -376,34 +453,44 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                         ref = now;
                         l *= keep;
                         if (begun) {                         // (the MMAs of the tiles before have ended: S came after them)
-#pragma unroll
-                            for (int k = 0; k < kDp / 32; ++k) {
+#pragma unroll 1
+                            for (int k = 0; k < kDp / 64; ++k) {
+                                const uint32_t at = t_lanes + C::kO + s * kDp + half * (kDp / 2) + 32 * k;
                                 uint32_t o[32];
-                                tmem_ld32(t_lanes + C::kO + s * kDp + 32 * k, o);
+                                tmem_ld32(at, o);
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * keep);
-                                tmem_st16(t_lanes + C::kO + s * kDp + 32 * k, reinterpret_cast<const uint32_t(&)[16]>(o[0]));
-                                tmem_st16(t_lanes + C::kO + s * kDp + 32 * k + 16, reinterpret_cast<const uint32_t(&)[16]>(o[16]));
+                                tmem_st16(at, reinterpret_cast<const uint32_t(&)[16]>(o[0]));
+                                tmem_st16(at + 16, reinterpret_cast<const uint32_t(&)[16]>(o[16]));
                             }
                         }
                     }
                     const float minus = ref == -INFINITY ? 0.f : -ref;
-                    float l2[2] = {0.f, 0.f};
+                    const uint64_t scale2 = both(a.scale_log2, a.scale_log2), minus2 = both(minus, minus);
+                    uint64_t sum2[2] = {0, 0};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t p[16];
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t x[32], p[16];
+                        tmem_ld32(t_s + 32 * k, x);
+                        tmem_ld_wait();
+                        if (tail) hide(x, seen[k]);
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
-                            const float e0 = exp2_approx(fmaf(__uint_as_float(x[k][c]), a.scale_log2, minus));
-                            const float e1 = exp2_approx(fmaf(__uint_as_float(x[k][c + 1]), a.scale_log2, minus));
-                            l2[0] += e0;
-                            l2[1] += e1;
+                            uint64_t d;
+                            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(both(__uint_as_float(x[c]), __uint_as_float(x[c + 1]))), "l"(scale2), "l"(minus2));
+                            float e0, e1;
+                            asm("mov.b64 {%0, %1}, %2;" : "=f"(e0), "=f"(e1) : "l"(d));
+                            e0 = exp2_approx(e0), e1 = exp2_approx(e1);
+                            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum2[c >> 1 & 1]) : "l"(both(e0, e1)));
                             p[c / 2] = pack2<BF16>(e0, e1);
                         }
-                        tmem_st16(t_s + 16 * k, p);
+                        tmem_st16(t_s + 16 * k, p);          // (where S has been read)
                     }
-                    l += l2[0] + l2[1];
+                    float l4[4];
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(l4[0]), "=f"(l4[1]) : "l"(sum2[0]));
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(l4[2]), "=f"(l4[3]) : "l"(sum2[1]));
+                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     tmem_st_wait();
                 }
                 begun = true;
@@ -417,128 +504,129 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             }
             o_phase ^= 1;
             tc_fence_after();
-            s_stat[s * kLanes + row] = make_float2(ref, l);
+            s_stat[(s * 2 + half) * kLanes + row] = make_float2(ref, l);         // (Q has been read: O is there)
             if (tid == 32 * kSoftmaxWarp) ctl_i[2] = *abort_flag;
-            bar_sync(1, 256);
-            if (ctl_i[2]) break;                             // (all 256 threads alike)
-            // ---- join the streams where they share rows; each then has half of the columns
-            float M = ref, L = l, f0 = 1.f, f1 = 1.f;
+            bar_sync(1, kSoftmax);
+            if (ctl_i[2]) break;                             // (all these threads alike)
+            // ---- join the halves' sums, and the streams where they share rows; each thread then has a part of the row's columns
+            const float2 h0 = s_stat[(pair ? s * 2 : 0) * kLanes + row], h1 = s_stat[((pair ? s * 2 : 0) + 1) * kLanes + row];
+            float M = h0.x, L = h0.y + h1.y, f0 = 1.f, f1 = 1.f;
             if (!pair) {
-                const float2 p = s_stat[row], q = s_stat[kLanes + row];
-                M = fmaxf(p.x, q.x);
+                const float2 g0 = s_stat[2 * kLanes + row], g1 = s_stat[3 * kLanes + row];
+                M = fmaxf(h0.x, g0.x);
                 const float at = M == -INFINITY ? 0.f : M;
-                f0 = exp2_approx(p.x - at);
-                f1 = exp2_approx(q.x - at);
-                L = p.y * f0 + q.y * f1;
+                f0 = exp2_approx(h0.x - at);
+                f1 = exp2_approx(g0.x - at);
+                L = L * f0 + (g0.y + g1.y) * f1;
             }
-            const bool bad = ctl_i[4];
-            const bool whole = w.pieces == 1;
+            const bool live = row_of(u) < u->rows;
+            const int token = token_of(u), head = head_of(u, token);
+            const bool bad = ctl_i[4], whole = u->pieces == 1;
             const float inv = L == 0.f ? 0.f : 1.f / L;
-            constexpr int kCh = kDp / 32;
-            const int k0 = pair ? 0 : s * (kCh / 2), k1 = pair ? kCh : k0 + kCh / 2;
+            const int k0 = pair ? half * (kDp / 32) : (2 * s + half) * (kDp / 64), k1 = k0 + (pair ? kDp / 32 : kDp / 64);     // in sixteens
             const int unit_row = (pair ? s * kLanes : 0) + row;
+            const bool tells = half == 0 && (pair || s == 0);            // of the threads with a row, the one that writes its lse
+            uint16_t* const out = a.out + static_cast<long long>(u->first + token) * a.o_ts + head * a.o_hs;
+            auto store16 = [&](int k, const float (&y)[16], float by) {
+#pragma unroll
+                for (int c = 0; c < 16; c += 8) {
+                    if (16 * k + c >= a.D) break;
+                    float z[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] = y[c + e] * by;
+                    *reinterpret_cast<uint4*>(out + 16 * k + c) = pack8<BF16>(z);
+                }
+            };
             if (!idle) {
+#pragma unroll 1
                 for (int k = k0; k < k1; ++k) {
-                    uint32_t o[32];
-                    tmem_ld32(t_lanes + C::kO + (pair ? s * kDp : 0) + 32 * k, o);
-                    if (!pair && n > 1) {
-                        uint32_t o1[32];
-                        tmem_ld32(t_lanes + C::kO + kDp + 32 * k, o1);
+                    uint32_t o[16];
+                    float y[16];
+                    tmem_ld16(t_lanes + C::kO + (pair ? s * kDp : 0) + 16 * k, o);
+                    if (!pair && u->n > 1) {
+                        uint32_t o1[16];
+                        tmem_ld16(t_lanes + C::kO + kDp + 16 * k, o1);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            o[c] = __float_as_uint(__uint_as_float(o[c]) * f0 + __uint_as_float(o1[c]) * f1);
+                        for (int c = 0; c < 16; ++c) y[c] = __uint_as_float(o[c]) * f0 + __uint_as_float(o1[c]) * f1;
                     } else {
                         tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) y[c] = __uint_as_float(o[c]);
                     }
                     if (bad && live) {
-                        const int lo = max(0, w.t0 * kTile - w.context), hi = min(w.count, w.t1 * kTile - w.context);
+                        const int lo = max(0, u->t0 * kTile - u->context), hi = min(u->count, (u->t0 + u->n) * kTile - u->context);
+#pragma unroll 1
                         for (int j = lo; j < hi; ++j) {
-                            const int place = w.context + j, i = place / a.cache.page_size;
-                            if (!a.sees(first + token, token, place, w.context, w.count)) continue;
-                            const int page = a.table[static_cast<long long>(w.b) * a.ld_table + i];
+                            const int place = u->context + j, i = place / a.cache.page_size;
+                            if (!a.sees(u->first + token, token, place, u->context, u->count)) continue;
+                            const int page = a.table[static_cast<long long>(u->b) * a.ld_table + i];
                             if (page < 0 || page >= a.cache.pages) continue;
                             const uint16_t* v = a.cache.v + page * a.cache.v_page + (place - i * a.cache.page_size) * a.cache.v_token +
-                                                w.h * a.cache.v_head + 32 * k;
+                                                u->h * a.cache.v_head + 16 * k;
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (32 * k + c < a.D && not_finite<BF16>(v[c]) & 1u) o[c] = __float_as_uint(__uint_as_float(o[c]) + to_f32<BF16>(v[c]));
+                            for (int c = 0; c < 16; ++c)
+                                if (16 * k + c < a.D && not_finite<BF16>(v[c]) & 1u) y[c] += to_f32<BF16>(v[c]);
                         }
                     }
                     if (whole) {
-                        if (live) {
-                            uint16_t* to = a.out + static_cast<long long>(first + token) * a.o_ts + head * a.o_hs + 32 * k;
-#pragma unroll
-                            for (int c = 0; c < 32; c += 8) {
-                                if (32 * k + c >= a.D) break;
-                                float y[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[c + e]) * inv;
-                                *reinterpret_cast<uint4*>(to + c) = pack8<BF16>(y);
-                            }
-                        }
+                        if (live) store16(k, y, inv);
                     } else {
-                        float4* to = reinterpret_cast<float4*>(a.parts) + (static_cast<long long>(w.part) * (kDp / 4) + 8 * k) * kUnitRows + unit_row;
+                        float4* to = reinterpret_cast<float4*>(a.parts) + (static_cast<long long>(u->part) * (kDp / 4) + 4 * k) * kUnitRows + unit_row;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            __stcg(to + c * kUnitRows, make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                                                   __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3])));
+                        for (int c = 0; c < 4; ++c)
+                            __stcg(to + c * kUnitRows, make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]));
                     }
                 }
             }
             if (whole) {
-                if (live && a.lse && (pair || s == 0)) a.lse[static_cast<long long>(first + token) * a.Hq + head] = lse_of(M, L);
-                bar_sync(1, 256);                            // (s_stat and ctl_i[2] are written again)
+                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(M, L);
+                bar_sync(1, kSoftmax);                       // (s_stat, where Q comes, and ctl_i[2] are written again)
                 continue;
             }
-            if (pair || s == 0) __stcg(a.stats + static_cast<long long>(w.part) * kUnitRows + unit_row, make_float2(M, L));
+            if (tells) __stcg(a.stats + static_cast<long long>(u->part) * kUnitRows + unit_row, make_float2(M, L));
             __threadfence();
-            bar_sync(1, 256);
+            bar_sync(1, kSoftmax);
             if (tid == 32 * kSoftmaxWarp) {
-                const int before = atomic_add_acq_rel_gpu(a.counters + w.first_cta, 1);
-                const bool last = before == w.pieces - 1;
-                if (last) st_relaxed_gpu(a.counters + w.first_cta, 0);   // as the next call finds it
+                const int before = atomic_add_acq_rel_gpu(a.counters + u->first_cta, 1);
+                const bool last = before == u->pieces - 1;
+                if (last) st_relaxed_gpu(a.counters + u->first_cta, 0);   // as the next call finds it
                 ctl_i[1] = last;
             }
-            bar_sync(1, 256);
+            bar_sync(1, kSoftmax);
             if (ctl_i[1] && !idle) {
                 __threadfence();
                 float most = -INFINITY, sum = 0.f;
-                for (int i = 0; i < w.pieces; ++i) most = fmaxf(most, __ldcg(a.stats + static_cast<long long>(w.part_of(i)) * kUnitRows + unit_row).x);
+#pragma unroll 4
+                for (int i = 0; i < u->pieces; ++i) most = fmaxf(most, __ldcg(a.stats + static_cast<long long>(u->part_of(i)) * kUnitRows + unit_row).x);
                 const float at = most == -INFINITY ? 0.f : most;
+#pragma unroll 1
                 for (int k = k0; k < k1; ++k) {
-                    float y[32];
+                    float y[16];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) y[c] = 0.f;
+                    for (int c = 0; c < 16; ++c) y[c] = 0.f;
                     sum = 0.f;
-                    for (int i = 0; i < w.pieces; ++i) {
-                        const int part = w.part_of(i);
+#pragma unroll 2
+                    for (int i = 0; i < u->pieces; ++i) {
+                        const int part = u->part_of(i);
                         const float2 st = __ldcg(a.stats + static_cast<long long>(part) * kUnitRows + unit_row);
+                        const float4* from = reinterpret_cast<const float4*>(a.parts) + (static_cast<long long>(part) * (kDp / 4) + 4 * k) * kUnitRows + unit_row;
+                        float4 v[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) v[c] = __ldcg(from + c * kUnitRows);
                         const float f = exp2_approx(st.x - at);
                         sum = fmaf(st.y, f, sum);
-                        const float4* from = reinterpret_cast<const float4*>(a.parts) + (static_cast<long long>(part) * (kDp / 4) + 8 * k) * kUnitRows + unit_row;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float4 v = __ldcg(from + c * kUnitRows);
-                            y[4 * c] = fmaf(v.x, f, y[4 * c]), y[4 * c + 1] = fmaf(v.y, f, y[4 * c + 1]);
-                            y[4 * c + 2] = fmaf(v.z, f, y[4 * c + 2]), y[4 * c + 3] = fmaf(v.w, f, y[4 * c + 3]);
+                        for (int c = 0; c < 4; ++c) {
+                            y[4 * c] = fmaf(v[c].x, f, y[4 * c]), y[4 * c + 1] = fmaf(v[c].y, f, y[4 * c + 1]);
+                            y[4 * c + 2] = fmaf(v[c].z, f, y[4 * c + 2]), y[4 * c + 3] = fmaf(v[c].w, f, y[4 * c + 3]);
                         }
                     }
-                    if (!live) continue;
-                    const float by = sum == 0.f ? 0.f : 1.f / sum;
-                    uint16_t* to = a.out + static_cast<long long>(first + token) * a.o_ts + head * a.o_hs + 32 * k;
-#pragma unroll
-                    for (int c = 0; c < 32; c += 8) {
-                        if (32 * k + c >= a.D) break;
-                        float z[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) z[e] = y[c + e] * by;
-                        *reinterpret_cast<uint4*>(to + c) = pack8<BF16>(z);
-                    }
+                    if (live) store16(k, y, sum == 0.f ? 0.f : 1.f / sum);
                 }
-                if (live && a.lse && (pair || s == 0)) a.lse[static_cast<long long>(first + token) * a.Hq + head] = lse_of(most, sum);
+                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(most, sum);
             }
-            bar_sync(1, 256);                                // (ctl_i[1] is written again)
+            bar_sync(1, kSoftmax);                           // (ctl_i[1] is written again)
         }
         tc_fence_before();
     }
@@ -549,8 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     }
     // where a wait ran out, copies in flight land before the CTA goes
     if (warp == 0 && lane == 0 && *abort_flag)
-        for (uint32_t i = ring.it > C::kSlots ? ring.it - C::kSlots : 0; i < ring.it; ++i)
-            mbar_wait_plain(s_full + 8 * (i % C::kSlots), (i / C::kSlots) & 1, drain_limit(a.timeout_cycles));
+        for (uint32_t i = ring.it > static_cast<uint32_t>(slots) ? ring.it - slots : 0; i < ring.it; ++i)
+            mbar_wait_plain(s_full + 8 * (i % slots), (i / slots) & 1, drain_limit(a.timeout_cycles));
 }
 
 template <bool BF16, int NC>
@@ -561,13 +649,13 @@ int go(const Runtime& rt, const AttnArgs& a, wq4_stream_t st) {
     const int regs = ready.get(rt.device, [&]() -> int {
         cudaFuncAttributes fa;
         if (cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) == cudaSuccess)
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kMaxSmem) == cudaSuccess)
             return fa.numRegs;
         cudaGetLastError();
         return -1;
     });
-    if (regs != 168) return WQ4_ERR_CUDA;            // the warps' shares count on the registers of the launch; with fewer they would wait
-    return launch(rt, kern, dim3(a.grid), kThreads, C::kSmem, 1, st, a);
+    if (regs != 96) return WQ4_ERR_CUDA;             // the warps' shares count on the registers of the launch; with fewer they would wait
+    return launch(rt, kern, dim3(a.grid), kThreads, C::smem(a.max_rows > kLanes ? 2 : 1), 1, st, a);
 }
 
 }  // namespace

@@ -7,6 +7,7 @@
 // Work is split over the caches' lengths: all units' tiles of 64 places lie one after the other, and each CTA takes an
 // equal share of them, whichever units they belong to. A unit that several CTAs share is joined by
 // the CTA that finishes last, from (maximum, sum, O) of each, in the order of the tiles.
+#include <algorithm>
 #include <cstdio>
 
 #include "wq4_attention.cuh"
@@ -505,11 +506,11 @@ int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_
     a.cache = CacheArgs(cache);
     a.ld_table = ld_table, a.table_width = table_width, a.mask_words = mask_words;
     a.B = B, a.T = T, a.max_tokens = max_tokens, a.Hq = q_heads, a.Hk = kv_heads, a.G = q_heads / kv_heads, a.D = D;
+    a.max_rows = static_cast<int>(std::min(static_cast<long long>(max_tokens) * a.G, 1LL << 20));
     a.scale_log2 = scale * 1.4426950408889634f;
     a.counters = static_cast<int*>(workspace);
     a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + sp.stats);
     a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.parts);
-    a.least = 4;
     a.test_stall = rt.test_stall;
     a.status = rt.status;
     a.timeout_cycles = rt.timeout_cycles;
