@@ -66,12 +66,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// Values as the B operand of O = P V: 64 features by 8 places are the swizzle's atom, so the features are the leading
-// dimension; `panel` bytes from one 64 features to the next.
-__device__ __forceinline__ uint64_t values_desc(uint32_t saddr, uint32_t panel) {
-    uint64_t d = make_sdesc_sw128(saddr);
-    d &= ~(static_cast<uint64_t>(0x3fff) << 16);
-    return d | static_cast<uint64_t>(panel >> 4) << 16;
+// Operands in shared memory are named by descriptors whose upper word is the same for all of them (eight rows of 128 bytes to a
+// swizzle atom, as make_sdesc_sw128 says) and whose lower word is the address in units of 16 bytes, so that the thread that
+// issues the MMAs adds constants: built anew for each, they took longer than the MMAs (112 cycles each against 65).
+// Values are the B operand of O = P V with the features leading: 64 features by 8 places are the atom, and the lower word also
+// holds the distance from one 64 features to the next.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t rows_lo(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t values_lo(uint32_t saddr, uint32_t panel) { return saddr >> 4 | panel >> 4 << 16; }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
+    return d;
 }
 
 // The items of a unit's ring in order: values of tile j - lag, then keys of tile j.
@@ -231,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 constexpr uint32_t kIdescS = make_idesc(BF16, kLanes, kTile);
                 constexpr uint32_t kIdescO = make_idesc(BF16, kLanes, kDp) | (1u << 16);    // values: features lead
                 const int ksteps = (a.D + 15) / 16;
+                const uint32_t k_lo = rows_lo(s_ring), v_lo = values_lo(s_ring, kPanel), q_lo = rows_lo(s_q);
                 uint32_t vok_phase = 0, p_phase = 0, q_phase = 0;   // p_phase: bit s
                 bool ok = work, any = false;
                 while (ok && w.next()) {
@@ -259,23 +266,29 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                             if (!(ok = mbar_wait(s_full + 8 * k_slot, ring.phase, ctl))) break;
                             ring.step();
                         }
+#pragma unroll 1
                         for (int s = 0; s < 2; ++s) {
                             if (v >= 0 && (pair || (v & 1) == s)) {
                                 if (!(ok = mbar_wait(s_pfull + 8 * s, p_phase >> s & 1u, ctl))) break;
                                 p_phase ^= 1u << s;
                                 tc_fence_after();
-                                const uint32_t from = s_ring + v_slot * C::kSlot;
+                                uint32_t from = v_lo + v_slot * (C::kSlot >> 4);
+                                asm volatile("" : "+r"(from));           // (the sums below are not worth registers)
 #pragma unroll
                                 for (int k = 0; k < kTile / 16; ++k)
-                                    mma_ts(tmem + C::kO + s * kDp, tmem + s * kTile + (k >> 2) * 64 + (k & 3) * 8, values_desc(from + k * 2048, kPanel), kIdescO,
-                                           (begun >> s & 1u) | (k > 0));
+                                    mma_ts(tmem + C::kO + s * kDp, tmem + s * kTile + (k >> 2) * 64 + (k & 3) * 8, desc_of(from + k * (2048 >> 4)),
+                                           kIdescO, k > 0 ? 1u : begun >> s & 1u);
                                 begun |= 1u << s;
                             }
                             if (j < n && (pair || (j & 1) == s)) {
-                                const uint32_t q = s_q + (pair ? s * C::kQ : 0), from = s_ring + k_slot * C::kSlot;
-                                for (int k = 0; k < ksteps; ++k) {
-                                    const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-                                    mma_ss(tmem + s * kTile, make_sdesc_sw128(q + off), make_sdesc_sw128(from + off), kIdescS, k > 0);
+                                uint32_t q = q_lo + (pair ? s * (C::kQ >> 4) : 0), from = k_lo + k_slot * (C::kSlot >> 4);
+                                asm volatile("" : "+r"(q), "+r"(from));
+#pragma unroll
+                                for (int k = 0; k < 4 * NC; ++k) {
+                                    constexpr int kStep = kPanel >> 4;
+                                    if (k < ksteps)
+                                        mma_ss(tmem + s * kTile, desc_of(q + (k >> 2) * kStep + (k & 3) * 2), desc_of(from + (k >> 2) * kStep + (k & 3) * 2),
+                                               kIdescS, k > 0);
                                 }
                                 mma_commit(s_sfull + 8 * s);
                             }
