@@ -21,7 +21,7 @@
 namespace wq4 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBlock = 1024;            // weights whose sums are held while the next token is searched
@@ -54,7 +54,43 @@ struct Sum {
         add(o.s);
         c = __fadd_rn(c, o.c);
     }
-    __device__ __forceinline__ double value() const { return static_cast<double>(s) + static_cast<double>(c); }
+    // hi + lo with hi the sum rounded
+    __device__ __forceinline__ Sum normal() const {
+        const float hi = __fadd_rn(s, c);
+        return Sum{hi, __fadd_rn(__fsub_rn(s, hi), c)};
+    }
+    __device__ __forceinline__ bool exceeds(const Sum& o) const {
+        const Sum x = normal(), y = o.normal();
+        return x.s > y.s || (x.s == y.s && x.c > y.c);
+    }
+};
+// Two sums beside each other, two operations to an instruction.
+struct Sum2 {
+    uint64_t s = 0, c = 0;
+    static __device__ __forceinline__ uint64_t plus(uint64_t a, uint64_t b) {
+        uint64_t d;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+        return d;
+    }
+    static __device__ __forceinline__ uint64_t minus(uint64_t a, uint64_t b) {
+        uint64_t d;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(b), "l"(0xbf800000bf800000ull), "l"(a));   // a - 1 b
+        return d;
+    }
+    __device__ __forceinline__ void add(float x0, float x1) {
+        uint64_t x;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+        const uint64_t t = plus(s, x), y = minus(t, s);
+        c = plus(c, plus(minus(s, minus(t, y)), minus(x, y)));
+        s = t;
+    }
+    __device__ __forceinline__ Sum sum() const {
+        Sum a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a.s), "=f"(b.s) : "l"(s));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a.c), "=f"(b.c) : "l"(c));
+        a.add(b);
+        return a;
+    }
 };
 __device__ __forceinline__ Sum warp_sum(Sum x) {
 #pragma unroll
@@ -86,7 +122,7 @@ constexpr int kHeld = 128;              // drafts of a sequence whose parents, t
 struct Shared {
     Part part[2][kMaxCluster];          // [turn][CTA]: written by the others
     float top[kWarps], sum[kWarps];
-    int top_at[kWarps];
+    int top_at;
     Sum block[kMaxShare / kBlock];
     long long tokens[kHeld];
     int parents[kHeld];
@@ -97,31 +133,66 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, const Part& p) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(p.a), "f"(p.b), "f"(p.c), "f"(p.d) : "memory");
 }
 
-// Eight values of a row from column i on, where the row's columns are 16-byte aligned in eights, and one.
+// The kinds of logits: eight of them as they lie in memory, their values, and the larger of each, NaN where there is one.
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, long long i, uint4& lo, uint4& hi) {
-    if constexpr (DT == WQ4_FP32) {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-        lo = q[0], hi = q[1];
-    } else {
-        lo = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    }
-}
-template <int DT>
-__device__ __forceinline__ void values8(const uint4& lo, const uint4& hi, float (&v)[8]) {
-    if constexpr (DT == WQ4_FP32) {
-        const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+struct Kind {
+    static constexpr int kSize = DT == WQ4_FP32 ? 4 : 2, kWords = DT == WQ4_FP32 ? 8 : 4;
+    struct Eight {
+        uint32_t u[kWords];
+    };
+    static __device__ __forceinline__ uint32_t minus_inf() { return DT == WQ4_FP32 ? 0xff800000u : DT == WQ4_BF16 ? 0xff80ff80u : 0xfc00fc00u; }
+    // from column i of a row that holds n; aligned: its columns lie on 16-byte boundaries in eights
+    static __device__ __forceinline__ Eight load(const void* p, int i, int n, bool aligned) {
+        Eight e;
+        if (aligned && i + 8 <= n) {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + static_cast<long long>(i) * kSize);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(u[j]);
-    } else {
-        unpack8<DT == WQ4_BF16>(lo, v);
+            for (int k = 0; k < kWords / 4; ++k) {
+                const uint4 x = q[k];
+                e.u[4 * k] = x.x, e.u[4 * k + 1] = x.y, e.u[4 * k + 2] = x.z, e.u[4 * k + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                e.u[k] = minus_inf();
+                if constexpr (DT == WQ4_FP32) {
+                    if (i + k < n) e.u[k] = static_cast<const uint32_t*>(p)[i + k];
+                } else {
+                    const uint16_t* q = static_cast<const uint16_t*>(p) + i + 2 * k;
+                    if (i + 2 * k < n) e.u[k] = (e.u[k] & 0xffff0000u) | q[0];
+                    if (i + 2 * k + 1 < n) e.u[k] = (e.u[k] & 0x0000ffffu) | static_cast<uint32_t>(q[1]) << 16;
+                }
+            }
+        }
+        return e;
     }
-}
-template <int DT>
-__device__ __forceinline__ float value1(const void* p, long long i) {
-    if constexpr (DT == WQ4_FP32) return static_cast<const float*>(p)[i];
-    else return to_f32<DT == WQ4_BF16>(static_cast<const uint16_t*>(p)[i]);
-}
+    static __device__ __forceinline__ void values(const Eight& e, float (&v)[8]) {
+        if constexpr (DT == WQ4_FP32) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(e.u[k]);
+        } else {
+            unpack8<DT == WQ4_BF16>(make_uint4(e.u[0], e.u[1], e.u[2], e.u[3]), v);
+        }
+    }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        uint32_t d;
+        if constexpr (DT == WQ4_FP32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        else if constexpr (DT == WQ4_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    // the largest in m, +inf for NaN
+    static __device__ __forceinline__ float largest(uint32_t m) {
+        float x;
+        if constexpr (DT == WQ4_FP32) {
+            x = __uint_as_float(m);
+        } else {
+            const float lo = to_f32<DT == WQ4_BF16>(m & 0xffffu), hi = to_f32<DT == WQ4_BF16>(m >> 16);
+            x = isnan(lo) || isnan(hi) ? INFINITY : fmaxf(lo, hi);
+        }
+        return isnan(x) ? INFINITY : x;
+    }
+};
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -130,9 +201,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
-    extern __shared__ float4 w4[];                   // this CTA's logits, scaled, then weights
+__global__ void __launch_bounds__(kThreads, 3) verify_kernel(const VerifyArgs a) {
+    using K = Kind<DT>;
+    // This CTA's logits as they lie in memory, in the end of what the weights take; then the weights.
+    extern __shared__ float4 w4[];
     float* const w = reinterpret_cast<float*>(w4);
+    char* const raw = reinterpret_cast<char*>(w4) + a.share * (4 - K::kSize);
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0, b = blockIdx.x / C;
@@ -190,13 +264,28 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     // Whether the draft is kept, its weight and the weights' sum given. (In fp32: a random number lies as near to the border as these
     // three roundings reach once in some millions.)
     auto keeps = [&](float weight, float z) { return __fmul_rn(__fmul_rn(j < kHeld ? sh.uniforms[j] : a.uniforms[s0 + j], draft_q), z) < weight; };
+    auto scaled = [&](int i) {                       // a logit
+        float x;
+        if constexpr (DT == WQ4_FP32) x = reinterpret_cast<const float*>(raw)[i];
+        else x = to_f32<DT == WQ4_BF16>(reinterpret_cast<const uint16_t*>(raw)[i]);
+        return __fmul_rn(x, inv_heat);
+    };
     auto here = [&](long long t) { return t >= v0 && t < v0 + mine; };
+    auto sum_blocks = [&] {                          // in warp 0
+        Sum all{0.f, 0.f};
+        if (warp == 0) {
+            for (int k = lane; k < blocks; k += 32) all.add(sh.block[k]);
+            all = warp_sum(all);
+        }
+        return all;
+    };
     // f of each of the CTA's weights and of the same place of another row (null: 0): the sums of blocks of 1024 go to sh.block, f
     // itself, if it is to, into the weights' place. Returns the sum of all, in warp 0.
     auto weigh = [&](const float* other, bool write, auto f) {
         const bool vec = (reinterpret_cast<uintptr_t>(other) & 15u) == 0;
         for (int k = warp; k < blocks; k += kWarps) {
             Sum s{0.f, 0.f};
+            Sum2 s2;
             const int from = k * kBlock + lane * 4;
             if (vec && k * kBlock + kBlock <= mine) {
                 float4 o[8];
@@ -209,8 +298,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
                     float4 x = w4[at / 4];
                     x.x = f(at, x.x, o[i].x), x.y = f(at + 1, x.y, o[i].y), x.z = f(at + 2, x.z, o[i].z), x.w = f(at + 3, x.w, o[i].w);
                     if (write) w4[at / 4] = x;
-                    s.add(x.x), s.add(x.y), s.add(x.z), s.add(x.w);
+                    s2.add(x.x, x.y), s2.add(x.z, x.w);
                 }
+                s = s2.sum();
             } else {
                 for (int i0 = 0; i0 < kBlock; i0 += 256) {
                     float o[8];
@@ -234,12 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
             if (lane == 0) sh.block[k] = s;
         }
         __syncthreads();
-        Sum all{0.f, 0.f};
-        if (warp == 0) {
-            for (int k = lane; k < blocks; k += 32) all.add(sh.block[k]);
-            all = warp_sum(all);
-        }
-        return all;
+        return sum_blocks();
     };
     // The sum that the CTAs told, in every thread of the cluster to the same bits.
     auto sum_of = [&](int was) {
@@ -264,85 +349,76 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     float inv = 0.f;
     long long tried = -1;
     bool pending = false;                            // whether it is still to be taken
-    auto left = [&](int i, float x, float q) {
-        if (a.draft_probs) return fmaxf(__fsub_rn(__fmul_rn(x, inv), q), 0.f);
-        return i == tried ? 0.f : x;
+    float gone = 0.f;
+    auto take_off = [&](int, float x, float q) { return fmaxf(__fsub_rn(__fmul_rn(x, inv), q), 0.f); };
+    auto left = [&](int i) { return a.draft_probs ? take_off(i, w[i], q_row[i]) : w[i]; };
+    auto block_sum = [&](int k) {                    // (a warp)
+        Sum2 s2;
+        for (int i = lane * 2; i < kBlock; i += 64) s2.add(w[k * kBlock + i], w[k * kBlock + i + 1]);
+        return warp_sum(s2.sum());
     };
     while (fine) {
         // ---- the node's row: its logits, scaled, in shared memory; their maximum
-        const long long r0 = (s0 + node) * a.ld + v0;
-        float m = -INFINITY;
-        int m_at = 0x7fffffff;
-        bool odd = false;                            // NaN
-        constexpr int kSize = DT == WQ4_FP32 ? 4 : 2;
-        const bool vec = (reinterpret_cast<uintptr_t>(a.logits) + r0 * kSize) % 16 == 0;
-        int done = 0;
-        if (vec) {
-            constexpr int kBatch = DT == WQ4_FP32 ? 2 : 4;
-            for (int i0 = 0; i0 + 8 <= mine; i0 += kThreads * 8 * kBatch) {
-                uint4 lo[kBatch], hi[kBatch];
+        const char* const from = static_cast<const char*>(a.logits) + ((s0 + node) * a.ld + v0) * K::kSize;
+        const bool aligned = (reinterpret_cast<uintptr_t>(from) & 15u) == 0;
+        constexpr int kBatch = DT == WQ4_FP32 ? 2 : 4;
+        uint32_t most = K::minus_inf();
+        for (int i0 = tid * 8; i0 < a.share; i0 += kThreads * 8 * kBatch) {
+            typename K::Eight e[kBatch];
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int i = i0 + (k * kThreads + tid) * 8;
-                    if (i + 8 <= mine) load8<DT>(a.logits, r0 + i, lo[k], hi[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int i = i0 + (k * kThreads + tid) * 8;
-                    if (i + 8 > mine) break;
-                    float x[8];
-                    values8<DT>(lo[k], hi[k], x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        odd |= x[e] != x[e];
-                        if (greedy && x[e] > m) m_at = v0 + i + e;
-                        x[e] = __fmul_rn(x[e], inv_heat);
-                        m = fmaxf(m, x[e]);
-                    }
-                    w4[i / 4] = make_float4(x[0], x[1], x[2], x[3]);
-                    w4[i / 4 + 1] = make_float4(x[4], x[5], x[6], x[7]);
-                }
-            }
-            done = mine & ~7;
-        }
-        constexpr int kSingles = 8;
-        for (int i0 = done; i0 < mine; i0 += kThreads * kSingles) {
-            float x[kSingles];
-#pragma unroll
-            for (int k = 0; k < kSingles; ++k) {
-                const int i = i0 + k * kThreads + tid;
-                x[k] = i < mine ? value1<DT>(a.logits, r0 + i) : -INFINITY;
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * kThreads * 8;
+                if (i < a.share) e[k] = K::load(from, i, mine, aligned);
             }
 #pragma unroll
-            for (int k = 0; k < kSingles; ++k) {
-                const int i = i0 + k * kThreads + tid;
-                odd |= x[k] != x[k];
-                if (greedy && x[k] > m) m_at = v0 + i;
-                x[k] = __fmul_rn(x[k], inv_heat);
-                m = fmaxf(m, x[k]);
-                if (i < mine) w[i] = x[k];
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * kThreads * 8;
+                if (i >= a.share) break;
+#pragma unroll
+                for (int c = 0; c < K::kWords; ++c) most = K::larger(most, e[k].u[c]);
+#pragma unroll
+                for (int c = 0; c < K::kWords; c += 4)
+                    *reinterpret_cast<uint4*>(raw + i * K::kSize + 4 * c) = make_uint4(e[k].u[c], e[k].u[c + 1], e[k].u[c + 2], e[k].u[c + 3]);
             }
         }
-        if (odd) m = INFINITY;
+        float m_raw = K::largest(most);
         next_draft();
-        largest(m, m_at, 16);
-        if (lane == 0) sh.top[warp] = m, sh.top_at[warp] = m_at;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m_raw = fmaxf(m_raw, __shfl_xor_sync(0xffffffffu, m_raw, d));
+        if (lane == 0) sh.top[warp] = m_raw;
+        if (tid == 0) sh.top_at = 0x7fffffff;
         __syncthreads();
-        m = sh.top[lane % kWarps], m_at = sh.top_at[lane % kWarps];
-        largest(m, m_at, kWarps / 2);
+        m_raw = sh.top[lane % kWarps];
+#pragma unroll
+        for (int d = kWarps / 2; d; d >>= 1) m_raw = fmaxf(m_raw, __shfl_xor_sync(0xffffffffu, m_raw, d));
+        float m = __fmul_rn(m_raw, inv_heat);        // (rounding keeps the order)
+        if (isnan(m)) m = INFINITY;
+        if (greedy) {                                // its place
+            for (int i = tid * 8; i < mine; i += kThreads * 8) {
+                float x[8];
+                K::values(K::load(raw, i, a.share, true), x);
+#pragma unroll
+                for (int c = 7; c >= 0; --c)
+                    if (x[c] == m && i + c < mine) atomicMin(&sh.top_at, v0 + i + c);
+            }
+            __syncthreads();
+        }
         // ---- their sum, against the CTA's maximum. It decides on the first draft alone, whose random number is as near to the border
         // as this sum is off (2^-22) once in millions.
         float s = 0.f;
         if (!greedy && j < n && !isinf(m)) {
-            const float to2 = 1.44269504f, by = -m * to2;
+            // (differences first: where x and the maximum are near, they are exact)
+            const float to2 = 1.44269504f * inv_heat;
             float s2 = 0.f;
-            for (int i = tid; i < mine / 4; i += kThreads) {
-                const float4 x = w4[i];
-                s += exp2_fast(fmaf(x.x, to2, by)) + exp2_fast(fmaf(x.y, to2, by));
-                s2 += exp2_fast(fmaf(x.z, to2, by)) + exp2_fast(fmaf(x.w, to2, by));
+            for (int i = tid * 8; i < a.share; i += kThreads * 8) {
+                float x[8];
+                K::values(K::load(raw, i, a.share, true), x);
+#pragma unroll
+                for (int c = 0; c < 8; c += 2) {
+                    s += exp2_fast((x[c] - m_raw) * to2);
+                    s2 += exp2_fast((x[c + 1] - m_raw) * to2);
+                }
             }
-            const int i = (mine & ~3) + tid;
-            if (i < mine) s += exp2_fast(fmaf(w[i], to2, by));
             s += s2;
 #pragma unroll
             for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
@@ -352,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
 #pragma unroll
             for (int d = kWarps / 2; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
         }
-        was = exchange(Part{m, greedy ? __int_as_float(m_at) : s, j < n && here(draft) ? w[draft - v0] : -INFINITY, 0.f});
+        was = exchange(Part{m, greedy ? __int_as_float(sh.top_at) : s, j < n && here(draft) ? scaled(static_cast<int>(draft - v0)) : -INFINITY, 0.f});
         const Part told = sh.part[was][lane & (C - 1)];
         float draft_x = told.c;
         top = told.a, top_at = __float_as_int(told.b);
@@ -382,7 +458,38 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
             }
         }
         // ---- the weights themselves, and their sum
-        Sum all = weigh(nullptr, true, [&](int i, float x, float) { return greedy ? (v0 + i == top_at ? 1.f : 0.f) : expf(__fsub_rn(x, top)); });
+        // (A round of blocks is read by all before it is written: the weights of one round end ahead of the logits of the next.)
+        for (int k0 = 0; k0 < a.share / kBlock; k0 += kWarps) {
+            const int k = k0 + warp;
+            typename K::Eight e[4];
+            if (k * kBlock < mine) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] = K::load(raw, k * kBlock + (32 * i + lane) * 8, a.share, true);
+            }
+            __syncthreads();
+            if (k * kBlock < mine) {
+                Sum2 s2;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = k * kBlock + (32 * i + lane) * 8;
+                    float x[8];
+                    K::values(e[i], x);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        // (a product and a difference, rounded one by one)
+                        x[c] = greedy ? (v0 + at + c == top_at ? 1.f : 0.f) : expf(__fsub_rn(__fmul_rn(x[c], inv_heat), top));
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; c += 2) s2.add(x[c], x[c + 1]);
+                    w4[at / 4] = make_float4(x[0], x[1], x[2], x[3]);
+                    w4[at / 4 + 1] = make_float4(x[4], x[5], x[6], x[7]);
+                }
+                const Sum s = warp_sum(s2.sum());
+                if (lane == 0) sh.block[k] = s;
+            }
+            __syncthreads();
+        }
+        Sum all = sum_blocks();
         was = exchange(Part{all.s, all.c, -1.f, 0.f});
         if (j >= n) break;
         // ---- what each draft that is not kept leaves of them
@@ -391,21 +498,37 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
             inv = reciprocal(sum_of(was));
             q_row = a.draft_probs ? a.draft_probs + (s0 + node) * a.ldp + v0 : nullptr;
             tried = draft - v0;
-            all = weigh(q_row, false, left);
+            if (a.draft_probs) {
+                all = weigh(q_row, false, take_off);
+            } else {                                 // one weight is gone, and its block's sum is another
+                if (here(draft) && warp == 0) {
+                    const int i = static_cast<int>(tried), k = i / kBlock;
+                    gone = w[i];
+                    __syncwarp();
+                    if (lane == 0) w[i] = 0.f;
+                    __syncwarp();
+                    const Sum s = block_sum(k);
+                    if (lane == 0) sh.block[k] = s;
+                }
+                __syncthreads();
+                all = sum_blocks();
+            }
             next_draft();
             const int at = j < n && here(draft) ? static_cast<int>(draft - v0) : -1;
-            was = exchange(Part{all.s, all.c, at < 0 ? -1.f : left(at, w[at], q_row ? q_row[at] : 0.f), 0.f});
+            was = exchange(Part{all.s, all.c, at < 0 ? -1.f : left(at), 0.f});
             const bool some = sum_of(was).s > 0.f;
             if (!some) {                             // nothing is left: the weights stay
+                if (!a.draft_probs && tried >= 0 && tried < mine && tid == 0) w[tried] = gone;
+                __syncthreads();
                 all = weigh(nullptr, false, [](int, float x, float) { return x; });
                 was = exchange(Part{all.s, all.c, at < 0 ? -1.f : w[at], 0.f});
             }
             if (j >= n) {
-                pending = some;                      // (the search below takes what is left from the weights)
+                pending = some && a.draft_probs;     // (the search below takes what is left from the weights)
                 break;
             }
-            if (some) {
-                weigh(q_row, true, left);
+            if (some && a.draft_probs) {
+                weigh(q_row, true, take_off);
                 __syncthreads();
             }
             float draft_w = -1.f;
@@ -433,30 +556,44 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     // ---- the next token: the CTA, its block of 1024, of the block's 32 pieces and of the piece's 32 weights the first at which the
     // running sum exceeds the aim
     if (warp != 0) return;
-    auto first_over = [&](double x, double aim, double& upto, bool any) {    // the lane; upto: the sum ahead of it (any: the last with a weight)
-        double run = x;
+    // The first lane at which the running sum of x, from `upto` on, exceeds the aim, or -1; upto: the sum ahead of it. any: the last with
+    // a weight.
+    auto first_over = [&](const Sum& x, const Sum& aim, Sum& upto, bool any) {
+        Sum run = x;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, run, d);
-            if (lane >= d) run += y;
+            Sum o;
+            o.s = __shfl_up_sync(0xffffffffu, run.s, d);
+            o.c = __shfl_up_sync(0xffffffffu, run.c, d);
+            if (lane >= d) {
+                o.add(run);
+                run = o;
+            }
         }
-        const unsigned over = any ? 0u : __ballot_sync(0xffffffffu, upto + run > aim), some = __ballot_sync(0xffffffffu, x > 0);
+        Sum with = upto;
+        with.add(run);
+        const unsigned over = any ? 0u : __ballot_sync(0xffffffffu, with.exceeds(aim)), some = __ballot_sync(0xffffffffu, x.s > 0.f);
         const int at = over ? __ffs(over) - 1 : any && some ? 31 - __clz(some) : -1;
-        if (at != 0) upto += __shfl_sync(0xffffffffu, run, at < 0 ? 31 : at - 1);
+        if (at != 0) {
+            upto.s = __shfl_sync(0xffffffffu, with.s, at < 0 ? 31 : at - 1);
+            upto.c = __shfl_sync(0xffffffffu, with.c, at < 0 ? 31 : at - 1);
+        }
         return at;
     };
-    const double part = lane < C ? Sum{sh.part[was][lane].a, sh.part[was][lane].b}.value() : 0.0;
-    double z = part, upto = 0;
-#pragma unroll
-    for (int d = kMaxCluster / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-    const double aim = static_cast<double>(a.final_uniforms[b]) * __shfl_sync(0xffffffffu, z, 0);
+    const Sum part = lane < C ? Sum{sh.part[was][lane].a, sh.part[was][lane].b} : Sum{0.f, 0.f};
+    // u z as a pair: the product's rounding is what the fused operation finds
+    const Sum z = warp_sum(part).normal();
+    const float u = a.final_uniforms[b];
+    Sum aim{__fmul_rn(u, z.s), 0.f};
+    aim.c = __fmaf_rn(u, z.c, __fmaf_rn(u, z.s, -aim.s));
+    Sum upto{0.f, 0.f};
     int owner = first_over(part, aim, upto, false);
     bool end = owner < 0;                            // (u z rounded up to all of z): the last token with a weight
     if (end) owner = first_over(part, aim, upto, true);
     if (owner != rank) return;
     int k = -1;
     for (int at = 0; at < blocks && k < 0 && !end; at += 32) {
-        const double x = at + lane < blocks ? sh.block[at + lane].value() : 0.0;
+        const Sum x = at + lane < blocks ? sh.block[at + lane] : Sum{0.f, 0.f};
         const int f = first_over(x, aim, upto, false);
         if (f >= 0) k = at + f;
     }
@@ -469,9 +606,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         }
         k = max(k, 0);
     }
-    auto weight = [&](int at) { return at >= mine ? 0.f : pending ? left(at, w[at], q_row ? q_row[at] : 0.f) : w[at]; };
-    auto pick = [&](double x) {                      // the lane
-        double before = upto;
+    auto weight = [&](int at) { return at >= mine ? 0.f : pending ? left(at) : w[at]; };
+    auto pick = [&](const Sum& x) {                  // the lane
+        Sum before = upto;
         int at = end ? -1 : first_over(x, aim, before, false);
         if (at < 0) {
             end = true;
@@ -481,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         return at;
     };
     Sum mine_of_32{0.f, 0.f};
-    if (pending && q_row) {                          // (a row in global memory: read along it, a piece at a time)
+    if (pending) {                          // (a row in global memory: read along it, a piece at a time)
         float x[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = weight(k * kBlock + 32 * i + lane);
@@ -493,9 +630,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     } else {                                         // each lane's reads askew, so that the lanes lie in different banks
         for (int i = 0; i < 32; ++i) mine_of_32.add(weight(k * kBlock + lane * 32 + ((i + lane) & 31)));
     }
-    const int piece = pick(mine_of_32.value());
+    const int piece = pick(mine_of_32);
     const int from = k * kBlock + piece * 32;
-    const int at = pick(static_cast<double>(weight(from + lane)));
+    const int at = pick(Sum{weight(from + lane), 0.f});
     if (lane == 0) a.next_tokens[b] = v0 + from + at;
 }
 
