@@ -598,9 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 continue;
             }
             if (tells) __stcg(a.stats + static_cast<long long>(u->part) * kUnitRows + unit_row, make_float2(M, L));
-            __threadfence();
             bar_sync(1, kSoftmax);
             if (tid == 32 * kSoftmaxWarp) {
+                __threadfence();                             // (what the others wrote ahead of the barrier goes with it)
                 const int before = atomic_add_acq_rel_gpu(a.counters + u->first_cta, 1);
                 const bool last = before == u->pieces - 1;
                 if (last) st_relaxed_gpu(a.counters + u->first_cta, 0);   // as the next call finds it
@@ -608,7 +608,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             }
             bar_sync(1, kSoftmax);
             if (ctl_i[1] && !idle) {
-                __threadfence();
                 float most = -INFINITY, sum = 0.f;
 #pragma unroll 4
                 for (int i = 0; i < u->pieces; ++i) most = fmaxf(most, __ldcg(a.stats + static_cast<long long>(u->part_of(i)) * kUnitRows + unit_row).x);

@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 for (int e = 0; e < 2; ++e)
                     __stcg(a.stats + static_cast<long long>(w.part) * kRows + row_lo + 8 * e, make_float2(M[e], L[e]));
             }
-            __threadfence();
             __syncwarp();
             if (lane == 0) {
+                __threadfence();                     // (what the warp wrote ahead of its barrier goes with it)
                 const int before = atomic_add_acq_rel_gpu(a.counters + w.first_cta, 1);
                 const bool last = before == w.pieces - 1;
                 if (last) st_relaxed_gpu(a.counters + w.first_cta, 0);     // as the next call finds it
@@ -358,7 +358,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const bool last = shared_i[1];
         if (last) {
             // every piece is there: each warp joins its part of the columns
-            __threadfence();
             float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
             for (int i = 0; i < w.pieces; ++i)
 #pragma unroll

@@ -38,6 +38,7 @@ struct VerifyArgs {
     long long ld, ldp;
     int B, T, max_tokens, V, ld_path;
     int cluster, share;                 // CTAs of a sequence; weights of each, a multiple of kBlock
+    int ahead;                          // whether there is room for the row ahead
     unsigned int* status;
 };
 
@@ -203,10 +204,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 3) verify_kernel(const VerifyArgs a) {
     using K = Kind<DT>;
-    // This CTA's logits as they lie in memory, in the end of what the weights take; then the weights.
-    extern __shared__ float4 w4[];
-    float* const w = reinterpret_cast<float*>(w4);
-    char* const raw = reinterpret_cast<char*>(w4) + a.share * (4 - K::kSize);
+    // Two buffers of this CTA's logits as they lie in memory: of the node's row, and of the row the walk goes on with if it keeps the
+    // node's first draft, which is on its way meanwhile. The weights come where both are (16 bits) or where the row is.
+    extern __shared__ float4 buffers[];
+    auto buffer = [&](int i) { return reinterpret_cast<char*>(buffers) + i * a.share * K::kSize; };
+    int cur = 0;                                     // the node's row
+    char* raw = buffer(0);
+    float4* w4 = buffers;
+    float* w = reinterpret_cast<float*>(buffers);
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0, b = blockIdx.x / C;
@@ -342,6 +347,39 @@ __global__ void __launch_bounds__(kThreads, 3) verify_kernel(const VerifyArgs a)
             x = fmaxf(x, o);
         }
     };
+    // Brings this CTA's part of a row to a buffer: on its way when the call returns, there after arrived(). Returns false, with nothing
+    // done, for the row ahead where it cannot be copied in words.
+    bool ready = false;
+    auto bring = [&](int i, int buf) {
+        const char* const from = static_cast<const char*>(a.logits) + ((s0 + i) * a.ld + v0) * K::kSize;
+        char* const to = buffer(buf);
+        const bool aligned = (reinterpret_cast<uintptr_t>(from) & 15u) == 0;
+        if (!aligned && K::kSize == 2 && buf != cur) return false;
+        for (int c = tid * 8; c < a.share; c += kThreads * 8) {
+            if ((aligned || K::kSize == 4) && c + 8 <= mine) {
+                const uint32_t at = smem_u32(to + c * K::kSize);
+                const char* const p = from + static_cast<long long>(c) * K::kSize;
+                if (aligned) {
+#pragma unroll
+                    for (int k = 0; k < K::kSize / 2; ++k)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 16 * k), "l"(p + 16 * k) : "memory");
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 4 * k), "l"(p + 4 * k) : "memory");
+                }
+            } else {
+                const typename K::Eight e = K::load(from, c, mine, aligned);
+#pragma unroll
+                for (int k = 0; k < K::kWords; k += 4)
+                    *reinterpret_cast<uint4*>(to + c * K::kSize + 4 * k) = make_uint4(e.u[k], e.u[k + 1], e.u[k + 2], e.u[k + 3]);
+            }
+        }
+        return true;
+    };
+    auto arrived = [&] {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+    };
     float top = 0.f;
     int top_at = 0, was = 0;
     // a draft that was not kept: its row, 1 / sum of the weights it is taken from, its place among the CTA's
@@ -359,30 +397,20 @@ __global__ void __launch_bounds__(kThreads, 3) verify_kernel(const VerifyArgs a)
     };
     while (fine) {
         // ---- the node's row: its logits, scaled, in shared memory; their maximum
-        const char* const from = static_cast<const char*>(a.logits) + ((s0 + node) * a.ld + v0) * K::kSize;
-        const bool aligned = (reinterpret_cast<uintptr_t>(from) & 15u) == 0;
-        constexpr int kBatch = DT == WQ4_FP32 ? 2 : 4;
+        if (!ready) bring(node, cur);
+        arrived();
+        raw = buffer(cur);
+        if constexpr (K::kSize == 4) w4 = reinterpret_cast<float4*>(raw), w = reinterpret_cast<float*>(raw);
+        next_draft();
+        ready = false;
+        if (j < n && a.ahead) ready = bring(j, cur ^ 1);
         uint32_t most = K::minus_inf();
-        for (int i0 = tid * 8; i0 < a.share; i0 += kThreads * 8 * kBatch) {
-            typename K::Eight e[kBatch];
+        for (int i = tid * 8; i < a.share; i += kThreads * 8) {
+            const typename K::Eight e = K::load(raw, i, a.share, true);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int i = i0 + k * kThreads * 8;
-                if (i < a.share) e[k] = K::load(from, i, mine, aligned);
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int i = i0 + k * kThreads * 8;
-                if (i >= a.share) break;
-#pragma unroll
-                for (int c = 0; c < K::kWords; ++c) most = K::larger(most, e[k].u[c]);
-#pragma unroll
-                for (int c = 0; c < K::kWords; c += 4)
-                    *reinterpret_cast<uint4*>(raw + i * K::kSize + 4 * c) = make_uint4(e[k].u[c], e[k].u[c + 1], e[k].u[c + 2], e[k].u[c + 3]);
-            }
+            for (int c = 0; c < K::kWords; ++c) most = K::larger(most, e.u[c]);
         }
         float m_raw = K::largest(most);
-        next_draft();
 #pragma unroll
         for (int d = 16; d; d >>= 1) m_raw = fmaxf(m_raw, __shfl_xor_sync(0xffffffffu, m_raw, d));
         if (lane == 0) sh.top[warp] = m_raw;
@@ -453,14 +481,19 @@ __global__ void __launch_bounds__(kThreads, 3) verify_kernel(const VerifyArgs a)
                 if (rank == 0 && tid == 0) path[kept] = j;
                 ++kept;
                 node = j;
+                if (ready) cur ^= 1;
                 __syncthreads();                     // (the logits, and sh.top, are written again)
                 continue;
             }
         }
         // ---- the weights themselves, and their sum
-        // (A round of blocks is read by all before it is written: the weights of one round end ahead of the logits of the next.)
-        for (int k0 = 0; k0 < a.share / kBlock; k0 += kWarps) {
-            const int k = k0 + warp;
+        // (A round of blocks is read by all before it is written, and 16-bit logits in the second buffer are ahead of the weights
+        // that replace them if the first round comes first, those in the first buffer if the last one does.)
+        arrived();
+        ready = false;
+        const int rounds = (a.share / kBlock + kWarps - 1) / kWarps;
+        for (int round = 0; round < rounds; ++round) {
+            const int k = (cur ? round : rounds - 1 - round) * kWarps + warp;
             typename K::Eight e[4];
             if (k * kBlock < mine) {
 #pragma unroll
@@ -646,7 +679,8 @@ int go_verify(const Runtime& rt, const VerifyArgs& a, wq4_stream_t st) {
         return -1;
     });
     if (ok <= 0) return WQ4_ERR_CUDA;
-    return launch(rt, kern, dim3(static_cast<unsigned>(a.B) * a.cluster), kThreads, a.share * 4, a.cluster, st, a);
+    const int smem = a.share * (DT == WQ4_FP32 && a.ahead ? 8 : 4);
+    return launch(rt, kern, dim3(static_cast<unsigned>(a.B) * a.cluster), kThreads, smem, a.cluster, st, a);
 }
 
 }  // namespace
@@ -673,10 +707,11 @@ extern "C" int wq4_verify_drafts(const void* logits, long long ld, const long lo
     Runtime rt;
     if (const int rc = runtime(&rt)) return rc;
     VerifyArgs a{logits, tokens, parents, starts, draft_probs, temperature, uniforms, final_uniforms, accepted, path, next_tokens,
-                 ld, ldp, B, T, max_tokens, V, ld_path, 1, 0, rt.status};
+                 ld, ldp, B, T, max_tokens, V, ld_path, 1, 0, 0, rt.status};
     while (a.cluster < kMaxCluster && (V > 16 * kBlock * a.cluster || (2LL * a.cluster * B <= rt.sm_count && V > 2 * kBlock * a.cluster)))
         a.cluster *= 2;
     a.share = ((V + a.cluster - 1) / a.cluster + kBlock - 1) / kBlock * kBlock;
+    a.ahead = dtype != WQ4_FP32 || a.share <= kMaxShare / 2;
     if (rt.trace) std::fprintf(stderr, "wq4: verify_drafts B=%d tokens=%d V=%d cluster=%d\n", B, max_tokens, V, a.cluster);
     if (dtype == WQ4_BF16) return go_verify<WQ4_BF16>(rt, a, stream);
     if (dtype == WQ4_FP16) return go_verify<WQ4_FP16>(rt, a, stream);
