@@ -21,8 +21,7 @@
 namespace wq4 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 512;        // of a CTA, with few sequences; 256 with many
 constexpr int kMaxCluster = 8;
 constexpr int kBlock = 1024;            // weights whose sums are held while the next token is searched
 constexpr int kMaxShare = 50 * 1024;    // weights of a CTA: 200 KB
@@ -122,7 +121,7 @@ constexpr int kHeld = 128;              // drafts of a sequence whose parents, t
 
 struct Shared {
     Part part[2][kMaxCluster];          // [turn][CTA]: written by the others
-    float top[kWarps], sum[kWarps];
+    float top[kMaxThreads / 32], sum[kMaxThreads / 32];
     int top_at;
     Sum block[kMaxShare / kBlock];
     long long tokens[kHeld];
@@ -201,8 +200,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 3) verify_kernel(const VerifyArgs a) {
+template <int DT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verify_kernel(const VerifyArgs a) {
+    constexpr int kThreads = THREADS, kWarps = kThreads / 32;
     using K = Kind<DT>;
     // Two buffers of this CTA's logits as they lie in memory: of the node's row, and of the row the walk goes on with if it keeps the
     // node's first draft, which is on its way meanwhile. The weights come where both are (16 bits) or where the row is.
@@ -669,9 +669,9 @@ __global__ void __launch_bounds__(kThreads, 3) verify_kernel(const VerifyArgs a)
     if (lane == 0) a.next_tokens[b] = v0 + from + at;
 }
 
-template <int DT>
+template <int DT, int THREADS>
 int go_verify(const Runtime& rt, const VerifyArgs& a, wq4_stream_t st) {
-    auto kern = verify_kernel<DT>;
+    auto kern = verify_kernel<DT, THREADS>;
     static PerDevice ready;
     const int ok = ready.get(rt.device, [&]() -> int {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShare * 4) == cudaSuccess) return 1;
@@ -680,7 +680,15 @@ int go_verify(const Runtime& rt, const VerifyArgs& a, wq4_stream_t st) {
     });
     if (ok <= 0) return WQ4_ERR_CUDA;
     const int smem = a.share * (DT == WQ4_FP32 && a.ahead ? 8 : 4);
-    return launch(rt, kern, dim3(static_cast<unsigned>(a.B) * a.cluster), kThreads, smem, a.cluster, st, a);
+    return launch(rt, kern, dim3(static_cast<unsigned>(a.B) * a.cluster), THREADS, smem, a.cluster, st, a);
+}
+// As long as two CTAs of 512 threads to an SM hold all sequences at once, a walk over large shares is soonest done by them; else three of
+// 256 walk more of them at a time, or meet sooner (32 trees of 16 over 131072: 32.7 us with 512 threads, 36.4 with 256; 192 chains of
+// 6: 148 and 114; one chain of 5 over 32001, shares of 4096: 20.5 and 17.9).
+template <int DT>
+int go_verify(const Runtime& rt, const VerifyArgs& a, wq4_stream_t st) {
+    const bool few = static_cast<long long>(a.B) * a.cluster <= 2 * rt.sm_count && a.share > 8192;
+    return few ? go_verify<DT, kMaxThreads>(rt, a, st) : go_verify<DT, kMaxThreads / 2>(rt, a, st);
 }
 
 }  // namespace
