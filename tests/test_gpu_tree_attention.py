@@ -173,6 +173,65 @@ def test_trees_over_long_contexts(lib, dtype, D, counts, context, Hq, Hk):
     c.compare(out, lse, *parts)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("D", [8, 40, 64, 72, 80, 96, 128])
+@pytest.mark.parametrize("counts,context", [([12, 3, 40], [130, 0, 300]), ([5, 6, 0, 4, 5, 1], [33, 700, 9, 127, 128, 129])])
+def test_many_rows_of_head_sizes(lib, dtype, D, counts, context):
+    """More rows than one tile of 16 takes, of a whole batch: tiles of 128 rows, filled twice, once and in part."""
+    Case(counts, context, 16, 2, D, 16, dtype, True, seed=D, extra_rows=2).check(lib)
+
+
+@pytest.mark.parametrize("page", [16, 48, 64, 80, 128, 256])
+@pytest.mark.parametrize("masked", [False, True])
+def test_many_rows_of_page_sizes(lib, page, masked):
+    Case([9, 20, 7], [page - 2, 3 * page + 1, 2 * page], 8, 2, 128, page, "bf16", masked, seed=page).check(lib)
+
+
+@pytest.mark.parametrize("group", [3, 7, 12, 64, 129])
+def test_many_rows_of_groups(lib, group):
+    """Rows of one token in two tiles, and tokens that end inside one."""
+    Case([11, 2, 6, 1, 9], [60, 190, 0, 500, 128], group * 2, 2, 64, 32, "bf16", True, seed=group).check(lib)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 2.5, 40.0])
+def test_many_rows_scales(lib, scale):
+    Case([11, 20, 6], [60, 190, 0], 8, 2, 64, 32, "bf16", True).check(lib, scale=scale)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38])
+def test_many_rows_stale_places(lib, value):
+    c = Case([30, 41, 3], [130, 7, 500], 16, 2, 64, 16, "bf16", True, slack=3)
+    want = c.run(lib)
+    c.stale(value)
+    got = c.run(lib)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_many_rows_values_that_are_not_finite(lib, dtype):
+    """Drafted values, keys and the context's, in tiles that one CTA takes and that several share."""
+    c = Case([30, 41, 9], [140, 3000, 0], 16, 2, 128, 16, dtype, True, seed=7)
+
+    def at(b, place):
+        return c.table[b, place // 16].long(), place % 16
+    c.v[(*at(0, 140 + 2), 0, 3)] = float("inf")
+    c.v[(*at(0, 140 + 3), 1, 100)] = float("nan")
+    c.v[(*at(1, 3000 + 7), 0, 127)] = -float("inf")
+    c.k[(*at(1, 3000 + 9), 1, 5)] = float("nan")
+    c.v[(*at(1, 17), 1, 64)] = float("nan")
+    out, lse = c.check(lib)
+    assert not torch.isfinite(out).all() and torch.isfinite(out).any()
+
+
+def test_many_rows_that_see_nothing(lib):
+    c = Case([40, 30], [0, 20], 8, 2, 64, 16, "bf16", True)
+    for t in (1, 39, 45):
+        c.seen[t] = np.zeros(len(c.seen[t]), dtype=bool)
+    c.mask = words(c.seen, 70, 40)
+    out, lse = c.check(lib)
+    assert (out[1] == 0).all() and torch.isneginf(lse[39]).all()
+
+
 def test_many_sequences(lib):
     rng = np.random.default_rng(0)
     counts, context = rng.integers(0, 4, 400).tolist(), rng.integers(0, 90, 400).tolist()
@@ -243,8 +302,9 @@ def test_strided_tensors(lib):
     assert torch.equal(out, want) and (wide[:, :, 64:] == 0).all()
 
 
-def test_the_same_bits_every_time_and_the_workspace_lasts(lib):
-    c = Case([1, 9, 2], [5000, 800, 90], 16, 2, 128, 16, "bf16", True)
+@pytest.mark.parametrize("counts", [[1, 1, 1], [1, 9, 2], [30, 9, 64]])
+def test_the_same_bits_every_time_and_the_workspace_lasts(lib, counts):
+    c = Case(counts, [5000, 800, 90], 16, 2, 128, 16, "bf16", len(set(counts)) > 1)
     ws = lib.alloc_workspace(lib.tree_attention_workspace_bytes(3, c.most, 16, 2, 128))
     first = c.run(lib, workspace=ws)
     for _ in range(5):
@@ -305,14 +365,15 @@ def test_a_workspace_too_small_is_refused(lib):
     assert e.value.status == lib.ERR_WORKSPACE
 
 
-def test_a_wait_that_runs_out_is_reported(lib):
+@pytest.mark.parametrize("counts", [[1, 2], [40, 30]])
+def test_a_wait_that_runs_out_is_reported(lib, counts):
     """One wait per CTA that nothing ends: the call stops early, and the next one is as ever."""
-    c = Case([1, 2], [900, 90], 8, 2, 64, 16, "bf16", False)
+    c = Case(counts, [900, 90], 8, 2, 64, 16, "bf16", False)
     want = c.run(lib)
     lib.set_option(lib.OPT_TEST_STALL, 1)
     lib.set_option(lib.OPT_TIMEOUT_CYCLES, 2000000)
     try:
-        lib.tree_attention(c.q, c.k, c.v, c.table, c.starts, c.context, max_tokens=2)
+        lib.tree_attention(c.q, c.k, c.v, c.table, c.starts, c.context, max_tokens=c.most)
         assert lib.get_last_error() == lib.ERR_TIMEOUT
     finally:
         lib.set_option(lib.OPT_TEST_STALL, 0)

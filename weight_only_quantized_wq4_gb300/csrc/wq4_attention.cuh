@@ -40,14 +40,14 @@ struct AttnArgs {
 
 struct Scan {
     unsigned long long sum[32], part[32], before;
-    int b;
+    int longest[32], b;
 };
 
 // The work in order: sequence, kv head, tile of `rows` rows, tile of `places` places. A CTA walks over its share, unit by unit
 // (one sequence, kv head and tile of rows); every role of the CTA does so by itself, from the same start.
 struct Walk {
     const AttnArgs& a;
-    const int places, unit_rows;
+    const int places, unit_rows, least;              // least: tiles that are worth a CTA, where a unit has as many
     // the unit at hand
     int b, h, row0, rows, context, count, len;       // rows: of the whole problem (count G); len: places
     int t0, t1;                                      // this CTA's tiles of it
@@ -56,7 +56,7 @@ struct Walk {
     unsigned pos, end, chunk, base, work;            // base, work: of the sequence at hand
     int tiles, row_tiles, cta;
 
-    __device__ Walk(const AttnArgs& args, int places_, int rows_) : a(args), places(places_), unit_rows(rows_) {}
+    __device__ Walk(const AttnArgs& args, int places_, int rows_, int least_) : a(args), places(places_), unit_rows(rows_), least(least_) {}
 
     // Sequence i's lengths; its number of tiles, 0 where there is nothing to do or the lengths cannot be.
     __device__ __forceinline__ unsigned long long load(int i, int& n, int& c) const {
@@ -87,24 +87,28 @@ struct Walk {
         };
         // the sum of what each thread loads of all sequences; with no more of those than threads, their running sum too
         unsigned long long own = 0, mine = 0;
+        int longest = 0;                             // tiles of a unit
         for (int i = tid; i < a.B; i += threads) {
             own = load(i, n, c);
             mine += own;
+            if (own) longest = max(longest, static_cast<int>((static_cast<unsigned>(c) + n + places - 1) / places));
         }
         const unsigned long long upto = scan(mine);
-        if (lane == 31) sc.sum[warp] = upto;
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 31) sc.sum[warp] = upto, sc.longest[warp] = longest;
         __syncthreads();
         unsigned long long total = 0, ahead = 0;
         for (int i = 0; i < warps; ++i) {
             if (i == warp) ahead = total;
             total += sc.sum[i];
+            longest = max(longest, sc.longest[i]);
         }
         if (total > 0x7fffffffull) {
             if (tid == 0) atomicOr(a.status, kStatusBadIndex);
             return false;
         }
         cta = blockIdx.x;
-        chunk = max((static_cast<unsigned>(total) + a.grid - 1) / a.grid, 1u);
+        chunk = max((static_cast<unsigned>(total) + a.grid - 1) / a.grid, static_cast<unsigned>(min(least, longest)));
         const unsigned long long lo = static_cast<unsigned long long>(cta) * chunk;
         if (lo >= total) return false;
         if (a.B <= threads) {

@@ -18,6 +18,7 @@ namespace wq4 {
 namespace {
 
 constexpr int kTile = 128;              // places of a tile
+constexpr int kLeast = 4;               // tiles worth a CTA (8 tokens over 2000 places: 19 us, with 1 26)
 constexpr int kLanes = 128;             // rows of a stream's tile
 constexpr int kUnitRows = 2 * kLanes;
 constexpr int kSoftmaxWarp = 4;         // the first of sixteen; before them: copies, MMAs, two that look at drafted values
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(ctl_i[3]);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Walk w(a, kTile, kUnitRows);
+    Walk w(a, kTile, kUnitRows, kLeast);
     bool work = w.begin(scan, tid, kThreads);                // (all threads of the CTA alike)
     if (s_base & 1023u) {
         if (tid == 0) atomicOr(a.status, kStatusTimeout);

@@ -16,6 +16,7 @@ namespace wq4 {
 namespace {
 
 constexpr int kTile = 64;               // places of a tile
+constexpr int kLeast = 2;               // tiles worth a CTA (one sequence over 600 places: 9.5 us, with 1 9.7, with 4 12.9)
 constexpr int kRows = 16;               // rows of a unit
 constexpr int kWarps = 4;               // that compute: 16 places of each tile each
 constexpr int kThreads = 32 * (kWarps + 1);
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // This CTA's share of all the tiles.
-    Walk w(a, kTile, kRows);
+    Walk w(a, kTile, kRows, kLeast);
     if (!w.begin(scan, tid, kThreads)) return;                          // (all threads of the CTA alike)
     int issued = 0;
     const WaitCtl ctl{abort_flag, a.status, a.timeout_cycles};
@@ -436,8 +437,17 @@ Space space_of(int grid, int D, int rows) {
     return s;
 }
 
-// The kernel with tiles of 128 rows, where the rows of a kv head fill more than one of 16.
-bool use_tiles(int max_tokens, int group, int D) { return static_cast<long long>(max_tokens) * group > kRows && D <= 128; }
+// Whether the kernel with tiles of 128 rows applies: where the rows of a kv head fill more than one of 16 (rows of 16 read the keys and
+// values again for each 16).
+bool can_tile(int max_tokens, int group, int D) { return static_cast<long long>(max_tokens) * group > kRows && D <= 128; }
+
+// And whether it is the sooner done: but where there are few units of 16 rows, over contexts that L2 holds, their latency counts and not
+// what is read (8 tokens, 32 heads over 8: 12.5 us over 2000 places by rows of 16, 19.2 by tiles, 22 and 36 over 8000; 16
+// tokens over 2000: 17.6 and 19.5; eight sequences of 8: 35 and 30). Contexts are in device memory; the table's width bounds them.
+bool should_tile(const AttnArgs& a) {
+    const long long units = static_cast<long long>(a.B) * a.Hk * ((static_cast<long long>(a.max_tokens) * a.G + kRows - 1) / kRows);
+    return units > 32 || static_cast<long long>(a.table_width) * a.cache.page_size > 16384;
+}
 
 int check_heads(int B, int max_tokens, int q_heads, int kv_heads, int D) {
     if (B < 0 || max_tokens < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads || D < 1) return WQ4_ERR_INVALID;
@@ -457,7 +467,7 @@ int wq4_tree_attention_workspace_bytes(int B, int max_tokens, int q_heads, int k
     if (const int rc = check_heads(B, max_tokens, q_heads, kv_heads, D)) return rc;
     Runtime rt;
     if (const int rc = runtime(&rt)) return rc;
-    *bytes = space_of(rt.sm_count, D, use_tiles(max_tokens, q_heads / kv_heads, D) ? tiles_rows() : kRows).bytes;
+    *bytes = space_of(rt.sm_count, D, can_tile(max_tokens, q_heads / kv_heads, D) ? tiles_rows() : kRows).bytes;
     return WQ4_OK;
 }
 
@@ -490,10 +500,6 @@ int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_
     if (const int rc = runtime(&rt)) return rc;
     AttnArgs a{};
     a.grid = rt.sm_count;
-    // (the tiles' softmax takes maxima ahead of the scale; the other kernel, whose parts are smaller, after it)
-    const bool tiles = use_tiles(max_tokens, q_heads / kv_heads, D) && scale > 1e-30f;
-    const Space sp = space_of(a.grid, D, tiles ? tiles_rows() : kRows);
-    if (!workspace || workspace_bytes < sp.bytes) return WQ4_ERR_WORKSPACE;
     a.q = static_cast<const uint16_t*>(Q);
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
@@ -507,10 +513,14 @@ int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_
     a.B = B, a.T = T, a.max_tokens = max_tokens, a.Hq = q_heads, a.Hk = kv_heads, a.G = q_heads / kv_heads, a.D = D;
     a.max_rows = static_cast<int>(std::min(static_cast<long long>(max_tokens) * a.G, 1LL << 20));
     a.scale_log2 = scale * 1.4426950408889634f;
+    a.test_stall = rt.test_stall;
+    // (the tiles' softmax takes maxima ahead of the scale; the other kernel, whose parts are smaller, after it)
+    const bool can = can_tile(max_tokens, q_heads / kv_heads, D), tiles = can && scale > 1e-30f && should_tile(a);
+    if (!workspace || workspace_bytes < space_of(a.grid, D, can ? tiles_rows() : kRows).bytes) return WQ4_ERR_WORKSPACE;
+    const Space sp = space_of(a.grid, D, tiles ? tiles_rows() : kRows);
     a.counters = static_cast<int*>(workspace);
     a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + sp.stats);
     a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.parts);
-    a.test_stall = rt.test_stall;
     a.status = rt.status;
     a.timeout_cycles = rt.timeout_cycles;
     a.box = 16;                                      // the places of one copy: they lie in one page
