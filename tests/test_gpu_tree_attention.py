@@ -337,23 +337,25 @@ def test_captured_with_lengths_that_change(lib):
     assert lib.get_last_error() == 0
 
 
-def test_pages_and_lengths_that_cannot_be_are_reported(lib):
-    c = Case([2, 2], [50, 20], 4, 2, 64, 16, "bf16", False)
+@pytest.mark.parametrize("n,Hq", [(2, 4), (40, 16)])
+def test_pages_and_lengths_that_cannot_be_are_reported(lib, n, Hq):
+    c = Case([n, n], [50, 20], Hq, 2, 64, 16, "bf16", False)
     args = (c.q, c.k, c.v)
-    good = lib.tree_attention(*args, c.table, c.starts, c.context, max_tokens=2)
+    good = lib.tree_attention(*args, c.table, c.starts, c.context, max_tokens=n)
     assert lib.get_last_error() == 0
-    for page in (-1, c.k.shape[0], 2 ** 31 - 1, -2 ** 31):
+    for page in (-1, c.k.shape[0], c.k.shape[0] + 1, 2 ** 31 - 1, -2 ** 31):
         table = c.table.clone()
         table[0, 1] = page
-        lib.tree_attention(*args, table, c.starts, c.context, max_tokens=2)
+        lib.tree_attention(*args, table, c.starts, c.context, max_tokens=n)
         assert lib.get_last_error() == lib.ERR_INVALID, page
-    for context in ([50, -1], [c.table.shape[1] * 16 - 1, 20], [2 ** 31 - 1, 20]):
-        lib.tree_attention(*args, c.table, c.starts, torch.tensor(context, dtype=torch.int32, device="cuda"), max_tokens=2)
+    for context in ([50, -1], [c.table.shape[1] * 16 - n + 1, 20], [2 ** 31 - 1, 20]):
+        lib.tree_attention(*args, c.table, c.starts, torch.tensor(context, dtype=torch.int32, device="cuda"), max_tokens=n)
         assert lib.get_last_error() == lib.ERR_INVALID, context
-    for starts in ([0, 2, 5], [-1, 2, 4], [0, 3, 4], [0, 4, 2], [2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31 - 1], [-2 ** 31, 2 ** 31 - 1, 4]):
-        lib.tree_attention(*args, c.table, torch.tensor(starts, dtype=torch.int32, device="cuda"), c.context, max_tokens=2)
+    for starts in ([0, n, 2 * n + 1], [-1, n, 2 * n], [0, n + 1, 2 * n], [0, 2 * n, n], [2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31 - 1],
+                   [-2 ** 31, 2 ** 31 - 1, 2 * n]):
+        lib.tree_attention(*args, c.table, torch.tensor(starts, dtype=torch.int32, device="cuda"), c.context, max_tokens=n)
         assert lib.get_last_error() == lib.ERR_INVALID, starts
-    assert torch.equal(good, lib.tree_attention(*args, c.table, c.starts, c.context, max_tokens=2))
+    assert torch.equal(good, lib.tree_attention(*args, c.table, c.starts, c.context, max_tokens=n))
     assert lib.get_last_error() == 0
 
 

@@ -203,19 +203,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 const int n = w.t1 - w.t0, lag = two() ? 1 : 2;
                 // The page of this lane's places of a tile: looked up a tile ahead of its keys and kept for its values.
                 auto place_of = [&](int tile) { return (w.t0 + tile) * kTile + box * a.box; };
+                auto there = [&](int tile) { return mine && tile < n && place_of(tile) < w.len; };
                 auto find = [&](int tile) {
-                    const int place = place_of(tile);
-                    return mine && tile < n && place < w.len ? a.table[static_cast<long long>(w.b) * a.ld_table + place / a.cache.page_size]
-                                                             : a.cache.pages;    // past the last place: outside the tensor, zeros
+                    return there(tile) ? a.table[static_cast<long long>(w.b) * a.ld_table + place_of(tile) / a.cache.page_size] : 0;
                 };
                 int ahead = find(0), page[3] = {};           // of tile j + 1; of j, j - 1, j - 2
                 for (int j = 0; j < n + lag && ok; ++j) {
                     page[2] = page[1], page[1] = page[0], page[0] = ahead;
                     ahead = find(j + 1);
-                    if (page[0] < 0 || page[0] > a.cache.pages) {
-                        atomicOr(a.status, kStatusBadIndex);
-                        page[0] = a.cache.pages;
-                    }
+                    if (static_cast<unsigned>(page[0]) >= static_cast<unsigned>(a.cache.pages)) atomicOr(a.status, kStatusBadIndex), page[0] = a.cache.pages;
+                    if (!there(j)) page[0] = a.cache.pages;  // past the last place: outside the tensor, zeros
                     for (int kind = 0; kind < 2; ++kind) {               // 0: values of j - lag, 1: keys of j
                         if (kind ? j >= n : j < lag) continue;
                         if (lane == 0) ok = mbar_wait(s_empty + 8 * ring.slot, ring.phase ^ 1, ctl);

@@ -94,22 +94,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         int slot = 0;
         uint32_t phase = 1;
         bool ok = true;
+        const int boxes = kTile / a.box, nj = boxes * 2 * a.copies;
+        const int part = lane % (2 * a.copies), box = lane / (2 * a.copies);     // lane: (box, panel, keys or values) of a tile
+        const bool values = part & 1;
         while (ok && w.next()) {
-            const int boxes = kTile / a.box, nj = boxes * 2 * a.copies;
+            // The page of this lane's places, looked up a tile ahead.
+            auto there = [&](int t) { return lane < nj && t < w.t1 && t * kTile + box * a.box < w.len; };
+            auto find = [&](int t) {
+                return there(t) ? a.table[static_cast<long long>(w.b) * a.ld_table + (t * kTile + box * a.box) / a.cache.page_size] : 0;
+            };
+            int ahead = find(w.t0);
             for (int t = w.t0; t < w.t1 && ok; ++t) {
-                // lane: (box, keys or values, panel) of the tile
-                const int part = lane % (2 * a.copies), box = lane / (2 * a.copies), place = t * kTile + box * a.box;
-                int page = a.cache.pages;            // past the last place: outside the tensor, zeros
-                int at = 0;
-                if (lane < nj && place < w.len) {
-                    const int i = place / a.cache.page_size;
-                    page = a.table[static_cast<long long>(w.b) * a.ld_table + i];
-                    at = place - i * a.cache.page_size;
-                    if (page < 0 || page >= a.cache.pages) {
-                        atomicOr(a.status, kStatusBadIndex);
-                        page = a.cache.pages;
-                    }
-                }
+                int page = ahead;
+                ahead = find(t + 1);
+                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.cache.pages)) atomicOr(a.status, kStatusBadIndex), page = a.cache.pages;
+                if (!there(t)) page = a.cache.pages;         // past the last place: outside the tensor, zeros
                 if (lane == 0) ok = mbar_wait(s_empty + 8 * slot, phase, ctl);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
@@ -117,11 +116,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 if (lane == 0) mbar_arrive_expect_tx(bar, C::kStage);
                 __syncwarp();
                 if (lane < nj) {
-                    const bool values = part & 1;
                     const int panel = part >> 1;
                     const uint32_t dst = s_ring + slot * C::kStage + (values ? C::kHalf : 0) + box * a.box * kDp * 2 +
                                          panel * a.box * 128;
-                    tma_load_5d(dst, values ? &a.v_map : &a.k_map, bar, 64 * panel, at, 0, w.h, page, pol);
+                    tma_load_5d(dst, values ? &a.v_map : &a.k_map, bar, 64 * panel, (t * kTile + box * a.box) % a.cache.page_size, 0, w.h, page, pol);
                 }
                 ++issued;
                 if (++slot == C::kStages) slot = 0, phase ^= 1;
