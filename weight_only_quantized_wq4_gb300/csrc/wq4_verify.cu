@@ -166,6 +166,17 @@ struct Kind {
         }
         return e;
     }
+    // eight in a row in shared memory, filled to whole eights
+    static __device__ __forceinline__ Eight held(const char* raw, int i) {
+        Eight e;
+        const uint4* q = reinterpret_cast<const uint4*>(raw + i * kSize);
+#pragma unroll
+        for (int k = 0; k < kWords / 4; ++k) {
+            const uint4 x = q[k];
+            e.u[4 * k] = x.x, e.u[4 * k + 1] = x.y, e.u[4 * k + 2] = x.z, e.u[4 * k + 3] = x.w;
+        }
+        return e;
+    }
     static __device__ __forceinline__ void values(const Eight& e, float (&v)[8]) {
         if constexpr (DT == WQ4_FP32) {
 #pragma unroll
@@ -406,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
         if (j < n && a.ahead) ready = bring(j, cur ^ 1);
         uint32_t most = K::minus_inf();
         for (int i = tid * 8; i < a.share; i += kThreads * 8) {
-            const typename K::Eight e = K::load(raw, i, a.share, true);
+            const typename K::Eight e = K::held(raw, i);
 #pragma unroll
             for (int c = 0; c < K::kWords; ++c) most = K::larger(most, e.u[c]);
         }
@@ -424,7 +435,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
         if (greedy) {                                // its place
             for (int i = tid * 8; i < mine; i += kThreads * 8) {
                 float x[8];
-                K::values(K::load(raw, i, a.share, true), x);
+                K::values(K::held(raw, i), x);
 #pragma unroll
                 for (int c = 7; c >= 0; --c)
                     if (x[c] == m && i + c < mine) atomicMin(&sh.top_at, v0 + i + c);
@@ -440,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
             float s2 = 0.f;
             for (int i = tid * 8; i < a.share; i += kThreads * 8) {
                 float x[8];
-                K::values(K::load(raw, i, a.share, true), x);
+                K::values(K::held(raw, i), x);
 #pragma unroll
                 for (int c = 0; c < 8; c += 2) {
                     s += exp2_fast((x[c] - m_raw) * to2);
@@ -497,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
             typename K::Eight e[4];
             if (k * kBlock < mine) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = K::load(raw, k * kBlock + (32 * i + lane) * 8, a.share, true);
+                for (int i = 0; i < 4; ++i) e[i] = K::held(raw, k * kBlock + (32 * i + lane) * 8);
             }
             __syncthreads();
             if (k * kBlock < mine) {
@@ -507,10 +518,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
                     const int at = k * kBlock + (32 * i + lane) * 8;
                     float x[8];
                     K::values(e[i], x);
+                    if (greedy) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        // (a product and a difference, rounded one by one)
-                        x[c] = greedy ? (v0 + at + c == top_at ? 1.f : 0.f) : expf(__fsub_rn(__fmul_rn(x[c], inv_heat), top));
+                        for (int c = 0; c < 8; ++c) x[c] = v0 + at + c == top_at ? 1.f : 0.f;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) x[c] = expf(__fsub_rn(__fmul_rn(x[c], inv_heat), top));   // (rounded one by one)
                     }
 #pragma unroll
                     for (int c = 0; c < 8; c += 2) s2.add(x[c], x[c + 1]);
