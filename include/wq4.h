@@ -391,7 +391,7 @@ int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_
  *             within the sequence in order, then -1; next_tokens [B].
  * The walk ends with next token -1 at a row that holds a NaN or +inf, or nothing but -inf, for a temperature that is
  * negative, NaN, infinite or so small that the scaled logits overflow, and for a sequence without tokens.
- * Probabilities are fp32, sums over the vocabulary hold 44 bits and more. starts that do not ascend within
+ * Probabilities are fp32, sums over the vocabulary hold 44 bits and more. Results are identical from run to run. starts that do not ascend within
  * T and by at most max_tokens: as in wq4_tree_attention. V <= 400000. B == 0 is a no-op. */
 int wq4_verify_drafts(const void* logits, long long ld, const long long* tokens, const int* parents, const int* starts,
                       int B, int T, int max_tokens, int V, int dtype, const float* draft_probs, long long ldp,
@@ -422,7 +422,8 @@ int wq4_get_last_error(wq4_stream_t stream);
  * counters, and every output column against N. A failed check never faults or waits: the copy
  * reads the tensor's origin (or the blob's first record) instead, a store or workspace access is
  * skipped, the CTA stops at its next pipeline wait, and wq4_get_last_error reports
- * WQ4_ERR_BOUNDS; the call's outputs are then undefined. */
+ * WQ4_ERR_BOUNDS; the call's outputs are then undefined. Slots, pages, lengths and tokens that the attention
+ * operators read from device memory are checked in both builds (WQ4_ERR_INVALID). */
 int wq4_debug_checks(void);
 
 /* The first violation that the last WQ4_ERR_BOUNDS report read back: record[0] = the check site
@@ -454,8 +455,8 @@ int wq4_last_violation(int* record);
  *                           it touches global memory only after that kernel has completed);
  *                           -1 = plain stream order
  *   WQ4_OPT_TEST_STALL      1 = (tests of the failure path) the GEMM, decode and block-scaled
- *                           product kernels make one wait per CTA on a barrier that nothing
- *                           arrives on, and wq4_token_logprobs one per row that a cluster of
+ *                           product and attention kernels make one wait per CTA on a barrier
+ *                           that nothing arrives on, and wq4_token_logprobs one per row that a cluster of
  *                           CTAs shares; it runs out after the WQ4_OPT_TIMEOUT_CYCLES bound,
  *                           the call stops early and wq4_get_last_error reports
  *                           WQ4_ERR_TIMEOUT. Kernels without a bounded wait (norm, gated

@@ -7,6 +7,11 @@
 // Work is split over the caches' lengths: all units' tiles of 64 places lie one after the other, and each CTA takes an
 // equal share of them, whichever units they belong to. A unit that several CTAs share is joined by
 // the CTA that finishes last, from (maximum, sum, O) of each, in the order of the tiles.
+//
+// Bound by memory where there is much to read: 64 single tokens of 32 heads over 8 of 128, 500 to 16000 places, bf16: 331 us in pages of
+// 64 (6.5 TB/s, 96 % of the copy rate) and 353 in pages of 16, a copy for each of which takes the copy engine longer (410 with
+// each page looked up only when its turn came). Few tokens over short contexts are a chain of latencies: one token over
+// 600 places takes 9.4 us, of which 5.7 are there with 60 places too, and the join of the CTAs' parts most of the rest.
 #include <algorithm>
 #include <cstdio>
 
