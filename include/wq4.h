@@ -346,7 +346,7 @@ int wq4_rope_append(const void* Q, long long q_ts, long long q_hs, const void* K
  *   cache     this step's keys and values are in it (wq4_rope_append). k and v 16-byte aligned, strides multiples
  *             of 8; page_size a multiple of 16.
  *   page_table   [B][table_width] int, row stride ld_table: page i of sequence b holds its places from i page_size.
- *             Entries past a sequence's last place are not read.
+ *             Entries past a sequence's last place are not read. A sequence has at most 2^30 places.
  *   starts    [B + 1] int, in DEVICE memory as page_table and context [B] int; 0 <= starts[b] <= starts[b + 1] <= T.
  *   max_tokens   the most tokens that one sequence has in this step.
  *   mask      [T][mask_words] 64-bit words: token i of a sequence sees token j of the same where bit j % 64 of
@@ -362,7 +362,7 @@ int wq4_rope_append(const void* Q, long long q_ts, long long q_hs, const void* K
  *   workspace   wq4_tree_attention_workspace_bytes(...) bytes on the current device, 16-byte aligned, zero-filled once
  *             when allocated; every completed call leaves it fit for the next. Calls that may overlap
  *             on the GPU need separate workspaces (two graphs captured with the same one as well).
- * D a multiple of 8, at most 256 (WQ4_ERR_UNSUPPORTED otherwise). Results are identical from run to run for
+ * D a multiple of 8, at most 256; max_tokens * q_heads / kv_heads at most 2^30 (WQ4_ERR_UNSUPPORTED otherwise). Results are identical from run to run for
  * the same lengths. B == 0 or T == 0 is a no-op. */
 int wq4_tree_attention_workspace_bytes(int B, int max_tokens, int q_heads, int kv_heads, int D, size_t* bytes);
 int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_kv_cache* cache, const int* page_table,

@@ -68,7 +68,8 @@ def test_attention_rules(clib):
                 dict(c=cache(kp=16 * 512 + 4))):
         assert call(**bad) == wq4.ERR_ALIGN, bad
     wide = dict(qt=8192, qh=512, ot=8192, oh=512, c=cache(kp=1 << 17, kt=4096, kh=512, vp=1 << 17, vt=4096, vh=512))
-    for bad in (dict(D=63), dict(D=264, **wide), dict(most=(1 << 20) + 1, words=1 << 20), dict(c=cache(page_size=24)),
+    many = dict(Hq=65536, Hk=1, c=cache(kh=64, vh=64))
+    for bad in (dict(most=1 << 15, words=1 << 9, **many), dict(D=63), dict(D=264, **wide), dict(most=(1 << 20) + 1, words=1 << 20), dict(c=cache(page_size=24)),
                 dict(c=cache(page_size=8)), dict(c=cache(kp=1 << 39))):
         assert call(**bad) == wq4.ERR_UNSUPPORTED, bad
 

@@ -348,7 +348,7 @@ def test_pages_and_lengths_that_cannot_be_are_reported(lib, n, Hq):
         table[0, 1] = page
         lib.tree_attention(*args, table, c.starts, c.context, max_tokens=n)
         assert lib.get_last_error() == lib.ERR_INVALID, page
-    for context in ([50, -1], [c.table.shape[1] * 16 - n + 1, 20], [2 ** 31 - 1, 20]):
+    for context in ([50, -1], [c.table.shape[1] * 16 - n + 1, 20], [2 ** 31 - 1, 20], [2 ** 30, 20], [-2 ** 31, 20]):
         lib.tree_attention(*args, c.table, c.starts, torch.tensor(context, dtype=torch.int32, device="cuda"), max_tokens=n)
         assert lib.get_last_error() == lib.ERR_INVALID, context
     for starts in ([0, n, 2 * n + 1], [-1, n, 2 * n], [0, n + 1, 2 * n], [0, 2 * n, n], [2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31 - 1],

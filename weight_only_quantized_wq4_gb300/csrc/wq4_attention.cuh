@@ -38,6 +38,8 @@ struct AttnArgs {
     }
 };
 
+constexpr int kMostPlaces = 1 << 30;    // of a sequence: sums of a place and a tile stay in 32 bits
+
 struct Scan {
     unsigned long long sum[32], part[32], before;
     int longest[32], b;
@@ -64,7 +66,7 @@ struct Walk {
         c = a.context[i];
         n = static_cast<int>(static_cast<unsigned>(s1) - static_cast<unsigned>(s0));
         if (s0 < 0 || s1 < s0 || s1 > a.T || n > a.max_tokens || c < 0 ||
-            (n > 0 && static_cast<long long>(c) + n > static_cast<long long>(a.table_width) * a.cache.page_size)) {
+            (n > 0 && (c > kMostPlaces - n || c + n > static_cast<long long>(a.table_width) * a.cache.page_size))) {
             atomicOr(a.status, kStatusBadIndex);
             n = 0;
         }

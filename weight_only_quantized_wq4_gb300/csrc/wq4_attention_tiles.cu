@@ -38,7 +38,7 @@ struct Cfg {
     static constexpr int kDp = 64 * NC;
     static constexpr int kSlot = kTile * kDp * 2;            // a tile's keys, or values
     static constexpr int kQ = kLanes * kDp * 2;
-    static constexpr int kHead = 3072;                       // barriers, maxima
+    static constexpr int kHead = 3 * 1024;                   // barriers, maxima
     static constexpr int kMaxSmem = 232448;                  // 227 KB
     // Ring slots beside one or two streams' Q.
     __host__ __device__ static constexpr int slots(int q) {

@@ -454,7 +454,8 @@ bool should_tile(const AttnArgs& a) {
 
 int check_heads(int B, int max_tokens, int q_heads, int kv_heads, int D) {
     if (B < 0 || max_tokens < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads || D < 1) return WQ4_ERR_INVALID;
-    if (D % 8 || D > 256 || q_heads > 65536 || max_tokens > (1 << 20)) return WQ4_ERR_UNSUPPORTED;
+    if (D % 8 || D > 256 || q_heads > 65536 || max_tokens > (1 << 20) || static_cast<long long>(max_tokens) * (q_heads / kv_heads) > (1 << 30))
+        return WQ4_ERR_UNSUPPORTED;
     return WQ4_OK;
 }
 
