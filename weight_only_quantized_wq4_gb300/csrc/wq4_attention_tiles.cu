@@ -6,7 +6,7 @@
 // Two streams of S tiles keep the tensor cores and the softmax warps busy in turn. A unit of more than 128 rows gives each stream
 // 128 rows of its own and the same places (each tile of keys and values is read once for 256 rows); a
 // unit of fewer gives both the same rows and every other tile of places, and the streams' O, maxima and sums are joined at
-// the end. A row's maximum is taken over when it has grown by more than 2^8 (any reference will do for the softmax as
+// the end. A row's maximum is taken over when it has grown by more than 2^8, 2^2 in fp16 (any reference will do for the softmax as
 // long as nothing overflows), so that O is rarely scaled.
 //
 // Work is cut as in wq4_tree_attention.cu: equal shares of all the units' tiles, and the CTA that finishes last joins a unit.
@@ -31,7 +31,6 @@ constexpr int kSoftmaxWarp = 4;         // the first of sixteen; before them: co
 constexpr int kSoftmax = 512;           // their threads
 constexpr int kThreads = 32 * kSoftmaxWarp + kSoftmax;
 constexpr int kMaxSlots = 16;
-constexpr float kSlack = 8.f;           // log2 of what a probability may exceed 1 by
 
 template <int NC>
 struct Cfg {
@@ -133,6 +132,8 @@ template <bool BF16, int NC>
 __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __grid_constant__ AttnArgs a) {
     using C = Cfg<NC>;
     constexpr int kDp = C::kDp, kPanel = kTile * 128;
+    constexpr float kSlack = BF16 ? 8.f : 2.f;               // log2 of what a row's maximum may grow by before it is taken over
+    constexpr float kRoom = BF16 ? 0.f : kMostLog2 - kSlack;
     // (nothing else is in shared memory, so that it starts on a swizzle's boundary: checked below)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t s_base = smem_u32(smem_raw);
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                     top = fmaxf(top, other);
                     const bool grows = top > ref + kSlack || (ref == -INFINITY && top > ref);
                     if (__any_sync(0xffffffffu, grows)) {
-                        const float now = grows ? top : ref;
+                        const float now = !grows ? ref : BF16 ? top : ceilf(top);
                         const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - now);
                         ref = now;
                         l *= keep;
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                             }
                         }
                     }
-                    const float minus = ref == -INFINITY ? 0.f : -ref;
+                    const float minus = ref == -INFINITY ? 0.f : kRoom - ref;
                     const uint64_t scale2 = both(a.scale_log2, a.scale_log2), minus2 = both(minus, minus);
                     uint64_t sum2[2] = {0, 0};
 #pragma unroll
@@ -597,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 }
             }
             if (whole) {
-                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(M, L);
+                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(M - kRoom, L);
                 bar_sync(1, kSoftmax);                       // (s_stat, where Q comes, and ctl_i[2] are written again)
                 continue;
             }
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                     }
                     if (live) store16(k, y, sum == 0.f ? 0.f : 1.f / sum);
                 }
-                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(most, sum);
+                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(most - kRoom, sum);
             }
             bar_sync(1, kSoftmax);                           // (ctl_i[1] is written again)
         }
