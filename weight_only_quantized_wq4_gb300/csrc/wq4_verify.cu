@@ -6,11 +6,12 @@
 // w exceeds u z.
 //
 // A cluster of CTAs walks a sequence, each with its share of the vocabulary in shared memory: a row's logits as they lie in
-// memory, which decide on a node's first draft, and, where that is not kept or there is none, the weights as fp32. So a row is
-// read once however many children are tried. Each step ends with one exchange: every CTA tells the others its part of the
-// sum and, if it has it, the weight of the draft that is tried next; all of them then come to the same decision. Which token is drawn hangs on sums over the whole vocabulary next to a random border, so sums
-// are kept as a pair of floats (the rounding of each addition is carried along), 44 bits and more; the weights
-// themselves are rounded as fp32 operations round them, one by one.
+// memory, which decide on a node's first draft unless it is near to its border, and, where it is or is not kept or there
+// is none, the weights as fp32. So a row is read once however many children are tried. Each step ends with one exchange: every CTA
+// tells the others its part of the sum and, if it has it, the weight of the draft that is tried next; all of them then come
+// to the same decision. Decisions hang on sums over the whole vocabulary next to a random border, so sums are kept as a pair of
+// floats (the rounding of each addition is carried along), 44 bits and more; the weights themselves are rounded as fp32
+// operations round them, one by one.
 //
 // Bound by the latency of these steps, one after another: a visited row costs a load, two or three barriers and one exchange across the
 // cluster (about 5000 cycles with the row on its way ahead of time), the end of a walk a pass of exponentials, one over the draft's
@@ -282,9 +283,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
         }
         draft = -1;
     };
-    // Whether the draft is kept, its weight and the weights' sum given. (In fp32: a random number lies as near to the border as these
-    // three roundings reach once in some millions.)
-    auto keeps = [&](float weight, float z) { return __fmul_rn(__fmul_rn(j < kHeld ? sh.uniforms[j] : a.uniforms[s0 + j], draft_q), z) < weight; };
+    auto number = [&] { return j < kHeld ? sh.uniforms[j] : a.uniforms[s0 + j]; };
+    // Whether the draft is kept, its weight and the weights' sum given. (The products are held as pairs too: what each rounds off is
+    // what the fused operation finds.)
+    auto keeps = [&](float weight, const Sum& sum) {
+        const Sum z = sum.normal();
+        const float u = number(), uq = __fmul_rn(u, draft_q), uq_off = __fmaf_rn(u, draft_q, -uq), x = __fmul_rn(uq, z.s);
+        return Sum{weight, 0.f}.exceeds(Sum{x, __fmaf_rn(uq, z.s, -x) + (uq * z.c + uq_off * z.s)});
+    };
     auto scaled = [&](int i) {                       // a logit
         float x;
         if constexpr (DT == WQ4_FP32) x = reinterpret_cast<const float*>(raw)[i];
@@ -447,8 +453,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
             }
             __syncthreads();
         }
-        // ---- their sum, against the CTA's maximum. It decides on the first draft alone, whose random number is as near to the border
-        // as this sum is off (2^-22) once in millions.
+        // ---- their sum, against the CTA's maximum. It decides on the first draft where the draft is not near to its border.
         float s = 0.f;
         if (!greedy && j < n && !isinf(m)) {
             // (differences first: where x and the maximum are near, they are exact)
@@ -483,17 +488,25 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
             fine = false;
             break;
         }
-        // ---- the first draft
+        // ---- the first draft: by approximations, unless it lies as near to its border as they may be off: a hundred and some additions of
+        // 2^-24 each, exponentials to 2^-22 with arguments to 2^-24 of up to 20 (smaller weights do not tell), and of the
+        // logits that x / temperature is rounded to for the weights themselves. Then the weights decide: a sequence's
+        // tokens do not hang on how many threads and CTAs the batch gives it.
+        bool near = false;
         if (j < n) {
-            float draft_w = draft == top_at ? 1.f : 0.f, z = 1.f;
+            float draft_w = draft == top_at ? 1.f : 0.f;
+            bool keep = greedy && keeps(draft_w, Sum{1.f, 0.f});
             if (!greedy) {
                 draft_w = expf(__fsub_rn(draft_x, top));
-                z = lane < C ? told.b * expf(__fsub_rn(told.a, top)) : 0.f;
+                float z = lane < C ? told.b * expf(__fsub_rn(told.a, top)) : 0.f;
 #pragma unroll
                 for (int d = kMaxCluster / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
                 z = __shfl_sync(0xffffffffu, z, 0);
+                const float border = __fmul_rn(__fmul_rn(number(), draft_q), z);
+                near = fabsf(border - draft_w) <= (0x1p-16f + 0x1p-21f * fabsf(top)) * fmaxf(border, draft_w);
+                keep = !near && border < draft_w;
             }
-            if (keeps(draft_w, z)) {
+            if (keep) {
                 if (rank == 0 && tid == 0) path[kept] = j;
                 ++kept;
                 node = j;
@@ -541,8 +554,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
             __syncthreads();
         }
         Sum all = sum_blocks();
-        was = exchange(Part{all.s, all.c, -1.f, 0.f});
+        was = exchange(Part{all.s, all.c, near && here(draft) ? w[draft - v0] : -1.f, 0.f});
         if (j >= n) break;
+        // Whether the draft that is tried is kept by what the CTAs told: the walk goes on from it.
+        auto moves = [&] {
+            float draft_w = -1.f;
+            for (int i = 0; i < C; ++i) draft_w = fmaxf(draft_w, sh.part[was][i].c);
+            if (!keeps(draft_w, sum_of(was))) return false;
+            if (rank == 0 && tid == 0) path[kept] = j;
+            ++kept;
+            node = j;
+            __syncthreads();                         // (the weights are written over)
+            return true;
+        };
+        if (near && moves()) continue;
         // ---- what each draft that is not kept leaves of them
         bool moved = false;
         for (;;) {
@@ -582,17 +607,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
                 weigh(q_row, true, take_off);
                 __syncthreads();
             }
-            float draft_w = -1.f;
-            for (int i = 0; i < C; ++i) draft_w = fmaxf(draft_w, sh.part[was][i].c);
-            const Sum z = sum_of(was);
-            if (keeps(draft_w, __fadd_rn(z.s, z.c))) {
-                if (rank == 0 && tid == 0) path[kept] = j;
-                ++kept;
-                node = j;
-                moved = true;
-                __syncthreads();
-                break;
-            }
+            if ((moved = moves())) break;
         }
         if (!moved) break;
     }
