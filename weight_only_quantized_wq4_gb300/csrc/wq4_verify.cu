@@ -503,7 +503,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kMaxThreads ? 2 : 3) verif
                 for (int d = kMaxCluster / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
                 z = __shfl_sync(0xffffffffu, z, 0);
                 const float border = __fmul_rn(__fmul_rn(number(), draft_q), z);
-                near = fabsf(border - draft_w) <= (0x1p-16f + 0x1p-21f * fabsf(top)) * fmaxf(border, draft_w);
+                // (or there is no sum: 1.44 / temperature may overflow where 1 / temperature does not)
+                near = !(fabsf(border - draft_w) > (0x1p-16f + 0x1p-21f * fabsf(top)) * fmaxf(border, draft_w));
                 keep = !near && border < draft_w;
             }
             if (keep) {
