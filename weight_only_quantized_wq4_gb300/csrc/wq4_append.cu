@@ -160,8 +160,9 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const AppendA
             __syncthreads();
         }
         uint16_t* q_out = a.q_out + (t0 + tok0) * a.qo_ts + head * a.qo_hs;      // (of a query head)
-        for (int tok = tok0; tok < most; tok += beside, left -= beside) {
-            if (tok != tok0 && left > 0) {
+        // (as many rounds for lanes without a head: they take part in the others' exchanges)
+        for (int round = 0, tok = tok0; round < a.steps; ++round, tok += beside, left -= beside) {
+            if (round != 0 && left > 0) {
                 p += step_in;
                 x0 = *reinterpret_cast<const uint4*>(p + c0);
                 x1 = *reinterpret_cast<const uint4*>(p + c1);
