@@ -3,12 +3,13 @@
 //
 // Rotation: the first R features of a head are R / 2 pairs, (i, i + R / 2) or (2 i, 2 i + 1); pair i of a token at
 // position p is turned by the angle p f_i. In turns that is p f_i / 2 pi, of which only the fraction counts, so the
-// frequency is held as F = f_i / 2 pi in units of 2^-64 turns and p F is taken modulo 2^64: what the multiplication
-// drops is whole turns. F is exact to a unit, so the angle is off by p 2^-64 turns, at any position, where p f_i in
-// fp32 would be off by 2^-25 of its value: 0.004 rad at position 131072, half a step of bf16 (2^-8).
+// frequency is held as F = f_i / 2 pi in units of 2^-128 turns and p F is taken modulo 2^128: what the multiplication
+// drops is whole turns. F is exact to a unit (f_i units above 1), so the angle is off by |p| 2^-128 turns, 2^-65 at the farthest
+// position of 64 bits, where p f_i in fp32 would be off by 2^-25 of its value: 0.004 rad at position 131072, half a step of
+// bf16 (2^-8).
 //
 // Each element is read and written once, 16 elements per thread in two 16-byte vectors, chosen so that both halves of each pair
-// are the same thread's. 8192 tokens of 32 + 8 heads of 128, bf16: 44.6 us (4.5 TB/s, 67 % of the copy rate). Issue slots bind it as
+// are the same thread's. 8192 tokens of 32 + 8 heads of 128, bf16: 45.0 us (4.5 TB/s, 66 % of the copy rate). Issue slots bind it as
 // much as memory (62 % busy; some 310 instructions per thread and token): one token per CTA took 56 us, with conflicts in
 // shared memory 59, the next token's loads ahead of the last one's end 48 (registers spill), four CTAs of fewer registers 48. One
 // token takes 2.7 us, a launch and two trips to memory.
@@ -38,26 +39,40 @@ struct AppendArgs {
     unsigned int* status;
 };
 
-// 2^64 / 2 pi
-constexpr unsigned long long kTurn = 0x28be60db9391054aull;
+// 2^128 / 2 pi
+constexpr unsigned long long kTurnHi = 0x28be60db9391054aull, kTurnLo = 0x7f09d5f47d4d3770ull;
 
-// The frequency f (radians per position) in units of 2^-64 turns, modulo a turn: mantissa times kTurn, shifted by the exponent.
-__device__ __forceinline__ unsigned long long turns_of(float f) {
+struct Turns {                          // in units of 2^-128
+    unsigned long long hi, lo;
+};
+
+// The frequency f (radians per position), modulo a turn: mantissa times 2^128 / 2 pi, three words, shifted by the exponent.
+__device__ __forceinline__ Turns turns_of(float f) {
     const uint32_t u = __float_as_uint(f), e = (u >> 23) & 255u;
     const unsigned long long m = (u & 0x7fffffu) | (e ? 0x800000u : 0u);
-    const unsigned long long lo = m * kTurn, hi = __umul64hi(m, kTurn);
-    const int sh = 150 - static_cast<int>(e ? e : 1u);          // f = m 2^-sh
-    unsigned long long F;
-    if (sh >= 128) F = 0;
-    else if (sh >= 64) F = hi >> (sh - 64);
-    else if (sh > 0) F = (lo >> sh) | (hi << (64 - sh));
-    else F = sh > -64 ? lo << -sh : 0;
-    return u >> 31 ? 0ull - F : F;
+    unsigned long long x0 = m * kTurnLo, x1 = m * kTurnHi + __umul64hi(m, kTurnLo);
+    unsigned long long x2 = __umul64hi(m, kTurnHi) + (x1 < __umul64hi(m, kTurnLo));
+    int sh = 150 - static_cast<int>(e ? e : 1u);     // f = m 2^-sh
+    if (sh < 0) {                                    // (a frequency of 2^24 and more: whole words first, as below)
+        if (sh <= -64) x1 = x0, x0 = 0, sh += 64;
+        const int up = -sh;
+        x2 = 0;
+        if (up) x1 = x1 << up | x0 >> (64 - up), x0 <<= up;
+        sh = 0;
+    }
+    if (sh >= 64) x0 = x1, x1 = x2, x2 = 0, sh -= 64;
+    if (sh >= 64) x0 = x1, x1 = 0, sh -= 64;
+    Turns F{x1, x0};
+    if (sh) F.lo = x0 >> sh | x1 << (64 - sh), F.hi = x1 >> sh | x2 << (64 - sh);
+    if (u >> 31) F.lo = 0ull - F.lo, F.hi = ~F.hi + (F.lo == 0);
+    return F;
 }
 
 // cos and sin of p F turns
-__device__ __forceinline__ float2 turned(long long p, unsigned long long F, float f) {
-    const unsigned long long a = static_cast<unsigned long long>(p) * F;
+__device__ __forceinline__ float2 turned(long long p, const Turns& F, float f) {
+    // (the upper half of the product modulo 2^128; a negative p is 2^64 less than what is multiplied)
+    const unsigned long long up = static_cast<unsigned long long>(p);
+    const unsigned long long a = up * F.hi + __umul64hi(up, F.lo) - (p < 0 ? F.lo : 0ull);
     const float half = static_cast<float>(static_cast<int>(a >> 32)) * 0x1p-31f;     // in half turns, [-1, 1]
     float2 cs;
     sincospif(half, &cs.y, &cs.x);
