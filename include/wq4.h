@@ -361,7 +361,8 @@ int wq4_rope_append(const void* Q, long long q_ts, long long q_hs, const void* K
  * max_tokens give outputs that mean nothing, and wq4_get_last_error reports WQ4_ERR_INVALID; nothing
  * is read or written out of bounds.
  *   workspace   wq4_tree_attention_workspace_bytes(...) bytes on the current device, 16-byte aligned, zero-filled once
- *             when allocated; every completed call leaves it fit for the next. Calls that may overlap
+ *             when allocated (its first 4 bytes per SM have to be zero, the rest may hold anything); every completed
+ *             call leaves it fit for the next. Calls that may overlap
  *             on the GPU need separate workspaces (two graphs captured with the same one as well).
  * D a multiple of 8, at most 256; max_tokens * q_heads / kv_heads at most 2^30 (WQ4_ERR_UNSUPPORTED otherwise). Results are identical from run to run for
  * the same lengths. B == 0 or T == 0 is a no-op. */

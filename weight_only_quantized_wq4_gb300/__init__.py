@@ -551,7 +551,9 @@ def tree_attention(q, k_cache, v_cache, page_table, starts, context, max_tokens:
         torch = _torch()
         with torch.cuda.device(q.device):
             nbytes = tree_attention_workspace_bytes(page_table.shape[0], max_tokens, q.shape[-2], k_cache.shape[-2], q.shape[-1])
-        workspace = alloc_workspace(nbytes, q.device)
+        # (only the counters, 4 bytes per SM, have to be zero: clearing it all would write up to 40 MB per call)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace[:4 * torch.cuda.get_device_properties(q.device).multi_processor_count].zero_()
     rc = _binding.tree_attention(q, k_cache, v_cache, page_table, starts, context, max_tokens, mask, scale, out, lse, workspace)
     if rc:
         raise Wq4Error(rc, "wq4_tree_attention")
