@@ -56,6 +56,8 @@ class Decoder:
         self.caches = [[torch.zeros(batch * width, PAGE, self.kv_heads, HEAD, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
                        for _ in range(layers)]
         self.context = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        # for prompts and trees alike: calls on one stream share it, and the largest needs no less than the others
+        self.workspace = wq4.alloc_workspace(wq4.tree_attention_workspace_bytes(batch, places, self.heads, self.kv_heads, HEAD))
 
     def slots(self, sequence, place):
         return self.table[sequence, place // PAGE].long() * PAGE + place % PAGE
@@ -70,7 +72,8 @@ class Decoder:
             rows = wq4.mm(y, layer["qkv"], self.rows).view(len(tokens), -1, HEAD)
             q, k, v = rows.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
             q = wq4.rope_append(q, k, v, k_cache, v_cache, slots, position, self.inv_freq, layer["q_norm"], layer["k_norm"])
-            o = wq4.tree_attention(q, k_cache, v_cache, self.table, starts, self.context, max_tokens=max_tokens, mask=mask)
+            o = wq4.tree_attention(q, k_cache, v_cache, self.table, starts, self.context, max_tokens=max_tokens, mask=mask,
+                                   workspace=self.workspace)
             add = wq4.mm(o.view(len(tokens), -1), layer["out"], self.features)
         wq4.add_rmsnorm_quant(h, self.norm, residual=add, y=y)
         return wq4.mm(y, self.head, self.vocab)

@@ -1,4 +1,7 @@
 """A call without a workspace of the caller's: what is cleared for it, and that what memory holds does not matter."""
+import os
+import sys
+
 import pytest
 import torch
 
@@ -24,3 +27,20 @@ def test_only_the_counters_are_cleared(lib, counts, D, monkeypatch):
         got = c.run(lib)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert sum(t.numel() * t.element_size() for t in cleared) <= 2 * 4096
+
+
+def test_the_example_keeps_one_workspace(lib, monkeypatch):
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    try:
+        import speculative_decode as E
+    finally:
+        sys.path.pop(0)
+    seen, real = [], lib.tree_attention
+    monkeypatch.setattr(lib, "tree_attention", lambda *a, **k: seen.append(k.get("workspace")) or real(*a, **k))
+    g = torch.Generator(device="cuda").manual_seed(0)
+    model = E.Decoder(256, 2, 512, 2, places=80)
+    roots = model.prefill([[1, 2, 3], list(range(40))]).argmax(dim=1)
+    for _ in range(2):
+        roots = model.step(roots, torch.zeros(2, device="cuda"), g)[1]
+    assert lib.get_last_error() == 0
+    assert len(seen) == 6 and all(w is not None and w.data_ptr() == seen[0].data_ptr() for w in seen)
