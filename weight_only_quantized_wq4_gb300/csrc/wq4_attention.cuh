@@ -263,6 +263,7 @@ inline bool encode_cache(EncodeTiledFn fn, CUtensorMap* map, int dtype, void* p,
 // The kernel for many rows per kv head (wq4_attention_tiles.cu): D <= 128, scale above 0.
 int tiles_rows();                       // rows of a unit
 int tiles_places();                     // places of a tile
+bool attention_tiles_fit(const Runtime& rt, int dtype, int D);   // whether it can be launched; ahead of the call below
 int launch_attention_tiles(const Runtime& rt, const AttnArgs& a, int dtype, wq4_stream_t st);
 
 }  // namespace wq4

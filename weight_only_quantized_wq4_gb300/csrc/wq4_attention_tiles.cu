@@ -49,7 +49,8 @@ struct Cfg {
     static constexpr uint32_t kTmemCols = 512;
 };
 
-// Registers: 128 x 64 + 512 x 104 are those of the launch, 640 x 96.
+// Registers: 128 x 64 + 512 x 104 are those of the launch, 640 x 96 (a compiler that gives the kernel fewer: it does not fit).
+constexpr int kFewRegs = 64, kManyRegs = 104;
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     auto two = [&] { return w.rows - w.row0 > kLanes; };
 
     if (warp < kSoftmaxWarp) {
-        fewer_registers<64>();
+        fewer_registers<kFewRegs>();
         if (warp == 0) {
             // ------------------------------------------------------------ copies
             const uint64_t pol = policy_evict_first();
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             }
         }
     } else {
-        more_registers<104>();
+        more_registers<kManyRegs>();
         // ---------------------------------------------------------------- softmax
         // Two threads to a row of S, each with 64 places; they tell each other their maxima.
         const int s = (warp - kSoftmaxWarp) >> 3, half = warp >> 2 & 1, row = (warp & 3) * 32 + lane;
@@ -658,27 +659,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             mbar_wait_plain(s_full + 8 * (i % slots), (i / slots) & 1, drain_limit(a.timeout_cycles));
 }
 
+// Whether the kernel can run: its warps' shares count on the registers of the launch, with fewer they would wait.
 template <bool BF16, int NC>
-int go(const Runtime& rt, const AttnArgs& a, wq4_stream_t st) {
-    using C = Cfg<NC>;
+bool fits(const Runtime& rt) {
     auto kern = attention_tiles_kernel<BF16, NC>;
     static PerDevice ready;
-    const int regs = ready.get(rt.device, [&]() -> int {
+    return ready.get(rt.device, [&]() -> int {       // 1: it can, 2: it cannot
         cudaFuncAttributes fa;
         if (cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kMaxSmem) == cudaSuccess)
-            return fa.numRegs;
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NC>::kMaxSmem) == cudaSuccess)
+            return check::registers_cover(fa.numRegs, kThreads, 32 * kSoftmaxWarp * kFewRegs + kSoftmax * kManyRegs) ? 1 : 2;
         cudaGetLastError();
         return -1;
-    });
-    if (regs != 96) return WQ4_ERR_CUDA;             // the warps' shares count on the registers of the launch; with fewer they would wait
-    return launch(rt, kern, dim3(a.grid), kThreads, C::smem(a.max_rows > kLanes ? 2 : 1), 1, st, a);
+    }) == 1;
+}
+
+template <bool BF16, int NC>
+int go(const Runtime& rt, const AttnArgs& a, wq4_stream_t st) {
+    return launch(rt, attention_tiles_kernel<BF16, NC>, dim3(a.grid), kThreads, Cfg<NC>::smem(a.max_rows > kLanes ? 2 : 1), 1, st, a);
 }
 
 }  // namespace
 
 int tiles_rows() { return kUnitRows; }
 int tiles_places() { return kTile; }
+
+bool attention_tiles_fit(const Runtime& rt, int dtype, int D) {
+    if (dtype == WQ4_BF16) return D <= 64 ? fits<true, 1>(rt) : fits<true, 2>(rt);
+    return D <= 64 ? fits<false, 1>(rt) : fits<false, 2>(rt);
+}
 
 int launch_attention_tiles(const Runtime& rt, const AttnArgs& a, int dtype, wq4_stream_t st) {
     if (dtype == WQ4_BF16) return a.D <= 64 ? go<true, 1>(rt, a, st) : go<true, 2>(rt, a, st);

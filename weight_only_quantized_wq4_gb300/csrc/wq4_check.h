@@ -76,6 +76,9 @@ WQ4_HD inline bool block_copy_ok(long long b, long long blocks, long long row, l
     return b >= 0 && b < blocks && row >= 0 && row < rows;
 }
 
+// Whether a launch of `threads` threads, `regs` registers each (given out in eights), has as many as its warps share out anew.
+WQ4_HD inline bool registers_cover(int regs, int threads, int wanted) { return (regs + 7) / 8 * 8 * threads >= wanted; }
+
 }  // namespace check
 
 #if defined(__CUDACC__)

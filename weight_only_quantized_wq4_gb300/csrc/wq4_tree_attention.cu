@@ -520,7 +520,8 @@ int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_
     a.scale_log2 = scale * 1.4426950408889634f;
     a.test_stall = rt.test_stall;
     // (the tiles' softmax takes maxima ahead of the scale; the other kernel, whose parts are smaller, after it)
-    const bool can = can_tile(max_tokens, q_heads / kv_heads, D), tiles = can && scale > 1e-30f && should_tile(a);
+    const bool can = can_tile(max_tokens, q_heads / kv_heads, D);
+    const bool tiles = can && scale > 1e-30f && should_tile(a) && attention_tiles_fit(rt, dtype, D);
     if (!workspace || workspace_bytes < space_of(a.grid, D, can ? tiles_rows() : kRows).bytes) return WQ4_ERR_WORKSPACE;
     const Space sp = space_of(a.grid, D, tiles ? tiles_rows() : kRows);
     a.counters = static_cast<int*>(workspace);
