@@ -408,7 +408,8 @@ int wq4_verify_drafts(const void* logits, long long ld, const long long* tokens,
  * recorded in the device status word: a failed bounds check of the debug build (WQ4_ERR_BOUNDS),
  * else a blob header that did not match its call or an index in device memory outside what it
  * indexes (WQ4_ERR_INVALID), else a pipeline timeout
- * (WQ4_ERR_TIMEOUT); with nothing recorded, a pending CUDA error (WQ4_ERR_CUDA), else WQ4_OK. A
+ * (WQ4_ERR_TIMEOUT), else a kernel whose shared memory did not lie as it needs (WQ4_ERR_CUDA: its outputs are
+ * undefined); with nothing recorded, a pending CUDA error (WQ4_ERR_CUDA), else WQ4_OK. A
  * call whose waits ran out stops early and leaves its outputs undefined; the context stays
  * usable, but a workspace it used must be zero-filled again before the next call (its split
  * counters may be left non-zero). The status word is shared by every stream on the device and is

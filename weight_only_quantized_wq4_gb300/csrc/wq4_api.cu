@@ -1313,9 +1313,8 @@ int wq4_get_last_error(wq4_stream_t stream) {
             std::lock_guard<std::mutex> lk(g_mu);
             g_violation[0] = 1;
             for (int i = 0; i < check::kRecordWords; ++i) g_violation[1 + i] = static_cast<int>(w[1 + i]);
-            return WQ4_ERR_BOUNDS;
         }
-        return (st & (kStatusBadBlob | kStatusBadIndex)) ? WQ4_ERR_INVALID : WQ4_ERR_TIMEOUT;
+        return status_error(st);
     }
     if (se != cudaSuccess || cudaGetLastError() != cudaSuccess) return WQ4_ERR_CUDA;
     return WQ4_OK;

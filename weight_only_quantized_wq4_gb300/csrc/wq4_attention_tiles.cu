@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     Walk w(a, kTile, kUnitRows, kLeast);
     bool work = w.begin(scan, tid, kThreads);                // (all threads of the CTA alike)
     if (s_base & 1023u) {
-        if (tid == 0) atomicOr(a.status, kStatusTimeout);
+        if (tid == 0) atomicOr(a.status, kStatusPlacement);
         work = false;
     }
     __syncthreads();                                         // (Q comes where the schedule's sums were)

@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda.h>
 
+#include "wq4.h"
+
 namespace wq4 {
 
 constexpr int kTileN = 128;          // weight rows per tile (the MMA's M side after the transpose)
@@ -14,8 +16,18 @@ constexpr uint32_t kBlobMagic = 0x50345157u;   // "WQ4P"
 constexpr uint32_t kBlobVersion = 2;
 
 // Bits of the device status word: a bounded pipeline wait ran out; a blob header did not match
-// the call's arguments; a bounds check of the debug build failed; a slot, page or length in device memory lay outside its cache.
-enum : uint32_t { kStatusTimeout = 1u, kStatusBadBlob = 2u, kStatusBounds = 4u, kStatusBadIndex = 8u };
+// the call's arguments; a bounds check of the debug build failed; a slot, page or length in device memory lay outside its cache; a
+// kernel's shared memory does not begin on the boundary that its copies need.
+enum : uint32_t { kStatusTimeout = 1u, kStatusBadBlob = 2u, kStatusBounds = 4u, kStatusBadIndex = 8u, kStatusPlacement = 16u };
+
+// What wq4_get_last_error says of them, the gravest first.
+inline int status_error(uint32_t status) {
+    return status & kStatusBounds                        ? WQ4_ERR_BOUNDS
+           : status & (kStatusBadBlob | kStatusBadIndex) ? WQ4_ERR_INVALID
+           : status & kStatusTimeout                     ? WQ4_ERR_TIMEOUT
+           : status                                      ? WQ4_ERR_CUDA
+                                                         : WQ4_OK;
+}
 
 // Weight formats (the blob header's qtype code): uint4b8 (value = (q - 8) s), uint4 with a 4-bit
 // zero point per (group, row) (value = (q - z) s), uint4 with a float zero per (group, row), added
