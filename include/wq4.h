@@ -356,7 +356,7 @@ int wq4_rope_append(const void* Q, long long q_ts, long long q_hs, const void* K
  * A token that sees nothing gets zeros and an lse of -inf. What lies in places that a token does not see, NaN and
  * infinities among it, does not reach its output. Rows of out and lse past starts[B] are left as they are.
  * Probabilities are rounded to dtype before they multiply the values (their sum is not); all sums are fp32.
- * (WQ4_FP16: those below 2^-26 of a row's largest to steps of 2^-36 of it.)
+ * (WQ4_FP16: those below 2^-27 of a row's largest to steps of 2^-37 of it.)
  * A page outside the cache, a table too narrow for a sequence, or starts that do not ascend within T and by at most
  * max_tokens give outputs that mean nothing, and wq4_get_last_error reports WQ4_ERR_INVALID; nothing
  * is read or written out of bounds.

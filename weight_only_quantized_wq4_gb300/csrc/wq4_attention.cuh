@@ -40,10 +40,11 @@ struct AttnArgs {
 
 // Probabilities are rounded to the values' type, as the tensor cores' products read both operands in one type (an fp32 P would
 // take two products each; its half step is what the result's own rounding has too). Their sum is taken ahead of that, in fp32. fp16
-// has 2^-14 as its least normal number, and a long context may put much of a row's weight on places below that: P is
-// 2^(s - reference) 2^room with 2^15 as the most it may reach, and sum and O carry the same factor. The reference is a
-// whole number, so that reference - room is one too. What lies 2^-26 and more below the row's largest loses bits, 2^-37 below it
-// vanishes. bf16 has fp32's range and needs no room.
+// has 2^-14 as its least normal number, and a long context may put much of a row's weight on places below that: the
+// softmax's reference lies so far below the row's maximum that P reaches 2^15 at most, 2^13 at least, and sum and O carry the
+// same factor. (P of the maximum itself is a power of two, as it is without: where one place has nearly all of the weight, its
+// rounding is nearly all of the error.) What lies 2^-27 and more below the row's largest loses bits, 2^-38 below it vanishes.
+// bf16 has fp32's range and needs no room.
 constexpr float kMostLog2 = 15.f;
 
 constexpr int kMostPlaces = 1 << 30;    // of a sequence: sums of a place and a tile stay in 32 bits

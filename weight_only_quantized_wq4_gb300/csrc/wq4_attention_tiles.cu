@@ -464,10 +464,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                     bar_sync(2 + s * 4 + (warp & 3), 64);
                     float other;
                     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(max_at ^ (4 * kLanes)) : "memory");
-                    top = fmaxf(top, other);
+                    top = fmaxf(top, other) - kRoom;
                     const bool grows = top > ref + kSlack || (ref == -INFINITY && top > ref);
                     if (__any_sync(0xffffffffu, grows)) {
-                        const float now = !grows ? ref : BF16 ? top : ceilf(top);
+                        const float now = grows ? top : ref;
                         const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - now);
                         ref = now;
                         l *= keep;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                             }
                         }
                     }
-                    const float minus = ref == -INFINITY ? 0.f : kRoom - ref;
+                    const float minus = ref == -INFINITY ? 0.f : -ref;
                     const uint64_t scale2 = both(a.scale_log2, a.scale_log2), minus2 = both(minus, minus);
                     uint64_t sum2[2] = {0, 0};
 #pragma unroll
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 }
             }
             if (whole) {
-                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(M - kRoom, L);
+                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(M, L);
                 bar_sync(1, kSoftmax);                       // (s_stat, where Q comes, and ctl_i[2] are written again)
                 continue;
             }
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                     }
                     if (live) store16(k, y, sum == 0.f ? 0.f : 1.f / sum);
                 }
-                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(most - kRoom, sum);
+                if (live && a.lse && tells) a.lse[static_cast<long long>(u->first + token) * a.Hq + head] = lse_of(most, sum);
             }
             bar_sync(1, kSoftmax);                           // (ctl_i[1] is written again)
         }

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     float top = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float now = fmaxf(m[e], BF16 ? top : ceilf(top)), ref = now == -INFINITY ? 0.f : now;
+                    const float now = fmaxf(m[e], top - kRoom), ref = now == -INFINITY ? 0.f : now;
                     const float keep = exp2_approx(m[e] - ref);
                     m[e] = now;
                     l[e] *= keep;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     }
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        const float x = exp2_approx(s[n][2 * e] - (ref - kRoom)), y = exp2_approx(s[n][2 * e + 1] - (ref - kRoom));
+                        const float x = exp2_approx(s[n][2 * e] - ref), y = exp2_approx(s[n][2 * e + 1] - ref);
                         l[e] += x + y;
                         p[e + 2 * n] = pack2<BF16>(x, y);
                     }
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         const int d = n * 8 + quad * 2;
                         if (d < a.D) *reinterpret_cast<uint32_t*>(p + d) = pack2<BF16>(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
                     }
-                    if (a.lse && quad == 0) a.lse[static_cast<long long>(first + token[e]) * a.Hq + head] = lse_of(M[e] - kRoom, L[e]);
+                    if (a.lse && quad == 0) a.lse[static_cast<long long>(first + token[e]) * a.Hq + head] = lse_of(M[e], L[e]);
                 }
             }
             continue;
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     if (d < a.D) *reinterpret_cast<uint32_t*>(p + d) = pack2<BF16>(x * inv, y * inv);
                 }
                 if (a.lse && warp == 0 && quad == 0)
-                    a.lse[static_cast<long long>(first + token[e]) * a.Hq + head] = lse_of(top[e] - kRoom, sum[e]);
+                    a.lse[static_cast<long long>(first + token[e]) * a.Hq + head] = lse_of(top[e], sum[e]);
             }
         }
         bar_sync(1, 32 * kWarps);                    // (shared_i[1] is written again)
