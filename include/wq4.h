@@ -346,7 +346,8 @@ int wq4_rope_append(const void* Q, long long q_ts, long long q_hs, const void* K
  *   cache     this step's keys and values are in it (wq4_rope_append). k and v 16-byte aligned, strides multiples
  *             of 8; page_size a multiple of 16.
  *   page_table   [B][table_width] int, row stride ld_table: page i of sequence b holds its places from i page_size.
- *             Entries past a sequence's last place are not read. A sequence has at most 2^30 places.
+ *             Entries past a sequence's last place are not read. A sequence has at most 2^30 places. A table no wider
+ *             than the longest sequence needs is soonest: its width is all that the choice of kernel knows of the lengths.
  *   starts    [B + 1] int, in DEVICE memory as page_table and context [B] int; 0 <= starts[b] <= starts[b + 1] <= T.
  *   max_tokens   the most tokens that one sequence has in this step.
  *   mask      [T][mask_words] 64-bit words: token i of a sequence sees token j of the same where bit j % 64 of
@@ -380,7 +381,7 @@ int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_
  * walk is at, j is tried: it is kept if uniforms[j] q(token_j) < p(token_j), and the walk goes on from j
  * with the p of its row; otherwise what the draft accounts for is taken from the target,
  * p = max(p - q, 0) / its sum (p stays where nothing is left). q is the node's row of draft_probs, the distribution that
- * its children were drawn from; without draft_probs a draft is certain: q = 1 at the token tried, 0 elsewhere. At the
+ * each of its children was drawn from, independently and with replacement; without draft_probs a draft is certain: q = 1 at the token tried, 0 elsewhere. At the
  * end the next token is drawn from p: the first one at which the sum of p exceeds final_uniforms[b].
  *   logits    [T][V] dtype (WQ4_BF16, WQ4_FP16 or WQ4_FP32), row stride ld. -inf: a token that cannot occur.
  *   tokens    [T]; parents [T] int, the parent's place within the sequence (the first token's is not read); starts
@@ -393,8 +394,9 @@ int wq4_tree_attention(const void* Q, long long q_ts, long long q_hs, const wq4_
  *             within the sequence in order, then -1; next_tokens [B].
  * The walk ends with next token -1 at a row that holds a NaN or +inf, or nothing but -inf, for a temperature that is
  * negative, NaN, infinite or so small that the scaled logits overflow, and for a sequence without tokens.
- * Probabilities are fp32, sums over the vocabulary hold 44 bits and more. Results are identical from run to run. starts that do not ascend within
- * T and by at most max_tokens: as in wq4_tree_attention. V <= 400000. B == 0 is a no-op. */
+ * Probabilities are fp32, decisions are by sums over the vocabulary that are off by less than 2^-37 of them. Results are identical
+ * from run to run; the sums' order hangs on B, V and the device, so that a sequence may go another way in another batch where a
+ * random number lies as near to a border as that. starts that do not ascend within T and by at most max_tokens: as in wq4_tree_attention. V <= 400000. B == 0 is a no-op. */
 int wq4_verify_drafts(const void* logits, long long ld, const long long* tokens, const int* parents, const int* starts,
                       int B, int T, int max_tokens, int V, int dtype, const float* draft_probs, long long ldp,
                       const float* temperature, const float* uniforms, const float* final_uniforms, int* accepted,

@@ -567,7 +567,7 @@ def verify_drafts(logits, tokens, parents, starts, uniforms, final_uniforms, max
     logits: bf16, fp16 or fp32 [T][V], row t answering token t; tokens int64 [T]; parents int32 [T], places within the
     sequence; starts int32 [B + 1]; the first token of each sequence is certain, the others are drafts. uniforms fp32
     [T] and final_uniforms fp32 [B]: random numbers of [0, 1). draft_probs fp32 [T][V]: row t is what t's children were
-    drawn from; None: drafts are certain. temperature fp32 [B], 0 for greedy. Returns (accepted int32 [B], path int32
+    drawn from, independently and with replacement; None: drafts are certain. temperature fp32 [B], 0 for greedy. Returns (accepted int32 [B], path int32
     [B][max(1, max_tokens - 1)]: the kept drafts' places, then -1; next_tokens int64 [B]); allocated if not given."""
     if _bound is not _lib or _lib is None:
         _bind()

@@ -13,7 +13,7 @@
 //
 // 16 trees of 32 tokens over 1000 to 8000 places, 32 heads over 8 of 128: 79 us (3.9 TB/s; memory's floor 45): a tile of 64 KB takes 2950
 // cycles where memory would take 2800, and about 25 us go by before the first tile, at the joins and at the end. One
-// tree of 64 tokens, 64 heads over 8, over 131000 places: 272 us (1.01 PFLOP/s, 52 % of the MMAs' rate): per stream, the
+// tree of 64 tokens, 64 heads over 8, over 131000 places: 275 us (1.00 PFLOP/s, 51 % of the MMAs' rate): per stream, the
 // softmax (some 1350 cycles from S to P, 700 of them exponentials) is longer than the other stream's MMAs (1040). One thread per row
 // took 298 us; a thread that issues the MMAs of each stream, in place of one for both, 304; descriptors built for each MMA 300.
 #include <new>

@@ -10,12 +10,12 @@
 // is none, the weights as fp32. So a row is read once however many children are tried. Each step ends with one exchange: every CTA
 // tells the others its part of the sum and, if it has it, the weight of the draft that is tried next; all of them then come
 // to the same decision. Decisions hang on sums over the whole vocabulary next to a random border, so sums are kept as a pair of
-// floats (the rounding of each addition is carried along), 44 bits and more; the weights themselves are rounded as fp32
-// operations round them, one by one.
+// floats (the rounding of each addition is carried along; some fifty of them leave 2^-37 of a sum at worst); the weights
+// themselves are rounded as fp32 operations round them, one by one.
 //
 // Bound by the latency of these steps, one after another: a visited row costs a load, two or three barriers and one exchange across the
 // cluster (about 5000 cycles with the row on its way ahead of time), the end of a walk a pass of exponentials, one over the draft's
-// row and a search (some 20000). One chain of 5 over 32001 tokens, fp32: 17.0 us; 32 trees of 16 over 131072, bf16: 31; 192
+// row and a search (some 20000). One chain of 5 over 32001 tokens, fp32: 17.3 us; 32 trees of 16 over 131072, bf16: 32; 192
 // chains of 6: 108, 1.9 TB/s of the rows that are visited. Sums in 64-bit arithmetic took five times as long (650 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
