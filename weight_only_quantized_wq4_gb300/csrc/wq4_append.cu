@@ -10,7 +10,7 @@
 //
 // Each element is read and written once, 16 elements per thread in two 16-byte vectors, chosen so that both halves of each pair
 // are the same thread's. 8192 tokens of 32 + 8 heads of 128, bf16: 45.5 us (4.4 TB/s, 65 % of the copy rate). Too few bytes are under way
-// beside some 310 instructions per thread and token (issue slots 62 % busy, 47 % of the warps an SM could hold): one token per CTA
+// beside some 320 instructions per thread and token (issue slots 63 % busy, 47 % of the warps an SM could hold): one token per CTA
 // took 56 us, with conflicts in shared memory 59, the next token's loads ahead of the last one's end 48 (registers spill), four
 // CTAs of fewer registers 48. One token takes 2.8 us, a launch and two trips to memory.
 #include <cuda_bf16.h>
